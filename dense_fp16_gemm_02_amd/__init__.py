@@ -11,6 +11,10 @@ not built, importing the functions below raises.
     tg_device_info() -> (status, compute_units, max_clock_khz, arch)
     gemm(A, B, out=None, stream=None) -> D   (torch wrapper; fp16 or bf16)
 
+and, from ``projection.py``, the operators around a trained projection: the
+softmax cross entropy of H·Wᵀ with its gradients (``linear_cross_entropy``) and
+the Newton–Schulz update (``newton_schulz``), with their C entry points.
+
 Pointers may be given as torch tensors (their ``data_ptr()``) or integers;
 ``stream`` may be a ``torch.cuda.Stream``, an integer hipStream_t or None
 (the null stream).
@@ -20,6 +24,13 @@ from __future__ import annotations
 import ctypes
 import os
 
+from .projection import (TG_NS_MAX_STEPS, TG_XENT_MEAN, TG_XENT_NONE, TG_XENT_SUM, linear_cross_entropy,
+                         newton_schulz, tg_newton_schulz_bf16, tg_newton_schulz_f16, tg_newton_schulz_f32,
+                         tg_newton_schulz_plan, tg_newton_schulz_workspace_bytes, tg_xent_bf16, tg_xent_bwd_bf16,
+                         tg_xent_bwd_f16, tg_xent_bwd_workspace_bytes, tg_xent_f16, tg_xent_plan,
+                         tg_xent_workspace_bytes)
+from .projection import declare as _declare_projection
+
 __all__ = ["TG_OK", "TG_ERR_INVALID_ARG", "TG_ERR_LAUNCH", "TG_ERR_DEVICE", "TG_ERR_TOO_LARGE",
            "TG_ERR_LAYOUT", "TG_MFMA_F16_16X16X32", "TG_MFMA_F16_32X32X16", "TG_MFMA_BF16_16X16X32",
            "TG_MFMA_MXF8_32X32X64", "tg_gemm_mxf8", "tg_gemm_mxf8_plan", "tg_gemm_mxf8_packed",
@@ -28,7 +39,11 @@ __all__ = ["TG_OK", "TG_ERR_INVALID_ARG", "TG_ERR_LAUNCH", "TG_ERR_DEVICE", "TG_
            "tg_gemm_mx_packed_plan",
            "TgError", "lib_path", "load", "tg_gemm_f16", "tg_gemm_f16_plan", "tg_gemm_bf16",
            "tg_gemm_bf16_plan", "tg_status_string", "tg_device_info", "tg_mfma_ceiling", "tg_hbm_read_ceiling",
-           "tg_gemm_f16_xcd_stamps", "gemm"]
+           "tg_gemm_f16_xcd_stamps", "gemm",
+           "TG_XENT_NONE", "TG_XENT_SUM", "TG_XENT_MEAN", "TG_NS_MAX_STEPS", "tg_xent_f16", "tg_xent_bf16",
+           "tg_xent_bwd_f16", "tg_xent_bwd_bf16", "tg_xent_workspace_bytes", "tg_xent_bwd_workspace_bytes",
+           "tg_xent_plan", "tg_newton_schulz_f32", "tg_newton_schulz_f16", "tg_newton_schulz_bf16",
+           "tg_newton_schulz_workspace_bytes", "tg_newton_schulz_plan", "linear_cross_entropy", "newton_schulz"]
 
 TG_MX_E4M3 = 0  # block-scaled element encodings (include/tg_gemm.h)
 TG_MX_E5M2 = 1
@@ -113,6 +128,7 @@ def load():
     lib.tg_device_info.restype = ctypes.c_int
     lib.tg_device_info.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
                                    ctypes.c_char_p, i64]
+    _declare_projection(lib)
     _lib = lib
     return lib
 

@@ -17,6 +17,7 @@ LIB = os.path.join(PKG, "libtg_gemm.so")
 ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "tg_gemm.hip"), os.path.join(CSRC, "tg_ceiling.hip"),
+           os.path.join(CSRC, "tg_xent.hip"), os.path.join(CSRC, "tg_ortho.hip"),
            os.path.join(CSRC, "tile_layout_abi.cpp")]
 
 FLAGS = [

@@ -1,0 +1,549 @@
+// tg_ortho.hip — Newton–Schulz orthogonalisation of a projection's update.  See
+// include/tg_ortho.h for the contract.
+//
+// With s the shorter and l the longer side, a step is three products:
+//
+//   gram     A = X·Xᵀ (tall: Xᵀ·X)   s×s over l   symmetric
+//   square   B = b·A + c·A²          s×s over s   symmetric
+//   update   X ← a·X + B·X (X·B)     s×l over s
+//
+// The symmetric products compute the tiles of the lower triangle and store
+// each twice, as it is and transposed: s·(s+1)·l instead of 2·s²·l flop.
+// X is never transposed: its row-major image is the K-major operand of X·Xᵀ
+// and X·B and the transposed one of Xᵀ·X and B·X.
+//
+// Numbers.  An early step multiplies small singular values by a ≈ 3.4, so an
+// error made in X then is amplified by up to 3.4⁵ ≈ 485 where the value it
+// perturbs is small beside the norm; X is therefore carried in fp32, and only
+// the products' operands are rounded.  Near convergence B ≈ −2.4·I plus a small
+// remainder; rounding B as a whole would put an error of 2.4·2⁻¹² on every
+// row, so the diagonals of A and B are kept in fp32 (d, e) and the products
+// run on the off-diagonal parts O and P alone:
+//
+//   A² = d_i² or (d_i + d_j)·O_ij, plus O·O        B = diag(e) + P
+//   X ← (a + e_i)·X + P·X
+//
+// Measured against 64 bits on Gaussian, low-rank-plus-noise and 1/k spectra:
+// 1.66e-3 to 1.85e-3 (relative, 2-norm) for the bfloat16 result, 1.66e-3 being
+// the rounding of the result itself; with B rounded whole 2.1e-3 to 2.7e-3,
+// with X carried in 16 bits up to 4.4e-3, with bfloat16 operands 1e-2 to 3e-2.
+//
+// Operands are binary16 times 2^14 (X) and 2^12 (O, P): entries of X start near
+// (rows·cols)^-1/2 and of O near 1/s·l^-1/2, far below binary16's 2^-14, and the
+// scales keep 11 bits down to 2^-28 and 2^-26.
+#include "proj_tile.hpp"
+
+#include <algorithm>
+#include <math.h>
+#include <stdio.h>
+
+#include "tg_gemm.h"
+#include "tg_ortho.h"
+
+namespace {
+using namespace pt;
+
+typedef _Float16 half_t;
+typedef half_t half4 __attribute__((ext_vector_type(4)));
+
+constexpr float X_SCALE = 16384.0f, S_SCALE = 4096.0f;  // of X, and of O and P
+
+// ------------------------------------------------------------- norm, scaling
+constexpr int NORM_BLOCKS = 128;  // most partial sums per matrix
+// Sums of squares in 64 bits: fp32 squares would overflow or vanish for
+// elements beyond 1e19 or below 1e-23.  Reads G once.
+template <typename G>
+__global__ __launch_bounds__(256) void ns_norm_kernel(const G *g, int64_t rows, int64_t cols, int64_t ld,
+                                                      int64_t stride, int blocks, double *part)
+{
+    __shared__ double sh[4];
+    const int m = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    const G *p = g + (int64_t)m * stride;
+    double s = 0.0;
+    const int64_t total = rows * cols;
+    if (ld == cols) {
+        for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
+            const double x = (double)(float)p[i];
+            s += x * x;
+        }
+    } else {
+        for (int64_t r = blk; r < rows; r += blocks)
+            for (int64_t c = threadIdx.x; c < cols; c += 256) {
+                const double x = (double)(float)p[r * ld + c];
+                s += x * x;
+            }
+    }
+    for (int o = 32; o; o >>= 1)
+        s += __shfl_xor(s, o);
+    if ((threadIdx.x & 63) == 0)
+        sh[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = ((sh[0] + sh[1]) + sh[2]) + sh[3];
+}
+
+// X0 = G / (norm + eps) in fp32, and its binary16 image padded with zeros to
+// ldx columns.  With `out` (no steps) the result itself.
+template <typename G>
+__global__ __launch_bounds__(256) void ns_scale_kernel(const G *g, int64_t rows, int64_t cols, int64_t ld,
+                                                       int64_t stride, int norm_blocks, const double *part, float eps,
+                                                       int blocks, float *x, half_t *xh, int64_t ldx, __bf16 *out,
+                                                       int64_t ldo, int64_t o_stride)
+{
+    const int m = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    double s = 0.0;
+    for (int i = threadIdx.x & 63; i < norm_blocks; i += 64)
+        s += part[m * norm_blocks + i];
+    for (int o = 32; o; o >>= 1)
+        s += __shfl_xor(s, o);
+    const double by = sqrt(s) + (double)eps;
+    // a zero matrix without eps stays zero
+    const double inv = by > 0.0 || by != by ? 1.0 / by : 0.0;
+    const G *p = g + (int64_t)m * stride;
+    const int64_t per = ldx / 4, total = rows * per;
+    for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
+        const int64_t r = i / per, c = (i - r * per) * 4;
+        f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < cols)
+                v[e] = (float)((double)(float)p[r * ld + c + e] * inv);
+        if (out) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols)
+                    out[(int64_t)m * o_stride + r * ldo + c + e] = (__bf16)v[e];
+            continue;
+        }
+        half4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            h[e] = (half_t)(v[e] * X_SCALE);
+        const int64_t at = ((int64_t)m * rows + r) * ldx + c;
+        *reinterpret_cast<f32x4 *>(x + at) = v;
+        *reinterpret_cast<half4 *>(xh + at) = h;
+    }
+}
+
+// -------------------------------------------------------- symmetric products
+// One workgroup per BM×BM tile of a lower triangle.  gram: SQUARE false, the
+// product of X with itself; square: the product of O with itself, joined with
+// O's own tile and the diagonal.
+struct SymArgs {
+    Operand x;           // one operand on both sides
+    int64_t x_stride;    // elements between matrices
+    int K, s;
+    half_t *out;         // s × lds, zero columns from s on
+    int64_t lds;
+    float *diag;         // lds per matrix, s of them set
+    const half_t *o;     // square: A's off-diagonal part and diagonal
+    const float *d;
+    float b, c;
+    int tri, total;      // tiles per matrix, in all
+};
+template <typename T, bool SQUARE>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void ns_sym_kernel(
+    SymArgs a)
+{
+    static_assert(T::BM == T::BN && T::WTM == T::WTN, "symmetric tiles");
+    __shared__ __attribute__((aligned(1024))) half_t smem[T::LDS_ELEMS];
+    const int logical = xcd_contiguous(blockIdx.x, a.total);
+    const int m = logical / a.tri;
+    int tm, tn;
+    triangle_tile(logical - m * a.tri, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm), tn = __builtin_amdgcn_readfirstlane(tn);
+    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    Operand x = a.x;
+    x.p = reinterpret_cast<const half_t *>(x.p) + (int64_t)m * a.x_stride;
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    T::run(smem, x, x, m0, n0, a.K, acc);
+
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int fr = lane & 15, fc = 4 * (lane >> 4);
+    const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
+    half_t *out = a.out + (int64_t)m * a.s * a.lds;
+    float *diag = a.diag + (int64_t)m * a.lds;
+    const half_t *o = SQUARE ? a.o + (int64_t)m * a.s * a.lds : nullptr;
+    const float *d = SQUARE ? a.d + (int64_t)m * a.lds : nullptr;
+    barrier_lds();
+    half_t *stg = smem + wave * T::WTM * T::WTN;
+    // columns outside, rows inside: one set of column masks is live at a time
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) {
+        const int col = c0 + 16 * j + fc;
+        f32x4 dc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (SQUARE && col < a.s)
+            dc = *reinterpret_cast<const f32x4 *>(d + col);
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) {
+            const int row = r0 + 16 * i + fr;
+            const bool in = row < a.s;
+            const float dr = SQUARE && in ? d[row] : 0.0f;
+            half4 oh = half4{0, 0, 0, 0}, h;
+            if (SQUARE && in && col < a.s)
+                oh = *reinterpret_cast<const half4 *>(o + (int64_t)row * a.lds + col);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const bool valid = in && col + v < a.s;
+                float y;
+                if constexpr (SQUARE) {
+                    const float f = (float)oh[v];
+                    y = a.b * f + a.c * ((dr + dc[v]) * f + acc[i][j][v] * (1.0f / S_SCALE));
+                    if (valid && row == col + v) {
+                        diag[row] = a.b * dr + a.c * (dr * dr + acc[i][j][v] * (1.0f / (S_SCALE * S_SCALE)));
+                        y = 0.0f;
+                    }
+                } else {
+                    y = acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE));
+                    if (valid && row == col + v) {
+                        diag[row] = acc[i][j][v] * (1.0f / (X_SCALE * X_SCALE));
+                        y = 0.0f;
+                    }
+                }
+                // the rounding of the next product's operand
+                h[v] = valid ? (half_t)y : (half_t)0.0f;
+            }
+            *reinterpret_cast<half4 *>(stg + stage_off<T::WTN>(16 * i + fr, 16 * j + fc)) = h;
+        }
+    }
+    store_block<half_t, T::WTM, T::WTN>(stg, out, a.lds, r0, c0, a.s, (int)a.lds, true, nullptr, lane);
+    if (tm == tn)
+        return;
+    // the mirror image: the staged block, read by columns
+#pragma unroll 1
+    for (int p = 0; p < T::WTN * T::WTM / 8 / 64; ++p) {
+        const int idx = p * 64 + lane;
+        const int r = idx / (T::WTM / 8), c = (idx % (T::WTM / 8)) * 8;  // row of the image, first of 8 columns
+        typename El<half_t>::v8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = stg[stage_off<T::WTN>(c + e, r)];
+        if (c0 + r < a.s && r0 + c < a.lds)
+            *reinterpret_cast<typename El<half_t>::v8 *>(out + (int64_t)(c0 + r) * a.lds + r0 + c) = v;
+    }
+}
+
+// ------------------------------------------------------------------- update
+// X ← (a + e)·X + P·X, or with the factors on the right for a tall X.  Reads
+// and writes X in fp32 in place (each element by the one lane that owns it)
+// and writes the next operand; the last step writes the bfloat16 result.
+struct UpdateArgs {
+    Operand l, r;           // left and right operand
+    int64_t l_stride, r_stride;
+    int K, rows, cols;
+    float *x;
+    half_t *xh;
+    int64_t ldx;
+    const float *e;
+    int64_t lds;
+    float a;
+    __bf16 *out;
+    int64_t ldo, o_stride;
+    bool vec;
+    int tiles_m, tiles_n, total;
+};
+template <typename T, bool TALL, bool LAST>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void ns_update_kernel(
+    UpdateArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) half_t smem[T::LDS_ELEMS];
+    const int tiles = a.tiles_m * a.tiles_n;
+    const int logical = xcd_contiguous(blockIdx.x, a.total);
+    const int m = logical / tiles;
+    int tm, tn;
+    grouped_tile<4>(logical - m * tiles, a.tiles_m, a.tiles_n, tm, tn);
+    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    Operand l = a.l, r = a.r;
+    l.p = reinterpret_cast<const half_t *>(l.p) + (int64_t)m * a.l_stride;
+    r.p = reinterpret_cast<const half_t *>(r.p) + (int64_t)m * a.r_stride;
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    T::run(smem, l, r, m0, n0, a.K, acc);
+
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int fr = lane & 15, fc = 4 * (lane >> 4);
+    const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
+    const float *e = a.e + (int64_t)m * a.lds;
+    float *x = a.x + ((int64_t)m * a.rows + r0 + fr) * a.ldx;
+    barrier_lds();
+    half_t *stg = smem + wave * T::WTM * T::WTN;
+    // columns outside, rows inside: one set of column masks is live at a time
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) {
+        const int col = c0 + 16 * j + fc;
+        f32x4 ec = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (TALL && col < a.cols)
+            ec = *reinterpret_cast<const f32x4 *>(e + col);
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) {
+            const int row = r0 + 16 * i + fr;
+            const bool have = row < a.rows && col < a.ldx;
+            const float er = !TALL && row < a.rows ? e[row] : 0.0f;
+            f32x4 *px = reinterpret_cast<f32x4 *>(x + (int64_t)(16 * i) * a.ldx + col);
+            f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (have)
+                v = *px;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = TALL ? ec[k] : er;
+                // columns from cols on stay the zeros the next products read
+                v[k] = col + k < a.cols ? (a.a + f) * v[k] + acc[i][j][k] * (1.0f / (S_SCALE * X_SCALE)) : 0.0f;
+            }
+            const int at = stage_off<T::WTN>(16 * i + fr, 16 * j + fc);
+            if constexpr (LAST) {
+                typename El<__bf16>::v4 h;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    h[k] = (__bf16)v[k];
+                *reinterpret_cast<typename El<__bf16>::v4 *>(reinterpret_cast<__bf16 *>(stg) + at) = h;
+            } else {
+                half4 h;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    h[k] = (half_t)(v[k] * X_SCALE);
+                if (have)
+                    *px = v;
+                *reinterpret_cast<half4 *>(stg + at) = h;
+            }
+        }
+    }
+    if constexpr (LAST)
+        store_block<__bf16, T::WTM, T::WTN>(reinterpret_cast<const __bf16 *>(stg), a.out + (int64_t)m * a.o_stride,
+                                            a.ldo, r0, c0, a.rows, a.cols, a.vec, nullptr, lane);
+    else
+        store_block<half_t, T::WTM, T::WTN>(stg, a.xh + (int64_t)m * a.rows * a.ldx, a.ldx, r0, c0, a.rows,
+                                            (int)a.ldx, true, nullptr, lane);
+}
+
+// -------------------------------------------------------------------- plans
+// Tile classes by the number of tiles of the whole batch: 256×256 from 5/8
+// of the compute units on, 128×128 from 5/16, 64×64 below.
+enum Class { C256, C128, C64 };
+const char *const CLASS_NAME[] = {"256x256", "128x128", "64x64"};
+template <bool TA, bool TB>
+using T256 = Tile<half_t, 256, 256, 2, 2, 2, TA, TB>;
+template <bool TA, bool TB>
+using T128 = Tile<half_t, 128, 128, 2, 2, 2, TA, TB>;
+template <bool TA, bool TB>
+using T64 = Tile<half_t, 64, 64, 2, 2, 3, TA, TB>;
+
+struct Plan {
+    int64_t s, l, ldx, lds;
+    bool tall;
+    Class sym, upd;
+    int norm_blocks;
+};
+int64_t triangle(int64_t s, int b)
+{
+    const int64_t t = cdiv(s, b);
+    return t * (t + 1) / 2;
+}
+Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
+{
+    Plan p;
+    p.tall = rows > cols;
+    p.s = std::min(rows, cols), p.l = std::max(rows, cols);
+    p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
+    const auto cls = [&](auto count) {
+        return count(256) >= 160 ? C256 : count(128) >= 80 ? C128 : C64;
+    };
+    p.sym = cls([&](int b) { return batch * triangle(p.s, b); });
+    p.upd = cls([&](int b) { return batch * cdiv(rows, b) * cdiv(cols, b); });
+    const int64_t want = cdiv(rows * cols, 8192);
+    p.norm_blocks = (int)std::max((int64_t)1, std::min(want, std::max((int64_t)1, std::min((int64_t)NORM_BLOCKS, 2048 / batch))));
+    return p;
+}
+struct Buffers {
+    double *part;
+    float *x, *d, *e;
+    half_t *xh[2], *o, *p;
+    int64_t used = 0;
+};
+Buffers lay_out(char *base, const Plan &p, int64_t batch, int64_t rows)
+{
+    Buffers b;
+    const auto take = [&](auto *&ptr, int64_t n) {
+        using X = std::remove_reference_t<decltype(*ptr)>;
+        ptr = base ? reinterpret_cast<X *>(base + b.used) : nullptr;
+        b.used += round_up(n * (int64_t)sizeof(X), 256);
+    };
+    take(b.part, batch * p.norm_blocks);
+    take(b.x, batch * rows * p.ldx);
+    take(b.xh[0], batch * rows * p.ldx);
+    take(b.xh[1], batch * rows * p.ldx);
+    take(b.o, batch * p.s * p.lds);
+    take(b.p, batch * p.s * p.lds);
+    take(b.d, batch * p.lds);
+    take(b.e, batch * p.lds);
+    return b;
+}
+
+int validate_sizes(int64_t batch, int64_t rows, int64_t cols)
+{
+    if (batch < 0 || rows < 0 || cols < 0)
+        return TG_ERR_INVALID_ARG;
+    const int64_t lim = (int64_t)1 << 31;
+    if (rows >= MAX_DMA_LD - BK || cols >= MAX_DMA_LD - BK || batch >= lim)
+        return TG_ERR_TOO_LARGE;
+    if (batch * cdiv(rows, 64) >= lim || batch * cdiv(rows, 64) * cdiv(cols, 64) >= lim)
+        return TG_ERR_TOO_LARGE;
+    return TG_OK;
+}
+
+template <typename T>
+int64_t update_grid(UpdateArgs &u, int64_t batch)
+{
+    u.tiles_m = (int)cdiv(u.rows, T::BM), u.tiles_n = (int)cdiv(u.cols, T::BN);
+    u.total = (int)(batch * u.tiles_m * u.tiles_n);
+    return u.total;
+}
+template <template <bool, bool> class T, bool TALL>
+bool launch_step(UpdateArgs u, bool last, int64_t batch, void *stream)
+{
+    // wide: P (K-major) · X (transposed); tall: X (K-major) · P (K-major, symmetric)
+    using Tl = T<false, !TALL>;
+    const int64_t g = update_grid<Tl>(u, batch);
+    return last ? launch(ns_update_kernel<Tl, TALL, true>, g, Tl::THREADS, stream, u)
+                : launch(ns_update_kernel<Tl, TALL, false>, g, Tl::THREADS, stream, u);
+}
+template <template <bool, bool> class T, bool SQUARE, bool TRANS>
+bool launch_sym(SymArgs a, int64_t batch, void *stream)
+{
+    using Tl = T<TRANS, TRANS>;
+    a.tri = (int)triangle(a.s, Tl::BM);
+    a.total = (int)(batch * a.tri);
+    return launch(ns_sym_kernel<Tl, SQUARE>, a.total, Tl::THREADS, stream, a);
+}
+template <bool SQUARE, bool TRANS>
+bool launch_sym_class(Class c, const SymArgs &a, int64_t batch, void *stream)
+{
+    return c == C256   ? launch_sym<T256, SQUARE, TRANS>(a, batch, stream)
+           : c == C128 ? launch_sym<T128, SQUARE, TRANS>(a, batch, stream)
+                       : launch_sym<T64, SQUARE, TRANS>(a, batch, stream);
+}
+
+template <typename G>
+int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t g_stride,
+                  int64_t ldo, int64_t o_stride, int steps, const float *coefficients, float eps, void *ws,
+                  int64_t ws_bytes, void *stream)
+{
+    const int st = validate_sizes(batch, rows, cols);
+    if (st != TG_OK)
+        return st;
+    if (steps < 0 || steps > TG_NS_MAX_STEPS || !(eps >= 0.0f) || ldg < cols || ldo < cols || g_stride < 0)
+        return TG_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0 || cols == 0)
+        return TG_OK;
+    if (batch > 1 && o_stride < (rows - 1) * ldo + cols)
+        return TG_ERR_INVALID_ARG;
+    const Plan p = make_plan(batch, rows, cols);
+    const Buffers b = lay_out(reinterpret_cast<char *>(ws), p, batch, rows);
+    if (!g || !o || !ws || (uintptr_t)ws % 256 != 0 || ws_bytes < b.used)
+        return TG_ERR_INVALID_ARG;
+    if (gfx950_status() != 1)
+        return TG_ERR_DEVICE;
+    const G *src = reinterpret_cast<const G *>(g);
+    __bf16 *out = reinterpret_cast<__bf16 *>(o);
+    bool ok = launch(ns_norm_kernel<G>, batch * p.norm_blocks, 256, stream, src, rows, cols, ldg, g_stride,
+                     p.norm_blocks, b.part);
+    const int64_t chunks = cdiv(rows * p.ldx / 4, 256);
+    const int scale_blocks = (int)std::max((int64_t)1, std::min(chunks, std::max((int64_t)1, 8 * NUM_CU / batch)));
+    ok = ok && launch(ns_scale_kernel<G>, batch * scale_blocks, 256, stream, src, rows, cols, ldg, g_stride,
+                      p.norm_blocks, (const double *)b.part, eps, scale_blocks, b.x, b.xh[0], p.ldx,
+                      steps == 0 ? out : nullptr, ldo, o_stride);
+    for (int t = 0; ok && t < steps; ++t) {
+        static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
+        const float *k = coefficients ? coefficients + 3 * t : standard;
+        const half_t *xh = b.xh[t & 1];
+        SymArgs a = {};
+        a.x = {xh, p.ldx, (int)p.s};
+        a.x_stride = rows * p.ldx;
+        a.K = (int)(p.tall ? rows : round_up(cols, 8));
+        a.s = (int)p.s, a.out = b.o, a.lds = p.lds, a.diag = b.d;
+        ok = p.tall ? launch_sym_class<false, true>(p.sym, a, batch, stream)
+                    : launch_sym_class<false, false>(p.sym, a, batch, stream);
+        SymArgs q = {};
+        q.x = {b.o, p.lds, (int)p.s};
+        q.x_stride = p.s * p.lds;
+        q.K = (int)round_up(p.s, 8);
+        q.s = (int)p.s, q.out = b.p, q.lds = p.lds, q.diag = b.e, q.o = b.o, q.d = b.d;
+        q.b = k[1], q.c = k[2];
+        ok = ok && launch_sym_class<true, false>(p.sym, q, batch, stream);
+        UpdateArgs u = {};
+        const Operand x = {xh, p.ldx, (int)(p.tall ? rows : cols)}, pm = {b.p, p.lds, (int)p.s};
+        u.l = p.tall ? x : pm, u.r = p.tall ? pm : x;
+        u.l_stride = p.tall ? rows * p.ldx : p.s * p.lds, u.r_stride = p.tall ? p.s * p.lds : rows * p.ldx;
+        u.K = (int)(p.tall ? round_up(p.s, 8) : p.s);
+        u.rows = (int)rows, u.cols = (int)cols, u.x = b.x, u.xh = b.xh[(t + 1) & 1], u.ldx = p.ldx;
+        u.e = b.e, u.lds = p.lds, u.a = k[0];
+        u.out = out, u.ldo = ldo, u.o_stride = o_stride;
+        u.vec = ldo % 8 == 0 && o_stride % 8 == 0 && (uintptr_t)out % 16 == 0;
+        const bool last = t == steps - 1;
+        if (p.tall)
+            ok = ok && (p.upd == C256   ? launch_step<T256, true>(u, last, batch, stream)
+                        : p.upd == C128 ? launch_step<T128, true>(u, last, batch, stream)
+                                        : launch_step<T64, true>(u, last, batch, stream));
+        else
+            ok = ok && (p.upd == C256   ? launch_step<T256, false>(u, last, batch, stream)
+                        : p.upd == C128 ? launch_step<T128, false>(u, last, batch, stream)
+                                        : launch_step<T64, false>(u, last, batch, stream));
+    }
+    return ok ? TG_OK : TG_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" int64_t tg_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols)
+{
+    if (validate_sizes(batch, rows, cols) != TG_OK)
+        return -1;
+    if (batch == 0 || rows == 0 || cols == 0)
+        return 0;
+    return lay_out(nullptr, make_plan(batch, rows, cols), batch, rows).used;
+}
+
+extern "C" int tg_newton_schulz_f32(const void *G, void *O, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                    int64_t g_stride, int64_t ldo, int64_t o_stride, int steps,
+                                    const float *coefficients, float eps, void *workspace, int64_t workspace_bytes,
+                                    void *stream)
+{
+    return newton_schulz<float>(G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients, eps,
+                                workspace, workspace_bytes, stream);
+}
+
+extern "C" int tg_newton_schulz_f16(const void *G, void *O, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                    int64_t g_stride, int64_t ldo, int64_t o_stride, int steps,
+                                    const float *coefficients, float eps, void *workspace, int64_t workspace_bytes,
+                                    void *stream)
+{
+    return newton_schulz<_Float16>(G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients, eps,
+                                   workspace, workspace_bytes, stream);
+}
+
+extern "C" int tg_newton_schulz_bf16(const void *G, void *O, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                     int64_t g_stride, int64_t ldo, int64_t o_stride, int steps,
+                                     const float *coefficients, float eps, void *workspace, int64_t workspace_bytes,
+                                     void *stream)
+{
+    return newton_schulz<__bf16>(G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients, eps,
+                                 workspace, workspace_bytes, stream);
+}
+
+extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, char *name, int64_t name_len)
+{
+    if (name && name_len > 0)
+        name[0] = 0;
+    const int st = validate_sizes(batch, rows, cols);
+    if (st != TG_OK || batch == 0 || rows == 0 || cols == 0)
+        return st;
+    const Plan p = make_plan(batch, rows, cols);
+    if (name && name_len > 0)
+        snprintf(name, (size_t)name_len, "%s sym_%s update_%s", p.tall ? "tall" : "wide", CLASS_NAME[p.sym],
+                 CLASS_NAME[p.upd]);
+    return TG_OK;
+}

@@ -1,0 +1,356 @@
+"""The operators around a trained projection (include/tg_xent.h, include/tg_ortho.h).
+
+    tg_xent_f16 / tg_xent_bf16(...)          -> status   loss and lse of z = H·Wᵀ
+    tg_xent_bwd_f16 / tg_xent_bwd_bf16(...)  -> status   dH and dW
+    tg_xent_workspace_bytes(...), tg_xent_bwd_workspace_bytes(...), tg_xent_plan(...)
+    tg_newton_schulz_f32 / _f16 / _bf16(...) -> status
+    tg_newton_schulz_workspace_bytes(...), tg_newton_schulz_plan(...)
+    linear_cross_entropy(H, W, target, ...)  torch, differentiable
+    newton_schulz(G, ...)                    torch
+
+Argument marshalling, checks and autograd glue only, as in the package.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+TG_XENT_NONE = 0  # include/tg_xent.h
+TG_XENT_SUM = 1
+TG_XENT_MEAN = 2
+TG_NS_MAX_STEPS = 32
+_REDUCTIONS = {"none": TG_XENT_NONE, "sum": TG_XENT_SUM, "mean": TG_XENT_MEAN}
+
+
+def declare(lib) -> None:
+    """Argument types of the entry points (called once by the package's load())."""
+    i64, vp, ci, cf = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    for fn in (lib.tg_xent_workspace_bytes, lib.tg_xent_bwd_workspace_bytes):
+        fn.restype, fn.argtypes = i64, [vp, vp] + [i64] * 5
+    for fn in (lib.tg_xent_f16, lib.tg_xent_bf16):
+        fn.restype, fn.argtypes = ci, [vp] * 5 + [i64] * 6 + [ci, vp, i64, vp]
+    for fn in (lib.tg_xent_bwd_f16, lib.tg_xent_bwd_bf16):
+        fn.restype, fn.argtypes = ci, [vp] * 8 + [i64] * 8 + [ci, vp, i64, vp]
+    lib.tg_xent_plan.restype = ci
+    lib.tg_xent_plan.argtypes = [vp, vp] + [i64] * 5 + [ci, ctypes.c_char_p, i64, ctypes.POINTER(i64)]
+    lib.tg_newton_schulz_workspace_bytes.restype = i64
+    lib.tg_newton_schulz_workspace_bytes.argtypes = [i64] * 3
+    for fn in (lib.tg_newton_schulz_f32, lib.tg_newton_schulz_f16, lib.tg_newton_schulz_bf16):
+        fn.restype, fn.argtypes = ci, [vp, vp] + [i64] * 7 + [ci, ctypes.POINTER(cf), cf, vp, i64, vp]
+    lib.tg_newton_schulz_plan.restype = ci
+    lib.tg_newton_schulz_plan.argtypes = [i64] * 3 + [ctypes.c_char_p, i64]
+
+
+def _pkg():
+    import dense_fp16_gemm_02_amd as pkg
+
+    return pkg
+
+
+def _lib():
+    return _pkg().load()
+
+
+def _p(x):
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+def _s(s):
+    return s if s is None or isinstance(s, int) else s.cuda_stream
+
+
+def tg_xent_workspace_bytes(H, W, M: int, V: int, K: int, ldh: int, ldw: int) -> int:
+    """Workspace bytes of tg_xent_* for these arguments (-1: refused)."""
+    return _lib().tg_xent_workspace_bytes(_p(H), _p(W), M, V, K, ldh, ldw)
+
+
+def tg_xent_bwd_workspace_bytes(H, W, M: int, V: int, K: int, ldh: int, ldw: int) -> int:
+    """Workspace bytes of tg_xent_bwd_* for these arguments (-1: refused)."""
+    return _lib().tg_xent_bwd_workspace_bytes(_p(H), _p(W), M, V, K, ldh, ldw)
+
+
+def tg_xent_plan(H, W, M: int, V: int, K: int, ldh: int, ldw: int, backward: bool = False):
+    """Host-only: (status, kernel names, vocabulary pieces)."""
+    buf, pieces = ctypes.create_string_buffer(128), ctypes.c_int64(0)
+    st = _lib().tg_xent_plan(_p(H), _p(W), M, V, K, ldh, ldw, int(backward), buf, 128, ctypes.byref(pieces))
+    return st, buf.value.decode(), pieces.value
+
+
+def _xent(name, H, W, target, loss, lse, M, V, K, ldh, ldw, ignore_index, reduction, workspace, workspace_bytes,
+          stream):
+    return getattr(_lib(), name)(_p(H), _p(W), _p(target), _p(loss), _p(lse), M, V, K, ldh, ldw, ignore_index,
+                                 reduction, _p(workspace), workspace_bytes, _s(stream))
+
+
+def tg_xent_f16(H, W, target, loss, lse, M: int, V: int, K: int, ldh: int, ldw: int, ignore_index: int,
+                reduction: int, workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue loss and lse of the logits H·Wᵀ (binary16); returns the C status code."""
+    return _xent("tg_xent_f16", H, W, target, loss, lse, M, V, K, ldh, ldw, ignore_index, reduction, workspace,
+                 workspace_bytes, stream)
+
+
+def tg_xent_bf16(H, W, target, loss, lse, M: int, V: int, K: int, ldh: int, ldw: int, ignore_index: int,
+                 reduction: int, workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_xent_f16 for bfloat16 operands."""
+    return _xent("tg_xent_bf16", H, W, target, loss, lse, M, V, K, ldh, ldw, ignore_index, reduction, workspace,
+                 workspace_bytes, stream)
+
+
+def _xent_bwd(name, H, W, target, lse, dloss, dlse, dH, dW, M, V, K, ldh, ldw, lddh, lddw, ignore_index, reduction,
+              workspace, workspace_bytes, stream):
+    return getattr(_lib(), name)(_p(H), _p(W), _p(target), _p(lse), _p(dloss), _p(dlse), _p(dH), _p(dW), M, V, K,
+                                 ldh, ldw, lddh, lddw, ignore_index, reduction, _p(workspace), workspace_bytes,
+                                 _s(stream))
+
+
+def tg_xent_bwd_f16(H, W, target, lse, dloss, dlse, dH, dW, M: int, V: int, K: int, ldh: int, ldw: int, lddh: int,
+                    lddw: int, ignore_index: int, reduction: int, workspace, workspace_bytes: int,
+                    stream=None) -> int:
+    """Enqueue dH and dW (binary16; either may be None); returns the C status code."""
+    return _xent_bwd("tg_xent_bwd_f16", H, W, target, lse, dloss, dlse, dH, dW, M, V, K, ldh, ldw, lddh, lddw,
+                     ignore_index, reduction, workspace, workspace_bytes, stream)
+
+
+def tg_xent_bwd_bf16(H, W, target, lse, dloss, dlse, dH, dW, M: int, V: int, K: int, ldh: int, ldw: int, lddh: int,
+                     lddw: int, ignore_index: int, reduction: int, workspace, workspace_bytes: int,
+                     stream=None) -> int:
+    """tg_xent_bwd_f16 for bfloat16 operands."""
+    return _xent_bwd("tg_xent_bwd_bf16", H, W, target, lse, dloss, dlse, dH, dW, M, V, K, ldh, ldw, lddh, lddw,
+                     ignore_index, reduction, workspace, workspace_bytes, stream)
+
+
+def tg_newton_schulz_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    """Workspace bytes of tg_newton_schulz_* for these sizes (-1: refused)."""
+    return _lib().tg_newton_schulz_workspace_bytes(batch, rows, cols)
+
+
+def tg_newton_schulz_plan(batch: int, rows: int, cols: int):
+    """Host-only: (status, tile classes of the products)."""
+    buf = ctypes.create_string_buffer(128)
+    st = _lib().tg_newton_schulz_plan(batch, rows, cols, buf, 128)
+    return st, buf.value.decode()
+
+
+def _ns(name, G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients, eps, workspace,
+        workspace_bytes, stream):
+    c = None
+    if coefficients is not None:
+        if len(coefficients) != 3 * steps:
+            raise ValueError(f"coefficients holds {len(coefficients)} values, 3 for each of {steps} steps are needed")
+        c = (ctypes.c_float * max(1, 3 * steps))(*coefficients)
+    return getattr(_lib(), name)(_p(G), _p(O), batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, c, eps,
+                                 _p(workspace), workspace_bytes, _s(stream))
+
+
+def tg_newton_schulz_f32(G, O, batch: int, rows: int, cols: int, ldg: int, g_stride: int, ldo: int, o_stride: int,
+                         steps: int, coefficients, eps: float, workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue the iteration on fp32 matrices G into bfloat16 O; ``coefficients``
+    is a flat sequence of 3·steps numbers or None; returns the C status code."""
+    return _ns("tg_newton_schulz_f32", G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients,
+               eps, workspace, workspace_bytes, stream)
+
+
+def tg_newton_schulz_f16(G, O, batch: int, rows: int, cols: int, ldg: int, g_stride: int, ldo: int, o_stride: int,
+                         steps: int, coefficients, eps: float, workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_newton_schulz_f32 for binary16 matrices."""
+    return _ns("tg_newton_schulz_f16", G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients,
+               eps, workspace, workspace_bytes, stream)
+
+
+def tg_newton_schulz_bf16(G, O, batch: int, rows: int, cols: int, ldg: int, g_stride: int, ldo: int, o_stride: int,
+                          steps: int, coefficients, eps: float, workspace, workspace_bytes: int,
+                          stream=None) -> int:
+    """tg_newton_schulz_f32 for bfloat16 matrices."""
+    return _ns("tg_newton_schulz_bf16", G, O, batch, rows, cols, ldg, g_stride, ldo, o_stride, steps, coefficients,
+               eps, workspace, workspace_bytes, stream)
+
+
+# ------------------------------------------------------------------ torch
+def _row_stride(t, name, width):
+    """The row stride of a 2-D view whose rows do not overlap."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    if t.shape[0] <= 1:
+        return max(width, 1)
+    if t.stride(0) < width:
+        raise ValueError(f"{name} has row stride {t.stride(0)} < row length {width}; "
+                         "pass a tensor with non-overlapping rows (e.g. .contiguous())")
+    return t.stride(0)
+
+
+def _forward(H, W, target, ignore_index, reduction, want_lse):
+    import torch
+
+    M, K = H.shape
+    V = W.shape[0]
+    ldh, ldw = _row_stride(H, "H", K), _row_stride(W, "W", K)
+    lib = _lib()
+    h, w = H.data_ptr(), W.data_ptr()
+    size = lib.tg_xent_workspace_bytes(h, w, M, V, K, ldh, ldw)
+    dev = H.device
+    loss = torch.empty((M,) if reduction == TG_XENT_NONE else (), dtype=torch.float32, device=dev)
+    lse = torch.empty((M,), dtype=torch.float32, device=dev) if want_lse else None
+    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
+    fn = lib.tg_xent_f16 if H.dtype == torch.float16 else lib.tg_xent_bf16
+    with torch.cuda.device(dev):
+        st = fn(h, w, target.data_ptr(), loss.data_ptr(), _p(lse), M, V, K, ldh, ldw, ignore_index, reduction,
+                ws.data_ptr(), max(size, 0), torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        raise _pkg().TgError(st, "linear_cross_entropy")
+    return loss, lse
+
+
+def _backward(H, W, target, lse, dloss, dlse, need_h, need_w, ignore_index, reduction):
+    import torch
+
+    M, K = H.shape
+    V = W.shape[0]
+    ldh, ldw = _row_stride(H, "H", K), _row_stride(W, "W", K)
+    lib = _lib()
+    h, w = H.data_ptr(), W.data_ptr()
+    size = lib.tg_xent_bwd_workspace_bytes(h, w, M, V, K, ldh, ldw)
+    dev = H.device
+    dH = torch.empty((M, K), dtype=H.dtype, device=dev) if need_h else None
+    dW = torch.empty((V, K), dtype=W.dtype, device=dev) if need_w else None
+    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
+    fn = lib.tg_xent_bwd_f16 if H.dtype == torch.float16 else lib.tg_xent_bwd_bf16
+    with torch.cuda.device(dev):
+        st = fn(h, w, target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _p(dlse), _p(dH), _p(dW), M, V, K, ldh,
+                ldw, max(K, 1), max(K, 1), ignore_index, reduction, ws.data_ptr(), max(size, 0),
+                torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        raise _pkg().TgError(st, "linear_cross_entropy (backward)")
+    return dH, dW
+
+
+@functools.lru_cache(maxsize=None)
+def _xent_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class LinearCrossEntropy(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, H, W, target, ignore_index, reduction):
+            loss, lse = _forward(H, W, target, ignore_index, reduction, True)
+            ctx.save_for_backward(H, W, target, lse)
+            ctx.ignore_index, ctx.reduction = ignore_index, reduction
+            ctx.set_materialize_grads(False)
+            return loss, lse
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dloss, dlse):
+            H, W, target, lse = ctx.saved_tensors
+            if dloss is None and dlse is None:
+                return None, None, None, None, None
+            if dloss is None:
+                dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, device=H.device)
+            dloss = dloss.contiguous()
+            dlse = None if dlse is None else dlse.contiguous()
+            dH, dW = _backward(H, W, target, lse, dloss, dlse, ctx.needs_input_grad[0], ctx.needs_input_grad[1],
+                               ctx.ignore_index, ctx.reduction)
+            return dH, dW, None, None, None
+
+    return LinearCrossEntropy
+
+
+def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str = "mean", return_lse: bool = False):
+    """Softmax cross entropy of the logits H·Wᵀ, which are never stored.
+
+    H (M×K, hidden states) and W (V×K, the vocabulary projection) are fp16 or
+    bf16 GPU tensors of one dtype on one device, with a contiguous last
+    dimension and non-overlapping rows; ``target`` holds M int64 indices.
+    Tokens whose target is ``ignore_index`` take no part: loss 0, gradient 0,
+    not counted in the mean.  Any other target outside [0, V) gives a NaN loss.
+
+    ``reduction`` is "mean" (over the tokens that count; 0 if there are none),
+    "sum" or "none" (one loss per token).  Returns the fp32 loss, or (loss, lse)
+    with ``return_lse``, lse the log of each token's sum of exponentials (0 for
+    ignored tokens); both can be differentiated with respect to H and W, once.
+    For a penalty on the normaliser add e.g. ``1e-4 * (lse * lse).sum()``.
+
+    Runs on torch's current stream and takes its workspace from torch's
+    allocator.  Raises TypeError / ValueError on tensors it cannot take and
+    TgError on a non-zero status.
+    """
+    import torch
+
+    if H.dtype != W.dtype or H.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("H and W must both be float16 or both bfloat16")
+    if target.dtype != torch.int64:
+        raise TypeError("target must be int64")
+    if not H.is_cuda or W.device != H.device or target.device != H.device:
+        raise ValueError("H, W and target must be GPU tensors on the same device")
+    if H.dim() != 2 or W.dim() != 2 or target.dim() != 1:
+        raise ValueError("H and W must be 2-D, target 1-D")
+    if H.shape[1] != W.shape[1]:
+        raise ValueError(f"K mismatch: H is {tuple(H.shape)}, W is {tuple(W.shape)}")
+    if target.shape[0] != H.shape[0]:
+        raise ValueError(f"{target.shape[0]} targets for {H.shape[0]} rows of H")
+    if reduction not in _REDUCTIONS:
+        raise ValueError("reduction is 'none', 'sum' or 'mean'")
+    _row_stride(H, "H", H.shape[1])
+    _row_stride(W, "W", W.shape[1])
+    target = target.contiguous()
+    if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
+        loss, lse = _xent_function().apply(H, W, target, ignore_index, _REDUCTIONS[reduction])
+    else:
+        loss, lse = _forward(H, W, target, ignore_index, _REDUCTIONS[reduction], return_lse)
+    return (loss, lse) if return_lse else loss
+
+
+def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=None):
+    """Orthogonalised update: X ← a·X + (b·A + c·A²)·X, A = X·Xᵀ, ``steps`` times
+    from X = G / (‖G‖_F + eps), for a matrix or a batch of matrices.
+
+    G is a GPU tensor (rows × cols, or batch × rows × cols) of fp32, fp16 or
+    bf16 with a contiguous last dimension; the result is bfloat16 of the same
+    shape (see include/tg_ortho.h for the precision held inside).
+    ``coefficients`` is one triple (a, b, c) for all steps, or one per step;
+    the default is (3.4445, -4.7750, 2.0315).  ``out``, where given, is a bf16
+    tensor of G's shape with non-overlapping rows and matrices.
+
+    Runs on torch's current stream and takes its workspace from torch's
+    allocator; not differentiable.  Raises TypeError / ValueError on tensors it
+    cannot take and TgError on a non-zero status.
+    """
+    import torch
+
+    if G.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError("G must be float32, float16 or bfloat16")
+    if not G.is_cuda:
+        raise ValueError("G must be a GPU tensor")
+    if G.dim() not in (2, 3):
+        raise ValueError("G must be a matrix or a batch of matrices")
+    if not 0 <= steps <= TG_NS_MAX_STEPS:
+        raise ValueError(f"steps is 0 to {TG_NS_MAX_STEPS}")
+    flat = None
+    if coefficients is not None:
+        flat = [float(x) for c in coefficients for x in c] if steps and hasattr(coefficients[0], "__len__") \
+            else [float(x) for x in coefficients] * steps
+        if len(flat) != 3 * steps:
+            raise ValueError("coefficients is one (a, b, c), or one for each step")
+    if out is None:
+        out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+    elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
+        raise ValueError("out must be a bfloat16 tensor of G's shape on G's device")
+    g, o = (G, out) if G.dim() == 3 else (G.unsqueeze(0), out.unsqueeze(0))
+    batch, rows, cols = g.shape
+    if batch == 0 or rows == 0 or cols == 0:
+        return out
+    ldg, ldo = _row_stride(g[0], "G", cols), _row_stride(o[0], "out", cols)
+    if batch > 1 and o.stride(0) < (rows - 1) * ldo + cols:
+        raise ValueError("out has overlapping matrices")
+    lib = _lib()
+    size = lib.tg_newton_schulz_workspace_bytes(batch, rows, cols)
+    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=G.device)
+    fn = {torch.float32: lib.tg_newton_schulz_f32, torch.float16: lib.tg_newton_schulz_f16,
+          torch.bfloat16: lib.tg_newton_schulz_bf16}[G.dtype]
+    c = None if flat is None else (ctypes.c_float * max(1, len(flat)))(*flat)
+    with torch.cuda.device(G.device):
+        st = fn(g.data_ptr(), o.data_ptr(), batch, rows, cols, ldg, g.stride(0) if batch > 1 else rows * ldg, ldo,
+                o.stride(0) if batch > 1 else rows * ldo, steps, c, eps, ws.data_ptr(), max(size, 0),
+                torch.cuda.current_stream(G.device).cuda_stream)
+    if st:
+        raise _pkg().TgError(st, "newton_schulz")
+    return out
