@@ -26,9 +26,10 @@
 //              16 columns inside each group of 16 lanes: lane s of a group
 //              supplies row s / 4 and columns 4·(s % 4) .. +3, lane i receives
 //              column i of the four rows.  The 32-byte column slots of row k
-//              are XORed with k's bits 0, 1 and 3 (64 columns: bits 1 and 3),
-//              so that the eight rows a half wave reads fall on eight different
-//              32-byte bank groups (without it four rows share one).
+//              are XORed with k's bits 0, 1 and 3 (64 and 192 columns, whose
+//              odd rows start half a bank line further: bits 1 and 3), so that
+//              the eight rows a half wave reads fall on eight different 32-byte
+//              bank groups (without it four rows share one).
 //
 // Rings: S + 1 stages of A and S of B, refilled S K-tiles ahead.  K-tile t is
 // two 32-K steps: step 0 multiplies while step 1's fragments are read and
@@ -151,6 +152,26 @@ __device__ inline int lane_id()
     return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
 }
 
+__device__ inline void pin(f32x4 &v)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+a"(v));
+#else
+    (void)v;
+#endif
+}
+// A value that is the same in every lane, in scalar registers: buffer
+// descriptors built from values that the compiler takes for per-lane ones cost a
+// loop over the lanes at every DMA.
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline const char *uniform(const char *p)
+{
+    const uint64_t u = (uint64_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+    return reinterpret_cast<const char *>((uint64_t)hi << 32 | lo);
+}
+
 // Workgroup id → tile.  Workgroup w runs on XCD w mod 8; each XCD takes a
 // contiguous range of logical ids, which walk groups of GM tile rows column
 // by column, so that the tiles resident on one XCD share operand bands in its
@@ -208,7 +229,7 @@ static_assert(tg::layout::check_swizzled_tile(tg::layout::swizzle_bank256_f16(25
 template <int BX>
 __host__ __device__ constexpr int trans_swz(int k)
 {
-    return BX >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
+    return BX % 128 == 0 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
 }
 // element offset of column x (a multiple of 4) of K row k
 template <int BX>
@@ -236,8 +257,8 @@ constexpr bool trans_reads_are_conflict_free()
             }
     return true;
 }
-static_assert(trans_reads_are_conflict_free<256>() && trans_reads_are_conflict_free<128>() &&
-                  trans_reads_are_conflict_free<64>(),
+static_assert(trans_reads_are_conflict_free<256>() && trans_reads_are_conflict_free<192>() &&
+                  trans_reads_are_conflict_free<128>() && trans_reads_are_conflict_free<64>(),
               "transposed fragment reads must spread over the banks");
 
 // One operand of a tile product.
@@ -279,8 +300,9 @@ struct Tile {
                 const int kc = (lane & 7) ^ kmajor_swz(t);
                 off[p] = (uint32_t)((int64_t)imin(t, extent - 1 - x0) * ld * 2 + 16 * kc);
             } else {
-                constexpr int CPR = BX / 8, RPD = 512 / BX;
-                const int k = RPD * (p * NW + wave) + lane / CPR, cp = lane % CPR;
+                constexpr int CPR = BX / 8;
+                const int slot = (p * NW + wave) * 64 + lane;
+                const int k = slot / CPR, cp = slot % CPR;
                 const int x = ((((cp >> 1) ^ trans_swz<BX>(k)) << 1) | (cp & 1)) * 8;
                 off[p] = (uint32_t)((int64_t)k * ld * 2 + 2 * imin(x, ((extent - 1 - x0) & ~7)));
             }
@@ -291,9 +313,13 @@ struct Tile {
     // KT = cdiv(K, 64) K-tiles; K == 0 adds nothing.  Every wave's DMAs have
     // landed on return, but other waves may still read the stages: a caller
     // that reuses smem first passes a barrier.
+    // `ahead` is called before the last K-tile's products (256×256) or after
+    // them: a place for an epilogue's first loads.
+    template <typename F>
     __device__ static __attribute__((always_inline)) void run(E *smem, const Operand &a, const Operand &b, int x0a,
-                                                             int x0b, int K, f32x4 (&acc)[TM][TN])
+                                                             int x0b, int K, f32x4 (&acc)[TM][TN], F ahead)
     {
+        x0a = uniform(x0a), x0b = uniform(x0b), K = uniform(K);
         E *const a_ring = smem;
         E *const b_ring = smem + (S + 1) * STAGE_A;
         const int lane = threadIdx.x & 63;
@@ -306,9 +332,9 @@ struct Tile {
         dma_offsets<TA, BM>(a_off, a.ld, x0a, a.extent, lane, wave);
         dma_offsets<TB, BN>(b_off, b.ld, x0b, b.extent, lane, wave);
         const char *const a_base =
-            reinterpret_cast<const char *>(a.p) + 2 * (TA ? (int64_t)x0a : (int64_t)x0a * a.ld + k0);
+            uniform(reinterpret_cast<const char *>(a.p) + 2 * (TA ? (int64_t)x0a : (int64_t)x0a * a.ld + k0));
         const char *const b_base =
-            reinterpret_cast<const char *>(b.p) + 2 * (TB ? (int64_t)x0b : (int64_t)x0b * b.ld + k0);
+            uniform(reinterpret_cast<const char *>(b.p) + 2 * (TB ? (int64_t)x0b : (int64_t)x0b * b.ld + k0));
         const int64_t a_step = TA ? 2 * BK * a.ld : 2 * BK, b_step = TB ? 2 * BK * b.ld : 2 * BK;
         // K-tile t's buffer: empty past the end; a transposed operand's ends
         // with its last K row.  32-bit scalar arithmetic without branches: a
@@ -427,9 +453,15 @@ struct Tile {
         for (int q = 0; q < NFRAG; ++q)
             read_frag(0, 0, 0, q, fa[0], fb[0]);
 
+        // Up to 192×192 the last K-tile is one like the others (its refills have
+        // empty ranges, the fragments it reads ahead go unused; K == 0 runs
+        // none): half the code, and a launch of few workgroups pays for its
+        // instruction fetches.  At 256×256 it is peeled off (K == 0: on zeros):
+        // there the allocator moves accumulators around the plain loop.
+        constexpr bool PEEL = BM * BN >= 256 * 256;
         int sa = 0, sb = 0;       // stages of K-tile t
         int da = S % (S + 1);     // stage A(t+S) goes into
-        for (int t = 0; t < KT - 1; ++t) {
+        for (int t = 0; t < (PEEL ? KT - 1 : KT); ++t) {
             step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 1, rsrc_a(t + S), da);
             wait_vmem<(S - 2) * (PA + PB) + PA>();  // K-tile t+1 has landed (this wave's part)
             barrier_lds();                          // ... for every wave; K-tile t's stages are drained
@@ -439,11 +471,26 @@ struct Tile {
             sa = sa1;
             sb = sb1;
         }
-        // the last K-tile (K == 0: zeros, from empty buffer ranges)
-        const auto none = __builtin_amdgcn_make_buffer_rsrc(nullptr, (short)0, 0, BUFFER_WORD3);
-        step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 0, none, 0);
-        step(fa[1], fb[1], false, 0, 0, 0, fa[0], fb[0], 0, none, 0);
+        ahead();
+        if constexpr (PEEL) {
+            const auto none = __builtin_amdgcn_make_buffer_rsrc(nullptr, (short)0, 0, BUFFER_WORD3);
+            step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 0, none, 0);
+            step(fa[1], fb[1], false, 0, 0, 0, fa[0], fb[0], 0, none, 0);
+        }
+        // (the accumulators stay where they are between the loop and the
+        // epilogue: without this some instantiations spilled a few of them)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                pin(acc[i][j]);
         wait_vmem<0>();
+    }
+
+    __device__ static __attribute__((always_inline)) void run(E *smem, const Operand &a, const Operand &b, int x0a,
+                                                             int x0b, int K, f32x4 (&acc)[TM][TN])
+    {
+        run(smem, a, b, x0a, x0b, K, acc, [] {});
     }
 
     __device__ static __attribute__((always_inline)) void clear(f32x4 (&acc)[TM][TN])
@@ -458,41 +505,113 @@ struct Tile {
 
 // ------------------------------------------------------- staged block stores
 // A wave's R×C block of 16-bit values in LDS, row-major with the 16-byte
-// chunk index of row r XORed with r mod (C/8).
+// chunk index of row r XORed with r mod the largest power of two in C/8.
 template <int C>
 __host__ __device__ constexpr int stage_off(int r, int c)
 {
-    return r * C + (((c >> 3) ^ (r & (C / 8 - 1))) << 3) + (c & 7);
+    constexpr int MASK = ((C / 8) & -(C / 8)) - 1;
+    return r * C + (((c >> 3) ^ (r & MASK)) << 3) + (c & 7);
 }
 // Rows [0, R) of the staged block to D rows row0 + r (through `map` where it
 // is given: D row map[row0 + r]), columns col0 .., inside rows × cols; `vec`:
-// D's rows are 16-byte aligned.
-template <typename E, int R, int C>
+// D's rows are 16-byte aligned.  WORKSPACE: they always are, and cols is a
+// multiple of 8.
+template <typename E, int R, int C, bool WORKSPACE = false>
 __device__ inline void store_block(const E *stg, E *__restrict__ D, int64_t ld, int row0, int col0, int rows,
                                    int cols, bool vec, const int *__restrict__ map, int lane)
 {
     using V8 = typename El<E>::v8;
-    constexpr int CH = C / 8, RPP = 64 / CH;
-    const int rc = lane % CH, rr = lane / CH, col = col0 + 8 * rc;
+    constexpr int CH = C / 8;
+    static_assert(R * CH % 64 == 0, "whole passes");
+    if (WORKSPACE || (vec && col0 + C <= cols)) {
 #pragma unroll 4
-    for (int r0 = 0; r0 < R; r0 += RPP) {
-        const int r = r0 + rr, row = row0 + r;
-        const V8 v = *reinterpret_cast<const V8 *>(stg + stage_off<C>(r, 8 * rc));
-        if (row >= rows)
-            continue;
-        E *dst = D + (int64_t)(map ? map[row] : row) * ld + col;
-        if (vec && col + 8 <= cols) {
-            *reinterpret_cast<V8 *>(dst) = v;
-        } else {
+        for (int p = 0; p < R * CH / 64; ++p) {
+            const int at = p * 64 + lane, rc = at % CH, r = at / CH;
+            const int row = row0 + r, col = col0 + 8 * rc;
+            const V8 v = *reinterpret_cast<const V8 *>(stg + stage_off<C>(r, 8 * rc));
+            if (row < rows && (!WORKSPACE || col < cols))
+                *reinterpret_cast<V8 *>(D + (int64_t)(map ? map[row] : row) * ld + col) = v;
+        }
+    } else {
+#pragma unroll 1
+        for (int p = 0; p < R * CH / 64; ++p) {
+            const int at = p * 64 + lane, rc = at % CH, r = at / CH;
+            const int row = row0 + r, col = col0 + 8 * rc;
+            const V8 v = *reinterpret_cast<const V8 *>(stg + stage_off<C>(r, 8 * rc));
+            if (row < rows) {
+                E *dst = D + (int64_t)(map ? map[row] : row) * ld + col;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col + e < cols)
-                    dst[e] = v[e];
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < cols)
+                        dst[e] = v[e];
+            }
         }
     }
 }
+// Zero what a staged R×C block holds from row `rows` or column `cols` on.
+template <typename E, int R, int C>
+__device__ inline void clear_outside(E *stg, int rows, int cols, int lane)
+{
+    using V8 = typename El<E>::v8;
+#pragma unroll 1
+    for (int p = 0; p < R * C / 8 / 64; ++p) {
+        const int at = p * 64 + lane, c = at % (C / 8) * 8, r = at / (C / 8);
+        V8 *q = reinterpret_cast<V8 *>(stg + stage_off<C>(r, c));
+        V8 v = *q;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = r < rows && c + e < cols ? v[e] : (E)0.0f;
+        *q = v;
+    }
+}
+
+// The transpose of a staged R×C block: D rows row0 .. row0 + C - 1, columns
+// col0 .. col0 + R - 1, inside rows × cols (cols a multiple of 8, D's rows
+// 16-byte aligned).  Two transposing LDS reads give a lane 8 consecutive
+// elements of one row of the transpose.
+template <typename E, int R, int C>
+__device__ inline void store_block_transposed(const E *stg, E *__restrict__ D, int64_t ld, int row0, int col0,
+                                              int rows, int cols, int lane)
+{
+    static_assert(R % 32 == 0 && C % 16 == 0, "whole groups");
+    const int s = lane & 15, g = lane >> 4;
+#pragma unroll 2
+    for (int q = 0; q < C / 16; ++q)
+#pragma unroll
+        for (int h = 0; h < R / 32; ++h) {
+            const int r = 32 * h + 8 * g;
+            union {
+                s16x4 h4[2];
+                uint4 v;
+            } u;
+            u.h4[0] = lds_read_tr(stg + stage_off<C>(r + (s >> 2), 16 * q + 4 * (s & 3)));
+            u.h4[1] = lds_read_tr(stg + stage_off<C>(r + 4 + (s >> 2), 16 * q + 4 * (s & 3)));
+            const int row = row0 + 16 * q + s, col = col0 + r;
+            if (row < rows && col < cols)
+                *reinterpret_cast<uint4 *>(D + (int64_t)row * ld + col) = u.v;
+        }
+}
 
 // ------------------------------------------------------------------- host
+// Time in microseconds of `n` tiles of class `c` with `ktiles` K-tiles each:
+// whole rounds of the workgroups that run at once, each the K-tiles of its tiles
+// and a fixed part (first loads, epilogue, instruction fetches).  The constants
+// were measured on one MI355X with launches of 1, 4 and 16 rounds and 2 to 224
+// K-tiles; the model is within some 15% of those times.
+struct TileClass {
+    int bm, bn;
+    int per_cu;     // workgroups per compute unit
+    double ktile;   // per K-tile with all of them running
+    double alone;   // with one per unit
+    double fixed;
+};
+inline double tile_time(const TileClass &c, int64_t n, int64_t ktiles)
+{
+    const int64_t slots = (int64_t)NUM_CU * c.per_cu, rounds = cdiv(n, slots), rest = n - (rounds - 1) * slots;
+    const double k = (double)ktiles;
+    return (double)(rounds - 1) * (k * c.ktile + c.fixed) + k * (rest > NUM_CU ? c.ktile : c.alone) + c.fixed;
+}
+
 // 1 yes, -1 no, 0 not yet asked, per device
 inline int gfx950_status()
 {

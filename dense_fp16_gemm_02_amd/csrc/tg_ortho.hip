@@ -49,9 +49,10 @@ typedef half_t half4 __attribute__((ext_vector_type(4)));
 constexpr float X_SCALE = 16384.0f, S_SCALE = 4096.0f;  // of X, and of O and P
 
 // ------------------------------------------------------------- norm, scaling
-constexpr int NORM_BLOCKS = 128;  // most partial sums per matrix
+constexpr int NORM_BLOCKS = 1024;  // most partial sums per matrix
 // Sums of squares in 64 bits: fp32 squares would overflow or vanish for
-// elements beyond 1e19 or below 1e-23.  Reads G once.
+// elements beyond 1e19 or below 1e-23.  Reads G once, 16 bytes per lane where
+// rows follow each other without gaps and are aligned.
 template <typename G>
 __global__ __launch_bounds__(256) void ns_norm_kernel(const G *g, int64_t rows, int64_t cols, int64_t ld,
                                                       int64_t stride, int blocks, double *part)
@@ -60,18 +61,28 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const G *g, int64_t rows, 
     const int m = blockIdx.x / blocks, blk = blockIdx.x % blocks;
     const G *p = g + (int64_t)m * stride;
     double s = 0.0;
+    const auto add = [&](G v) {
+        const double x = (double)(float)v;
+        s += x * x;
+    };
     const int64_t total = rows * cols;
     if (ld == cols) {
-        for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
-            const double x = (double)(float)p[i];
-            s += x * x;
+        constexpr int N = 16 / sizeof(G);
+        typedef G vec __attribute__((ext_vector_type(N)));
+        const int64_t chunks = (uintptr_t)p % 16 == 0 ? total / N : 0;
+#pragma unroll 4
+        for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < chunks; i += (int64_t)blocks * 256) {
+            const vec v = *reinterpret_cast<const vec *>(p + i * N);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                add(v[e]);
         }
+        for (int64_t i = chunks * N + (int64_t)blk * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256)
+            add(p[i]);
     } else {
         for (int64_t r = blk; r < rows; r += blocks)
-            for (int64_t c = threadIdx.x; c < cols; c += 256) {
-                const double x = (double)(float)p[r * ld + c];
-                s += x * x;
-            }
+            for (int64_t c = threadIdx.x; c < cols; c += 256)
+                add(p[r * ld + c]);
     }
     for (int o = 32; o; o >>= 1)
         s += __shfl_xor(s, o);
@@ -165,65 +176,67 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     const int fr = lane & 15, fc = 4 * (lane >> 4);
     const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
     half_t *out = a.out + (int64_t)m * a.s * a.lds;
-    float *diag = a.diag + (int64_t)m * a.lds;
-    const half_t *o = SQUARE ? a.o + (int64_t)m * a.s * a.lds : nullptr;
-    const float *d = SQUARE ? a.d + (int64_t)m * a.lds : nullptr;
+    float *__restrict__ diag = a.diag + (int64_t)m * a.lds;
+    const half_t *__restrict__ o = SQUARE ? a.o + (int64_t)m * a.s * a.lds : nullptr;
+    const float *__restrict__ d = SQUARE ? a.d + (int64_t)m * a.lds : nullptr;
     barrier_lds();
     half_t *stg = smem + wave * T::WTM * T::WTN;
-    // columns outside, rows inside: one set of column masks is live at a time
+    // Rows and columns past s hold copies of the last ones' products here (and
+    // their loads are clamped alike); they are cleared in the staged block.
+    // Columns outside, rows inside, so that a column's loads (O, d) are all in
+    // flight before they are used.
+    float dr[T::TM];
 #pragma unroll
-    for (int j = 0; j < T::TN; ++j) {
-        const int col = c0 + 16 * j + fc;
-        f32x4 dc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (SQUARE && col < a.s)
-            dc = *reinterpret_cast<const f32x4 *>(d + col);
+    for (int i = 0; i < T::TM; ++i)
+        dr[i] = SQUARE ? d[imin(r0 + 16 * i + fr, a.s - 1)] : 0.0f;
+    // the diagonal: in fp32, and out of the staged block (below)
+    if (r0 == c0 && fr >= fc && fr < fc + 4)
 #pragma unroll
         for (int i = 0; i < T::TM; ++i) {
-            const int row = r0 + 16 * i + fr;
-            const bool in = row < a.s;
-            const float dr = SQUARE && in ? d[row] : 0.0f;
-            half4 oh = half4{0, 0, 0, 0}, h;
-            if (SQUARE && in && col < a.s)
-                oh = *reinterpret_cast<const half4 *>(o + (int64_t)row * a.lds + col);
+            float y = 0.0f;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                y = fr == fc + v ? acc[i][i][v] : y;
+            if (r0 + 16 * i + fr < a.s)
+                diag[r0 + 16 * i + fr] = SQUARE
+                                             ? a.b * dr[i] + a.c * (dr[i] * dr[i] + y * (1.0f / (S_SCALE * S_SCALE)))
+                                             : y * (1.0f / (X_SCALE * X_SCALE));
+        }
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) {
+        const int col = imin(c0 + 16 * j + fc, (a.s - 1) & ~3);
+        f32x4 dc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        half4 oh[T::TM];
+        if constexpr (SQUARE) {
+            dc = *reinterpret_cast<const f32x4 *>(d + col);
+#pragma unroll
+            for (int i = 0; i < T::TM; ++i)
+                oh[i] = *reinterpret_cast<const half4 *>(o + (int64_t)imin(r0 + 16 * i + fr, a.s - 1) * a.lds + col);
+        }
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) {
+            half4 h;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const bool valid = in && col + v < a.s;
-                float y;
+                float y = acc[i][j][v] * (SQUARE ? 1.0f / S_SCALE : S_SCALE / (X_SCALE * X_SCALE));
                 if constexpr (SQUARE) {
-                    const float f = (float)oh[v];
-                    y = a.b * f + a.c * ((dr + dc[v]) * f + acc[i][j][v] * (1.0f / S_SCALE));
-                    if (valid && row == col + v) {
-                        diag[row] = a.b * dr + a.c * (dr * dr + acc[i][j][v] * (1.0f / (S_SCALE * S_SCALE)));
-                        y = 0.0f;
-                    }
-                } else {
-                    y = acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE));
-                    if (valid && row == col + v) {
-                        diag[row] = acc[i][j][v] * (1.0f / (X_SCALE * X_SCALE));
-                        y = 0.0f;
-                    }
+                    const float f = (float)oh[i][v];
+                    y = a.b * f + a.c * ((dr[i] + dc[v]) * f + y);
                 }
-                // the rounding of the next product's operand
-                h[v] = valid ? (half_t)y : (half_t)0.0f;
+                h[v] = (half_t)y;  // the rounding of the next product's operand
             }
             *reinterpret_cast<half4 *>(stg + stage_off<T::WTN>(16 * i + fr, 16 * j + fc)) = h;
         }
     }
-    store_block<half_t, T::WTM, T::WTN>(stg, out, a.lds, r0, c0, a.s, (int)a.lds, true, nullptr, lane);
-    if (tm == tn)
-        return;
-    // the mirror image: the staged block, read by columns
-#pragma unroll 1
-    for (int p = 0; p < T::WTN * T::WTM / 8 / 64; ++p) {
-        const int idx = p * 64 + lane;
-        const int r = idx / (T::WTM / 8), c = (idx % (T::WTM / 8)) * 8;  // row of the image, first of 8 columns
-        typename El<half_t>::v8 v;
+    if (r0 == c0 && fr >= fc && fr < fc + 4)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = stg[stage_off<T::WTN>(c + e, r)];
-        if (c0 + r < a.s && r0 + c < a.lds)
-            *reinterpret_cast<typename El<half_t>::v8 *>(out + (int64_t)(c0 + r) * a.lds + r0 + c) = v;
-    }
+        for (int i = 0; i < T::TM; ++i)
+            stg[stage_off<T::WTN>(16 * i + fr, 16 * i + fr)] = (half_t)0.0f;
+    if (imax(r0, c0) + T::WTM > a.s)
+        clear_outside<half_t, T::WTM, T::WTN>(stg, a.s - r0, a.s - c0, lane);
+    store_block<half_t, T::WTM, T::WTN, true>(stg, out, a.lds, r0, c0, a.s, (int)a.lds, true, nullptr, lane);
+    if (tm != tn)
+        store_block_transposed<half_t, T::WTM, T::WTN>(stg, out, a.lds, c0, r0, a.s, (int)a.lds, lane);
 }
 
 // ------------------------------------------------------------------- update
@@ -259,41 +272,55 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     Operand l = a.l, r = a.r;
     l.p = reinterpret_cast<const half_t *>(l.p) + (int64_t)m * a.l_stride;
     r.p = reinterpret_cast<const half_t *>(r.p) + (int64_t)m * a.r_stride;
-    f32x4 acc[T::TM][T::TN];
-    T::clear(acc);
-    T::run(smem, l, r, m0, n0, a.K, acc);
-
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / T::WN, wn = wave % T::WN;
     const int fr = lane & 15, fc = 4 * (lane >> 4);
     const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
-    const float *e = a.e + (int64_t)m * a.lds;
-    float *x = a.x + ((int64_t)m * a.rows + r0 + fr) * a.ldx;
+    const float *__restrict__ e = a.e + (int64_t)m * a.lds;
+    float *x = a.x + (int64_t)m * a.rows * a.ldx;
+    // X some columns of blocks ahead of its use, the first of them before the
+    // last K-tile: their loads (1 KiB each) are what the epilogue waits for,
+    // and with one column ahead it waited 35 us of a 4096×4096 step's 150.
+    // Loads are clamped; what lies past cols is cleared in the staged block.
+    constexpr int DEPTH = 4, EARLY = T::BM * T::BN >= 256 * 256 ? (LAST ? 0 : 1) : DEPTH - 1;
+    f32x4 xs[DEPTH][T::TM];
+    auto fetch = [&](int j) __attribute__((always_inline)) {
+        const int col = imin(c0 + 16 * j + fc, (a.cols - 1) & ~3);
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+            xs[j % DEPTH][i] = *reinterpret_cast<const f32x4 *>(x + (int64_t)imin(r0 + 16 * i + fr, a.rows - 1) * a.ldx + col);
+    };
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    T::run(smem, l, r, m0, n0, a.K, acc, [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < EARLY && j < T::TN; ++j)
+            fetch(j);
+    });
     barrier_lds();
     half_t *stg = smem + wave * T::WTM * T::WTN;
-    // columns outside, rows inside: one set of column masks is live at a time
+    float er[T::TM];
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+        er[i] = TALL ? 0.0f : e[imin(r0 + 16 * i + fr, a.rows - 1)];
+#pragma unroll
+    for (int j = EARLY; j < DEPTH - 1 && j < T::TN; ++j)
+        fetch(j);
 #pragma unroll
     for (int j = 0; j < T::TN; ++j) {
         const int col = c0 + 16 * j + fc;
+        if (j + DEPTH - 1 < T::TN)
+            fetch(j + DEPTH - 1);
         f32x4 ec = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (TALL && col < a.cols)
-            ec = *reinterpret_cast<const f32x4 *>(e + col);
+        if constexpr (TALL)
+            ec = *reinterpret_cast<const f32x4 *>(e + imin(col, (a.cols - 1) & ~3));
 #pragma unroll
         for (int i = 0; i < T::TM; ++i) {
-            const int row = r0 + 16 * i + fr;
-            const bool have = row < a.rows && col < a.ldx;
-            const float er = !TALL && row < a.rows ? e[row] : 0.0f;
-            f32x4 *px = reinterpret_cast<f32x4 *>(x + (int64_t)(16 * i) * a.ldx + col);
-            f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (have)
-                v = *px;
+            f32x4 v = xs[j % DEPTH][i];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float f = TALL ? ec[k] : er;
-                // columns from cols on stay the zeros the next products read
-                v[k] = col + k < a.cols ? (a.a + f) * v[k] + acc[i][j][k] * (1.0f / (S_SCALE * X_SCALE)) : 0.0f;
-            }
+            for (int k = 0; k < 4; ++k)
+                v[k] = (a.a + (TALL ? ec[k] : er[i])) * v[k] + acc[i][j][k] * (1.0f / (S_SCALE * X_SCALE));
             const int at = stage_off<T::WTN>(16 * i + fr, 16 * j + fc);
             if constexpr (LAST) {
                 typename El<__bf16>::v4 h;
@@ -306,27 +333,43 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     h[k] = (half_t)(v[k] * X_SCALE);
-                if (have)
-                    *px = v;
+                if (r0 + 16 * i + fr < a.rows && col < a.cols)
+                    *reinterpret_cast<f32x4 *>(x + (int64_t)(r0 + 16 * i + fr) * a.ldx + col) = v;
                 *reinterpret_cast<half4 *>(stg + at) = h;
             }
         }
     }
+    if (!LAST && c0 + T::WTN > a.cols)
+        clear_outside<half_t, T::WTM, T::WTN>(stg, T::WTM, a.cols - c0, lane);
     if constexpr (LAST)
         store_block<__bf16, T::WTM, T::WTN>(reinterpret_cast<const __bf16 *>(stg), a.out + (int64_t)m * a.o_stride,
                                             a.ldo, r0, c0, a.rows, a.cols, a.vec, nullptr, lane);
     else
-        store_block<half_t, T::WTM, T::WTN>(stg, a.xh + (int64_t)m * a.rows * a.ldx, a.ldx, r0, c0, a.rows,
+        store_block<half_t, T::WTM, T::WTN, true>(stg, a.xh + (int64_t)m * a.rows * a.ldx, a.ldx, r0, c0, a.rows,
                                             (int)a.ldx, true, nullptr, lane);
 }
 
 // -------------------------------------------------------------------- plans
-// Tile classes by the number of tiles of the whole batch: 256×256 from 5/8
-// of the compute units on, 128×128 from 5/16, 64×64 below.
-enum Class { C256, C128, C64 };
-const char *const CLASS_NAME[] = {"256x256", "128x128", "64x64"};
+// Tile classes, chosen by tile_time for the whole batch.  One 256×256 or
+// 192×192 workgroup per CU, two of the smaller ones.  192×192 is there for the
+// counts that leave most of a round of 256×256 tiles empty: the lower triangle
+// of 4096×4096 is 136 tiles of 256 (or 528 of 128, one round of 512 and 16 more)
+// but 253 of 192, one round of the 256 CUs.
+enum Class { C256, C192, C128, C64, CLASSES };
+const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64"};
+constexpr TileClass SYM_CLASS[] = {{256, 256, 1, 1.40, 1.40, 14.0},
+                                   {192, 192, 1, 1.15, 1.15, 5.0},
+                                   {128, 128, 2, 1.10, 0.50, 5.0},
+                                   {64, 64, 2, 0.50, 0.27, 4.0}};
+// the update's epilogue reads and writes X in fp32 besides
+constexpr TileClass UPD_CLASS[] = {{256, 256, 1, 1.50, 1.50, 35.0},
+                                   {192, 192, 1, 1.25, 1.25, 18.0},
+                                   {128, 128, 2, 1.10, 0.50, 14.0},
+                                   {64, 64, 2, 0.50, 0.27, 4.5}};
 template <bool TA, bool TB>
 using T256 = Tile<half_t, 256, 256, 2, 2, 2, TA, TB>;
+template <bool TA, bool TB>
+using T192 = Tile<half_t, 192, 192, 2, 2, 2, TA, TB>;
 template <bool TA, bool TB>
 using T128 = Tile<half_t, 128, 128, 2, 2, 2, TA, TB>;
 template <bool TA, bool TB>
@@ -335,7 +378,7 @@ using T64 = Tile<half_t, 64, 64, 2, 2, 3, TA, TB>;
 struct Plan {
     int64_t s, l, ldx, lds;
     bool tall;
-    Class sym, upd;
+    Class gram, square, upd;
     int norm_blocks;
 };
 int64_t triangle(int64_t s, int b)
@@ -349,13 +392,19 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
     p.tall = rows > cols;
     p.s = std::min(rows, cols), p.l = std::max(rows, cols);
     p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
-    const auto cls = [&](auto count) {
-        return count(256) >= 160 ? C256 : count(128) >= 80 ? C128 : C64;
+    const auto best = [&](const TileClass *cls, auto count, int64_t k) {
+        int c = 0;
+        for (int i = 1; i < CLASSES; ++i)
+            if (tile_time(cls[i], count(cls[i].bm), cdiv(k, BK)) < tile_time(cls[c], count(cls[c].bm), cdiv(k, BK)))
+                c = i;
+        return (Class)c;
     };
-    p.sym = cls([&](int b) { return batch * triangle(p.s, b); });
-    p.upd = cls([&](int b) { return batch * cdiv(rows, b) * cdiv(cols, b); });
+    const auto sym = [&](int b) { return batch * triangle(p.s, b); };
+    p.gram = best(SYM_CLASS, sym, p.l);
+    p.square = best(SYM_CLASS, sym, p.s);
+    p.upd = best(UPD_CLASS, [&](int b) { return batch * cdiv(rows, b) * cdiv(cols, b); }, p.s);
     const int64_t want = cdiv(rows * cols, 8192);
-    p.norm_blocks = (int)std::max((int64_t)1, std::min(want, std::max((int64_t)1, std::min((int64_t)NORM_BLOCKS, 2048 / batch))));
+    p.norm_blocks = (int)std::max((int64_t)1, std::min(want, std::max((int64_t)1, std::min((int64_t)NORM_BLOCKS, 4096 / batch))));
     return p;
 }
 struct Buffers {
@@ -411,6 +460,14 @@ bool launch_step(UpdateArgs u, bool last, int64_t batch, void *stream)
     return last ? launch(ns_update_kernel<Tl, TALL, true>, g, Tl::THREADS, stream, u)
                 : launch(ns_update_kernel<Tl, TALL, false>, g, Tl::THREADS, stream, u);
 }
+template <bool TALL>
+bool launch_step_class(Class c, const UpdateArgs &u, bool last, int64_t batch, void *stream)
+{
+    return c == C256   ? launch_step<T256, TALL>(u, last, batch, stream)
+           : c == C192 ? launch_step<T192, TALL>(u, last, batch, stream)
+           : c == C128 ? launch_step<T128, TALL>(u, last, batch, stream)
+                       : launch_step<T64, TALL>(u, last, batch, stream);
+}
 template <template <bool, bool> class T, bool SQUARE, bool TRANS>
 bool launch_sym(SymArgs a, int64_t batch, void *stream)
 {
@@ -423,6 +480,7 @@ template <bool SQUARE, bool TRANS>
 bool launch_sym_class(Class c, const SymArgs &a, int64_t batch, void *stream)
 {
     return c == C256   ? launch_sym<T256, SQUARE, TRANS>(a, batch, stream)
+           : c == C192 ? launch_sym<T192, SQUARE, TRANS>(a, batch, stream)
            : c == C128 ? launch_sym<T128, SQUARE, TRANS>(a, batch, stream)
                        : launch_sym<T64, SQUARE, TRANS>(a, batch, stream);
 }
@@ -465,15 +523,15 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         a.x_stride = rows * p.ldx;
         a.K = (int)(p.tall ? rows : round_up(cols, 8));
         a.s = (int)p.s, a.out = b.o, a.lds = p.lds, a.diag = b.d;
-        ok = p.tall ? launch_sym_class<false, true>(p.sym, a, batch, stream)
-                    : launch_sym_class<false, false>(p.sym, a, batch, stream);
+        ok = p.tall ? launch_sym_class<false, true>(p.gram, a, batch, stream)
+                    : launch_sym_class<false, false>(p.gram, a, batch, stream);
         SymArgs q = {};
         q.x = {b.o, p.lds, (int)p.s};
         q.x_stride = p.s * p.lds;
         q.K = (int)round_up(p.s, 8);
         q.s = (int)p.s, q.out = b.p, q.lds = p.lds, q.diag = b.e, q.o = b.o, q.d = b.d;
         q.b = k[1], q.c = k[2];
-        ok = ok && launch_sym_class<true, false>(p.sym, q, batch, stream);
+        ok = ok && launch_sym_class<true, false>(p.square, q, batch, stream);
         UpdateArgs u = {};
         const Operand x = {xh, p.ldx, (int)(p.tall ? rows : cols)}, pm = {b.p, p.lds, (int)p.s};
         u.l = p.tall ? x : pm, u.r = p.tall ? pm : x;
@@ -484,14 +542,8 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         u.out = out, u.ldo = ldo, u.o_stride = o_stride;
         u.vec = ldo % 8 == 0 && o_stride % 8 == 0 && (uintptr_t)out % 16 == 0;
         const bool last = t == steps - 1;
-        if (p.tall)
-            ok = ok && (p.upd == C256   ? launch_step<T256, true>(u, last, batch, stream)
-                        : p.upd == C128 ? launch_step<T128, true>(u, last, batch, stream)
-                                        : launch_step<T64, true>(u, last, batch, stream));
-        else
-            ok = ok && (p.upd == C256   ? launch_step<T256, false>(u, last, batch, stream)
-                        : p.upd == C128 ? launch_step<T128, false>(u, last, batch, stream)
-                                        : launch_step<T64, false>(u, last, batch, stream));
+        ok = ok && (p.tall ? launch_step_class<true>(p.upd, u, last, batch, stream)
+                           : launch_step_class<false>(p.upd, u, last, batch, stream));
     }
     return ok ? TG_OK : TG_ERR_LAUNCH;
 }
@@ -543,7 +595,7 @@ extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, 
         return st;
     const Plan p = make_plan(batch, rows, cols);
     if (name && name_len > 0)
-        snprintf(name, (size_t)name_len, "%s sym_%s update_%s", p.tall ? "tall" : "wide", CLASS_NAME[p.sym],
-                 CLASS_NAME[p.upd]);
+        snprintf(name, (size_t)name_len, "%s gram_%s square_%s update_%s", p.tall ? "tall" : "wide",
+                 CLASS_NAME[p.gram], CLASS_NAME[p.square], CLASS_NAME[p.upd]);
     return TG_OK;
 }

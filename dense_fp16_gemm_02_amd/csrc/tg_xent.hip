@@ -458,7 +458,7 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
             *reinterpret_cast<V4 *>(stg + stage_off<T::WTN>(16 * i + fr, 16 * j + fc)) = g;
         }
     }
-    store_block<E, T::WTM, T::WTN>(stg, reinterpret_cast<E *>(a.G), a.Gld, m0 + wm * T::WTM, n0 + wn * T::WTN, M,
+    store_block<E, T::WTM, T::WTN, true>(stg, reinterpret_cast<E *>(a.G), a.Gld, m0 + wm * T::WTM, n0 + wn * T::WTN, M,
                                    (int)a.Gld, true, nullptr, lane);
 }
 
@@ -510,17 +510,27 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     const int fr = lane & 15, fc = 4 * (lane >> 4);
     const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
     if constexpr (ACC) {
+        // a column of blocks ahead: the next one's sums are being loaded while
+        // one is added and stored
         float *out = a.acc + ((int64_t)z * a.acc_rows + r0 + fr) * a.K8 + c0 + fc;
+        f32x4 old[2][T::TM];
+        auto fetch = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < T::TM; ++i) {
-            if (r0 + 16 * i + fr < M) {
-#pragma unroll
-                for (int j = 0; j < T::TN; ++j)
-                    if (c0 + 16 * j + fc < a.K8) {
-                        f32x4 *p = reinterpret_cast<f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j);
-                        *p = a.add ? *p + acc[i][j] : acc[i][j];
-                    }
+            for (int i = 0; i < T::TM; ++i) {
+                old[j & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (a.add && r0 + 16 * i + fr < M && c0 + 16 * j + fc < a.K8)
+                    old[j & 1][i] = *reinterpret_cast<const f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j);
             }
+        };
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) {
+            if (j + 1 < T::TN)
+                fetch(j + 1);
+#pragma unroll
+            for (int i = 0; i < T::TM; ++i)
+                if (r0 + 16 * i + fr < M && c0 + 16 * j + fc < a.K8)
+                    *reinterpret_cast<f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j) = old[j & 1][i] + acc[i][j];
         }
         return;
     }
