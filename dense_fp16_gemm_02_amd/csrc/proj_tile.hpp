@@ -106,11 +106,14 @@ static_assert(256 * MAX_DMA_LD * 2 + 512 <= (int64_t)DMA_RANGE, "in-tile offsets
 #define PT_WAVES_PER_SIMD(n)
 #endif
 
-// 16 bytes per lane, buffer offset voff → LDS lds + 16·lane (lds wave-uniform)
+// 16 bytes per lane, buffer offset voff → LDS lds + 16·lane (lds wave-uniform).
+// CPOL: the instruction's cache policy, 0 cached, 3 (sc0 | nt) for an operand
+// that is read once and should not displace the other.
+template <int CPOL = 0>
 __device__ inline void dma16(__amdgpu_buffer_rsrc_t r, void *lds, uint32_t voff)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, voff, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, voff, 0, 0, CPOL);
 #else
     (void)r, (void)lds, (void)voff;
 #endif
@@ -271,8 +274,13 @@ struct Operand {
     int extent;
 };
 
-template <typename E, int BM_, int BN_, int WM_, int WN_, int S_, bool TA_, bool TB_>
+// STREAM: for a product bound by reading B (one tile row): B is loaded past the
+// caches, and the workgroups of the eight XCDs start at K-tiles spread over K and
+// wrap around, so that they read from different address ranges at any moment.
+template <typename E, int BM_, int BN_, int WM_, int WN_, int S_, bool TA_, bool TB_, bool STREAM_ = false>
 struct Tile {
+    static constexpr bool STREAM = STREAM_;
+    static_assert(!STREAM_ || (!TA_ && !TB_), "rotation is for the K-major product");
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
     static constexpr bool TA = TA_, TB = TB_;
     using V8 = typename El<E>::v8;
@@ -327,6 +335,7 @@ struct Tile {
         const int wm = wave / WN, wn = wave % WN;
         const int KT = (K + BK - 1) / BK;
         const int k0 = FIRST ? K - BK * KT : 0;
+        const int rot = STREAM ? (int)(blockIdx.x % NUM_XCD) * KT / NUM_XCD : 0;
 
         uint32_t a_off[PA], b_off[PB];
         dma_offsets<TA, BM>(a_off, a.ld, x0a, a.extent, lane, wave);
@@ -340,17 +349,30 @@ struct Tile {
         // with its last K row.  32-bit scalar arithmetic without branches: a
         // branch in the loop makes the register allocator move accumulators.
         auto rsrc = [&](const char *base, int64_t step, int64_t ld, int x0, bool trans, int t) {
+            int pt = t;  // K-tile in memory order
+            if constexpr (STREAM) {
+                pt += rot;
+                pt -= pt >= KT ? KT : 0;
+            }
             const int rows = imax(imin(K - t * BK, BK), 0);
             const int range = trans ? imax(rows * (2 * (int)ld) - 2 * x0, 0) : t < KT ? DMA_RANGE : 0;
-            return __builtin_amdgcn_make_buffer_rsrc((void *)(base + step * t), (short)0, range, BUFFER_WORD3);
+            return __builtin_amdgcn_make_buffer_rsrc((void *)(base + step * pt), (short)0, range, BUFFER_WORD3);
         };
         auto rsrc_a = [&](int t) { return rsrc(a_base, a_step, a.ld, x0a, TA, t); };
         auto rsrc_b = [&](int t) { return rsrc(b_base, b_step, b.ld, x0b, TB, t); };
-        auto dma_a = [&](__amdgpu_buffer_rsrc_t r, int stage, int p) {
-            dma16(r, a_ring + stage * STAGE_A + (p * NW + wave) * 512, a_off[p]);
+        // the first K-tile's columns below 0 read as zero; the passes' rows are
+        // NW·8 apart, so a lane's chunk is the same in all of them
+        const int kc = 8 * ((lane & 7) ^ kmajor_swz(8 * wave + (lane >> 3)));
+        static_assert(NW % 2 == 0, "swizzle repeats per pass");
+        auto below = [&](int t) {
+            const int pt = STREAM ? (t + rot >= KT ? t + rot - KT : t + rot) : t;
+            return FIRST && pt == 0 && k0 + kc < 0;
         };
-        auto dma_b = [&](__amdgpu_buffer_rsrc_t r, int stage, int p) {
-            dma16(r, b_ring + stage * STAGE_B + (p * NW + wave) * 512, b_off[p]);
+        auto dma_a = [&](__amdgpu_buffer_rsrc_t r, int stage, int p, bool zero) {
+            dma16(r, a_ring + stage * STAGE_A + (p * NW + wave) * 512, zero ? DMA_OOB : a_off[p]);
+        };
+        auto dma_b = [&](__amdgpu_buffer_rsrc_t r, int stage, int p, bool zero) {
+            dma16<STREAM ? 3 : 0>(r, b_ring + stage * STAGE_B + (p * NW + wave) * 512, zero ? DMA_OOB : b_off[p]);
         };
 
         // fragment reads
@@ -401,7 +423,7 @@ struct Tile {
         // fragment reads and the DMAs of operand `which` (1: A, 2: B), pinned
         // in program order so that they issue in the shadow of the MFMAs.
         auto step = [&](const V8 *fa, const V8 *fb, bool reads, int rsa, int rsb, int rkk, V8 *na, V8 *nb, int which,
-                        __amdgpu_buffer_rsrc_t r, int stage) {
+                        __amdgpu_buffer_rsrc_t r, int stage, bool zero) {
             constexpr int EA = SLOTS / PA > 0 ? SLOTS / PA : 1, EB = SLOTS / PB > 0 ? SLOTS / PB : 1;
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i) {
@@ -410,9 +432,9 @@ struct Tile {
                 if (reads && i % RSTRIDE == 0 && i / RSTRIDE < NFRAG)
                     read_frag(rsa, rsb, rkk, frag_of_slot(i / RSTRIDE), na, nb);
                 if (which == 1 && i % EA == EA / 4 && i / EA < PA)
-                    dma_a(r, stage, i / EA);
+                    dma_a(r, stage, i / EA, zero);
                 if (which == 2 && i % EB == EB / 4 && i / EB < PB)
-                    dma_b(r, stage, i / EB);
+                    dma_b(r, stage, i / EB, zero);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -422,29 +444,24 @@ struct Tile {
             if (which == 1)
 #pragma unroll
                 for (int p = (SLOTS + EA - 1) / EA; p < PA; ++p)
-                    dma_a(r, stage, p);
+                    dma_a(r, stage, p, zero);
             if (which == 2)
 #pragma unroll
                 for (int p = (SLOTS + EB - 1) / EB; p < PB; ++p)
-                    dma_b(r, stage, p);
+                    dma_b(r, stage, p, zero);
         };
 
-        // prologue: K-tiles 0 .. S-1; K-tile 0's columns below 0 read as zero
+        // prologue: K-tiles 0 .. S-1
 #pragma unroll
         for (int t = 0; t < S; ++t) {
             const auto ra = rsrc_a(t), rb = rsrc_b(t);
+            const bool zero = (STREAM || t == 0) && below(t);
 #pragma unroll
-            for (int p = 0; p < PA; ++p) {
-                const int kc = (lane & 7) ^ kmajor_swz(8 * (p * NW + wave) + (lane >> 3));
-                const bool below = FIRST && t == 0 && k0 + 8 * kc < 0;
-                dma16(ra, a_ring + t * STAGE_A + (p * NW + wave) * 512, below ? DMA_OOB : a_off[p]);
-            }
+            for (int p = 0; p < PA; ++p)
+                dma_a(ra, t, p, zero);
 #pragma unroll
-            for (int p = 0; p < PB; ++p) {
-                const int kc = (lane & 7) ^ kmajor_swz(8 * (p * NW + wave) + (lane >> 3));
-                const bool below = FIRST && t == 0 && k0 + 8 * kc < 0;
-                dma16(rb, b_ring + t * STAGE_B + (p * NW + wave) * 512, below ? DMA_OOB : b_off[p]);
-            }
+            for (int p = 0; p < PB; ++p)
+                dma_b(rb, t, p, zero);
         }
         wait_vmem<(S - 1) * (PA + PB)>();
         barrier_lds();
@@ -462,11 +479,13 @@ struct Tile {
         int sa = 0, sb = 0;       // stages of K-tile t
         int da = S % (S + 1);     // stage A(t+S) goes into
         for (int t = 0; t < (PEEL ? KT - 1 : KT); ++t) {
-            step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 1, rsrc_a(t + S), da);
+            step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 1, rsrc_a(t + S), da,
+                 STREAM && below(t + S));
             wait_vmem<(S - 2) * (PA + PB) + PA>();  // K-tile t+1 has landed (this wave's part)
             barrier_lds();                          // ... for every wave; K-tile t's stages are drained
             const int sa1 = sa == S ? 0 : sa + 1, sb1 = sb == S - 1 ? 0 : sb + 1;
-            step(fa[1], fb[1], true, sa1, sb1, 0, fa[0], fb[0], 2, rsrc_b(t + S), sb);
+            step(fa[1], fb[1], true, sa1, sb1, 0, fa[0], fb[0], 2, rsrc_b(t + S), sb,
+                 STREAM && below(t + S));
             da = da == S ? 0 : da + 1;
             sa = sa1;
             sb = sb1;
@@ -474,8 +493,8 @@ struct Tile {
         ahead();
         if constexpr (PEEL) {
             const auto none = __builtin_amdgcn_make_buffer_rsrc(nullptr, (short)0, 0, BUFFER_WORD3);
-            step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 0, none, 0);
-            step(fa[1], fb[1], false, 0, 0, 0, fa[0], fb[0], 0, none, 0);
+            step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 0, none, 0, false);
+            step(fa[1], fb[1], false, 0, 0, 0, fa[0], fb[0], 0, none, 0, false);
         }
         // (the accumulators stay where they are between the loop and the
         // epilogue: without this some instantiations spilled a few of them)

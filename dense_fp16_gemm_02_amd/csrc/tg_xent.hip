@@ -1,9 +1,9 @@
 // tg_xent.hip — softmax cross entropy of the vocabulary projection and its
 // gradients.  See include/tg_xent.h for the contract.
 //
-// Forward: the logits tile z = H·Wᵀ stays in the accumulators; per row and
-// per wave column strip the kernel keeps only the running maximum m and
-// s = Σ exp(z − m), so M·V logits shrink to M·(V/strip) pairs.  Two pairs join as
+// Forward: the logits tile z = H·Wᵀ stays in the accumulators; per row of a tile
+// the kernel keeps only the maximum m and s = Σ exp(z − m), so M·V logits
+// shrink to M·(V/256) pairs.  Two pairs join as
 // m = max(m1, m2), s = s1·exp(m1 − m) + s2·exp(m2 − m); a second kernel joins a
 // row's pairs and subtracts the target's logit, which the one lane that held
 // it has written out.
@@ -31,10 +31,11 @@ using namespace pt;
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 
-// What the index kernel finds out, at the start of a workspace.
+// What the first kernel finds out, at the start of a workspace.
 struct Head {
-    int live;     // tokens not ignored
-    float alpha;  // what G was divided by (backward)
+    int live;          // tokens not ignored
+    float alpha;       // what G was divided by (backward)
+    unsigned arrived;  // workgroups of the join that are done (forward)
 };
 
 // G is stored in the operands' type; binary16 stores it times 2^14, bfloat16 as
@@ -48,155 +49,172 @@ constexpr float g_scale()
 // exp through the hardware's base-2 exponential (1 ulp)
 __device__ inline float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
 
-// ------------------------------------------------------------ index, gather
-// One workgroup: numbers the live tokens, and for the backward pass their
-// coefficients.  A few microseconds at 8192 tokens; it reads 8·M bytes.
-struct IndexArgs {
+// ------------------------------------------------------------------ gather
+// Numbers the live tokens and copies their rows of H to consecutive rows, K
+// columns padded with zeros to K8; for the backward pass also each live token's
+// coefficients, and zeros for the ignored tokens' rows of dH.  A workgroup has
+// PREP_ROWS tokens at most and counts the live ones before them itself (8·M
+// bytes from the caches): one launch, no pass over the targets in between.
+constexpr int PREP_THREADS = 256, PREP_ROWS = 256;
+struct PrepArgs {
     const int64_t *target;
     int64_t M, V, ignore;
+    int rows;        // tokens per workgroup
     Head *head;
     int *map;        // live row -> token
     int *col;        // live row -> target, -1 if out of range
     float *loss;     // per-token loss and lse: zeroed for ignored tokens
     float *lse_out;
+    const uint16_t *H;
+    int64_t ldh;
+    uint16_t *hc;
+    int64_t K, K8;
+    bool vec;        // 16-byte aligned rows of H, K % 8 == 0
     // backward
     int reduction;
     const float *dloss, *dlse, *lse;
     float *lse_c, *cp, *ct;  // per live row: lse, and the coefficients of the softmax and of the target
+    uint16_t *dH;
+    int64_t lddh;
 };
-constexpr int INDEX_THREADS = 1024;
-template <bool BWD>
-__global__ __launch_bounds__(INDEX_THREADS) void xent_index_kernel(IndexArgs a)
+__device__ inline uint4 load8(const uint16_t *s, int64_t c, int64_t K, bool vec)
 {
-    __shared__ int wave_count[16];
-    __shared__ float wave_max[16];
+    if (vec)
+        return *reinterpret_cast<const uint4 *>(s + c);
+    union {
+        uint4 u;
+        uint16_t h[8];
+    } w;
+    w.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e < K)
+            w.h[e] = s[c + e];
+    return w.u;
+}
+template <typename X>
+__device__ inline X wave_sum(X x)
+{
+    for (int o = 32; o; o >>= 1)
+        x += __shfl_xor(x, o);
+    return x;
+}
+template <bool BWD>
+__global__ __launch_bounds__(PREP_THREADS) void xent_prep_kernel(PrepArgs a)
+{
+    constexpr int WAVES = PREP_THREADS / 64;
+    __shared__ int before_w[WAVES], all_w[WAVES];
+    __shared__ float top_w[WAVES];
+    __shared__ int place[PREP_ROWS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    auto live_at = [&](int64_t i) { return i < a.M && a.target[i] != a.ignore; };
+    const int64_t r0 = (int64_t)blockIdx.x * a.rows;
+    const int rows = (int)(a.M - r0 < a.rows ? a.M - r0 : a.rows);
+    int before = 0, all = 0;
+#pragma unroll 8
+    for (int64_t i = tid; i < a.M; i += PREP_THREADS) {
+        const int live = a.target[i] != a.ignore;
+        all += live;
+        before += i < r0 ? live : 0;
+    }
+    before = wave_sum(before), all = wave_sum(all);
+    if (lane == 0)
+        before_w[wave] = before, all_w[wave] = all;
+    __syncthreads();
+    before = all = 0;
+    for (int w = 0; w < WAVES; ++w)
+        before += before_w[w], all += all_w[w];
     float scale = 1.0f, top = 0.0f;
     if constexpr (BWD) {
-        if (a.reduction == TG_XENT_MEAN) {
-            int n = 0;
-            for (int64_t i = tid; i < a.M; i += INDEX_THREADS)
-                n += live_at(i);
-            for (int o = 32; o; o >>= 1)
-                n += __shfl_xor(n, o);
-            if (lane == 0)
-                wave_count[wave] = n;
-            __syncthreads();
-            n = 0;
-            for (int w = 0; w < 16; ++w)
-                n += wave_count[w];
-            __syncthreads();
-            scale = 1.0f / (float)imax(n, 1);
-        }
+        if (a.reduction == TG_XENT_MEAN)
+            scale = 1.0f / (float)imax(all, 1);
         // the largest coefficient (a NaN among them reaches its own row through
         // its coefficient, not through the maximum)
-        for (int64_t i = tid; i < a.M; i += INDEX_THREADS)
-            if (live_at(i)) {
-                const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
-                top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[i]) : 0.0f));
-            }
-        for (int o = 32; o; o >>= 1)
-            top = fmaxf(top, __shfl_xor(top, o));
-        if (lane == 0)
-            wave_max[wave] = top;
-        __syncthreads();
-        top = 0.0f;
-        for (int w = 0; w < 16; ++w)
-            top = fmaxf(top, wave_max[w]);
+        if (a.reduction != TG_XENT_NONE && !a.dlse) {
+            top = fabsf(a.dloss[0] * scale);
+        } else {
+            for (int64_t i = tid; i < a.M; i += PREP_THREADS)
+                if (a.target[i] != a.ignore) {
+                    const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
+                    top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[i]) : 0.0f));
+                }
+            for (int o = 32; o; o >>= 1)
+                top = fmaxf(top, __shfl_xor(top, o));
+            if (lane == 0)
+                top_w[wave] = top;
+            __syncthreads();
+            for (int w = 0; w < WAVES; ++w)
+                top = fmaxf(top, top_w[w]);
+        }
         if (!(top > 0.0f))
             top = 1.0f;
     }
-    int base = 0;
-    for (int64_t i0 = 0; i0 < a.M; i0 += INDEX_THREADS) {
-        const int64_t i = i0 + tid;
-        const bool live = live_at(i);
-        const unsigned long long votes = __ballot(live);
-        if (lane == 0)
-            wave_count[wave] = __popcll(votes);
-        __syncthreads();
-        int at = base, all = 0;
-        for (int w = 0; w < 16; ++w) {
-            at += w < wave ? wave_count[w] : 0;
-            all += wave_count[w];
-        }
-        at += __popcll(votes & ((1ull << lane) - 1));
-        __syncthreads();
-        base += all;
-        if (live) {
-            const int64_t t = a.target[i];
-            const bool in = t >= 0 && t < a.V;
-            a.map[at] = (int)i;
-            a.col[at] = in ? (int)t : -1;
-            if constexpr (BWD) {
-                const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
-                const float l = a.dlse ? a.dlse[i] : 0.0f;
-                a.lse_c[at] = a.lse[i];
-                a.cp[at] = in ? (g + l) / top : NAN;
-                a.ct[at] = g / top;
-            }
-        } else if (i < a.M) {
-            if constexpr (!BWD) {
+    if (blockIdx.x == 0 && tid == 0) {
+        a.head->live = all;
+        a.head->alpha = top;
+    }
+    // this workgroup's tokens, 64 at a time by the first wave
+    if (wave == 0)
+        for (int c = 0; c < rows; c += 64) {
+            const int64_t i = r0 + c + lane;
+            const int64_t t = c + lane < rows ? a.target[i] : a.ignore;
+            const bool live = c + lane < rows && t != a.ignore;
+            const unsigned long long votes = __ballot(live);
+            const int at = before + __popcll(votes & ((1ull << lane) - 1));
+            before += __popcll(votes);
+            if (c + lane >= rows)
+                continue;
+            place[c + lane] = live ? at : -1;
+            if (live) {
+                const bool in = t >= 0 && t < a.V;
+                a.map[at] = (int)i;
+                a.col[at] = in ? (int)t : -1;
+                if constexpr (BWD) {
+                    const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
+                    a.lse_c[at] = a.lse[i];
+                    a.cp[at] = in ? (g + (a.dlse ? a.dlse[i] : 0.0f)) / top : NAN;
+                    a.ct[at] = g / top;
+                }
+            } else if constexpr (!BWD) {
                 if (a.loss)
                     a.loss[i] = 0.0f;
                 if (a.lse_out)
                     a.lse_out[i] = 0.0f;
             }
         }
-    }
-    if (tid == 0) {
-        a.head->live = base;
-        a.head->alpha = top;
+    __syncthreads();
+    const int per = (int)(a.K8 / 8);
+    for (int r = wave; r < rows; r += WAVES) {
+        const int at = place[r];
+        if (at >= 0) {
+            const uint16_t *src = a.H + (r0 + r) * a.ldh;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.hc + at * a.K8);
+#pragma unroll 4
+            for (int c = lane; c < per; c += 64)
+                dst[c] = load8(src, 8 * (int64_t)c, a.K, a.vec);
+        } else if (BWD && a.dH) {
+            uint16_t *dst = a.dH + (r0 + r) * a.lddh;
+            for (int64_t c = lane; c < a.K; c += 64)
+                dst[c] = 0;
+        }
     }
 }
 
-// Rows map[0 .. *live) of src (all of the first `rows` where map is null) to
-// consecutive rows of dst, K columns padded with zeros to K8 (a multiple of
-// 8).  Rows of `zero` (dH) whose token is ignored are cleared: zero_target.
-struct GatherArgs {
-    const void *src;
-    int64_t ld;
-    void *dst;
-    int64_t rows, K, K8;
-    const int *map;
-    const Head *head;
-    bool vec;  // 16-byte aligned source rows, K % 8 == 0
-};
-__global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs a)
+// Rows of W padded with zeros to K8 columns (W whose rows are not aligned).
+__global__ __launch_bounds__(256) void xent_pack_kernel(const uint16_t *src, int64_t ld, uint16_t *dst, int64_t rows,
+                                                        int64_t K, int64_t K8)
 {
-    const int64_t rows = a.map ? a.head->live : a.rows;
-    const int64_t per = a.K8 / 8, total = rows * per;
-    const uint16_t *src = reinterpret_cast<const uint16_t *>(a.src);
-    uint16_t *dst = reinterpret_cast<uint16_t *>(a.dst);
+    const int64_t per = K8 / 8, total = rows * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per, c = (i - r * per) * 8;
-        const uint16_t *s = src + (a.map ? (int64_t)a.map[r] : r) * a.ld + c;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (a.vec) {
-            v = *reinterpret_cast<const uint4 *>(s);
-        } else {
-            union {
-                uint4 u;
-                uint16_t h[8];
-            } w;
-            w.u = v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < a.K)
-                    w.h[e] = s[e];
-            v = w.u;
-        }
-        *reinterpret_cast<uint4 *>(dst + r * a.K8 + c) = v;
+        *reinterpret_cast<uint4 *>(dst + r * K8 + c) = load8(src + r * ld, c, K, false);
     }
 }
-// dH rows of ignored tokens, or a whole matrix (target null), set to zero
-__global__ __launch_bounds__(256) void xent_zero_kernel(uint16_t *dst, int64_t ld, int64_t rows, int64_t cols,
-                                                        const int64_t *target, int64_t ignore)
+// dW, and the total, of no tokens
+__global__ __launch_bounds__(256) void xent_zero_kernel(uint16_t *dst, int64_t ld, int64_t rows, int64_t cols)
 {
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        if (!target || target[r] == ignore)
-            for (int64_t c = threadIdx.x; c < cols; c += 256)
-                dst[r * ld + c] = 0;
+        for (int64_t c = threadIdx.x; c < cols; c += 256)
+            dst[r * ld + c] = 0;
 }
 
 // ---------------------------------------------------------- logits, forward
@@ -211,11 +229,20 @@ struct StatsArgs {
     const int *col;     // live row -> target (compacted rows)
     const int64_t *target;
     int64_t Vall;
-    float2 *part;       // [strip][row]
+    float2 *part;       // [column of tiles][row]
     int64_t part_ld;
     float *at_target;   // row -> logit of its target
+    unsigned *arrived;  // for the join
     int tiles_n;
 };
+__device__ inline void join(float2 &a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    const float from = m == -INFINITY ? 0.0f : m;
+    // a NaN in either sum stays one
+    a.y = a.y * fast_exp(a.x - from) + b.y * fast_exp(b.x - from);
+    a.x = m;
+}
 template <typename E, typename T>
 __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void xent_stats_kernel(
     StatsArgs a)
@@ -223,6 +250,8 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
     const int M = a.head ? a.head->live : a.M;
     const int tiles_m = (M + T::BM - 1) / T::BM, total = tiles_m * a.tiles_n;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *a.arrived = 0;
     if ((int)blockIdx.x >= total)
         return;
     int tm, tn;
@@ -239,8 +268,9 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     const int wm = wave / T::WN, wn = wave % T::WN;
     const int row0 = m0 + wm * T::WTM + (lane & 15);
     const int col0 = n0 + wn * T::WTN + 4 * (lane >> 4);
-    float2 *part = a.part + (int64_t)(a.v0 / T::WTN + tn * T::WN + wn) * a.part_ld;
     const bool whole = n0 + wn * T::WTN + T::WTN <= a.V;
+    barrier_lds();
+    float2 *pairs = reinterpret_cast<float2 *>(smem);  // [WN][BM]
 #pragma unroll
     for (int i = 0; i < T::TM; ++i) {
         const int row = row0 + 16 * i;
@@ -282,113 +312,125 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
                 s += fast_exp(acc[i][j][v] - from);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        if (lane < 16 && row < M)
-            part[row] = make_float2(m, s);
+        if (lane < 16)
+            pairs[wn * T::BM + wm * T::WTM + 16 * i + lane] = make_float2(m, s);
+    }
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r < T::BM && m0 + r < M) {
+        float2 p = pairs[r];
+#pragma unroll
+        for (int w = 1; w < T::WN; ++w)
+            join(p, pairs[w * T::BM + r]);
+        a.part[(int64_t)(a.v0 / T::BN + tn) * a.part_ld + m0 + r] = p;
     }
 }
 
-// Joins each row's pairs: 64 rows per workgroup, 16 waves taking every 16th
-// strip.  Reads 8·strips·M bytes, coalesced along rows.
+// Joins each row's pairs: 16 rows per workgroup, 64 threads to a row, which take
+// every 64th tile.  Reads 8·M bytes per column of tiles, 128 at a time.  For SUM and MEAN each workgroup
+// leaves its own sum, and the one that arrives last adds them all, in their
+// order: which one that is changes nothing in the result.
+constexpr int JOIN_ROWS = 16;
 struct JoinArgs {
     const float2 *part;
     int64_t part_ld;
-    int strips, M, reduction;
+    int tiles, M, reduction;  // tiles: columns of tiles, the pairs of a row
     const Head *head;
     const int *map, *col;
     const int64_t *target;
     int64_t V, ignore;
     const float *at_target;
     float *loss, *lse;   // per token (loss null unless TG_XENT_NONE)
-    float2 *block_sum;   // per workgroup: sum of losses, tokens counted
-    float *total;        // SUM, MEAN with one workgroup
+    float2 *block_sum;   // per workgroup: sum of losses, tokens counted (null for NONE)
+    unsigned *arrived;   // set to 0 by the kernel before
+    float *total;
 };
-__device__ inline void join(float2 &a, float2 b)
-{
-    const float m = fmaxf(a.x, b.x);
-    const float from = m == -INFINITY ? 0.0f : m;
-    // a NaN in either sum stays one
-    a.y = a.y * fast_exp(a.x - from) + b.y * fast_exp(b.x - from);
-    a.x = m;
-}
 __device__ inline float reduced(float sum, float count, int reduction)
 {
     return reduction == TG_XENT_MEAN ? sum / fmaxf(count, 1.0f) : sum;
 }
 __global__ __launch_bounds__(1024) void xent_join_kernel(JoinArgs a)
 {
-    __shared__ float2 sh[16][64];
+    constexpr int ROWS = JOIN_ROWS, PER_ROW = 1024 / ROWS;
+    __shared__ float2 sh[PER_ROW][ROWS];
+    __shared__ bool last;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int M = a.head ? a.head->live : a.M;
-    const int row = blockIdx.x * 64 + lane;
+    const int row = blockIdx.x * ROWS + threadIdx.x % ROWS;
     float2 p = make_float2(-INFINITY, 0.0f);
     if (row < M)
-        for (int s = wave; s < a.strips; s += 16)
+#pragma unroll 4
+        for (int s = threadIdx.x / ROWS; s < a.tiles; s += PER_ROW)
             join(p, a.part[(int64_t)s * a.part_ld + row]);
-    sh[wave][lane] = p;
+    sh[threadIdx.x / ROWS][threadIdx.x % ROWS] = p;
     __syncthreads();
-    if (wave)
-        return;
+    if (wave == 0) {
+        // four lanes to a row, then across them (a fixed order)
+        p = sh[lane / ROWS][lane % ROWS];
 #pragma unroll
-    for (int w = 1; w < 16; ++w)
-        join(p, sh[w][lane]);
-    float loss = 0.0f, count = 0.0f;
-    if (row < M) {
-        float lse = p.x + LN2 * __builtin_amdgcn_logf(p.y);
-        bool live = true, in;
-        if (a.col) {
-            in = a.col[row] >= 0;
-        } else {
-            const int64_t t = a.target[row];
-            live = t != a.ignore;
-            in = t >= 0 && t < a.V;
+        for (int w = 64 / ROWS; w < PER_ROW; w += 64 / ROWS)
+            join(p, sh[w + lane / ROWS][lane % ROWS]);
+#pragma unroll
+        for (int o = ROWS; o < 64; o *= 2) {
+            const float2 q = make_float2(__shfl_xor(p.x, o), __shfl_xor(p.y, o));
+            join(p, q);
         }
-        const int out = a.map ? a.map[row] : row;
-        if (live) {
-            loss = in ? lse - a.at_target[row] : NAN;
-            count = 1.0f;
-        } else {
-            lse = 0.0f;
+        float loss = 0.0f, count = 0.0f;
+        if (row < M && lane < ROWS) {
+            float lse = p.x + LN2 * __builtin_amdgcn_logf(p.y);
+            bool live = true, in;
+            if (a.col) {
+                in = a.col[row] >= 0;
+            } else {
+                const int64_t t = a.target[row];
+                live = t != a.ignore;
+                in = t >= 0 && t < a.V;
+            }
+            const int out = a.map ? a.map[row] : row;
+            if (live) {
+                loss = in ? lse - a.at_target[row] : NAN;
+                count = 1.0f;
+            } else {
+                lse = 0.0f;
+            }
+            if (a.lse)
+                a.lse[out] = lse;
+            if (a.loss)
+                a.loss[out] = loss;
         }
-        if (a.lse)
-            a.lse[out] = lse;
-        if (a.loss)
-            a.loss[out] = loss;
+        if (a.block_sum) {
+            loss = wave_sum(loss), count = wave_sum(count);
+            if (lane == 0) {
+                // the sum is out before the arrival is: release at device scope
+                float2 *b = a.block_sum + blockIdx.x;
+                __hip_atomic_store(&b->x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(&b->y, count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                       gridDim.x - 1;
+            }
+        }
     }
-    if (a.block_sum) {
-        for (int o = 32; o; o >>= 1) {
-            loss += __shfl_xor(loss, o);
-            count += __shfl_xor(count, o);
-        }
-        if (lane == 0) {
-            if (a.total)
-                a.total[0] = reduced(loss, count, a.reduction);
-            else
-                a.block_sum[blockIdx.x] = make_float2(loss, count);
-        }
-    }
-}
-__global__ __launch_bounds__(1024) void xent_total_kernel(const float2 *block_sum, int blocks, int reduction,
-                                                          float *total)
-{
-    __shared__ float2 sh[16];
+    if (!a.block_sum)
+        return;
+    __syncthreads();
+    if (!last)
+        return;
+    __syncthreads();
     float2 s = make_float2(0.0f, 0.0f);
-    for (int i = threadIdx.x; i < blocks; i += 1024) {
-        s.x += block_sum[i].x;
-        s.y += block_sum[i].y;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += 1024) {
+        s.x += __hip_atomic_load(&a.block_sum[i].x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s.y += __hip_atomic_load(&a.block_sum[i].y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    for (int o = 32; o; o >>= 1) {
-        s.x += __shfl_xor(s.x, o);
-        s.y += __shfl_xor(s.y, o);
-    }
-    if ((threadIdx.x & 63) == 0)
-        sh[threadIdx.x >> 6] = s;
+    s.x = wave_sum(s.x), s.y = wave_sum(s.y);
+    if (lane == 0)
+        sh[wave][0] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 16; ++w) {
-            s.x += sh[w].x;
-            s.y += sh[w].y;
+            s.x += sh[w][0].x;
+            s.y += sh[w][0].y;
         }
-        total[0] = reduced(s.x, s.y, reduction);
+        a.total[0] = reduced(s.x, s.y, a.reduction);
     }
 }
 
@@ -463,31 +505,41 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 }
 
 // ------------------------------------------------------------ dH (+)= G·W
-// A: G, K-major; B: W of the piece, transposed.  With `acc` the product goes
-// to fp32 sums (one per split of the contraction, added to what earlier
-// pieces left), otherwise it is scaled, rounded and scattered to dH.
+// A: G, K-major; B: W of the piece, transposed.  dH has live·K outputs and a
+// contraction over the whole vocabulary: fp32 sums, added to what earlier
+// pieces left, and where the tiles are few the contraction is split, each split
+// with sums of its own.  How many splits is decided here, from the number of
+// live tokens, which the host does not know; the last kernel joins them.
 struct DhArgs {
     Operand g, w;
-    int V, split;       // contraction length, and how much of it a split takes
+    int V;              // contraction length
     const Head *head;
-    float *acc;         // [splits][M][K8]
-    int64_t acc_rows, K8;
+    float *acc;         // [splits][live][K8], room for `room` rows
+    int64_t room, K8;
     bool add;
     const int *map;
     void *dH;
     int64_t lddh;
     int K;
     bool vec;
-    int tiles_n, splits;
+    int bm, tiles_n, slots, piece;  // tile rows, columns of tiles, workgroups to fill, vocabulary per piece
 };
-template <typename E, typename T, bool ACC>
+// Splits of the contraction: as many as fill the slots and the room, each of at
+// least 8 K-tiles (the same for every piece).
+__device__ inline int dh_splits(const DhArgs &a, int live)
+{
+    const int t = imax((live + a.bm - 1) / a.bm * a.tiles_n, 1);
+    const int64_t room = a.room / imax(live, 1);
+    return imax(imin(imin(a.slots / t, (int)(room < 1024 ? room : 1024)), a.piece / (8 * BK)), 1);
+}
+template <typename E, typename T>
 __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void xent_dh_kernel(
     DhArgs a)
 {
-    using V4 = typename El<E>::v4;
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
     const int M = a.head->live;
-    const int tiles_m = (M + T::BM - 1) / T::BM, tiles = tiles_m * a.tiles_n, total = tiles * a.splits;
+    const int splits = dh_splits(a, M);
+    const int tiles_m = (M + T::BM - 1) / T::BM, tiles = tiles_m * a.tiles_n, total = tiles * splits;
     if ((int)blockIdx.x >= total)
         return;
     const int logical = xcd_contiguous(blockIdx.x, total);
@@ -495,7 +547,8 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     int tm, tn;
     grouped_tile<4>(logical - z * tiles, tiles_m, a.tiles_n, tm, tn);
     const int m0 = tm * T::BM, n0 = tn * T::BN;
-    const int from = z * a.split, len = imax(imin(a.split, a.V - from), 0);
+    const int split = (a.piece + splits * BK - 1) / (splits * BK) * BK;
+    const int from = z * split, len = imax(imin(split, a.V - from), 0);
     f32x4 acc[T::TM][T::TN];
     T::clear(acc);
     Operand g = a.g, w = a.w;
@@ -509,57 +562,44 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     const int wm = wave / T::WN, wn = wave % T::WN;
     const int fr = lane & 15, fc = 4 * (lane >> 4);
     const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
-    if constexpr (ACC) {
-        // a column of blocks ahead: the next one's sums are being loaded while
-        // one is added and stored
-        float *out = a.acc + ((int64_t)z * a.acc_rows + r0 + fr) * a.K8 + c0 + fc;
-        f32x4 old[2][T::TM];
-        auto fetch = [&](int j) __attribute__((always_inline)) {
+    // three columns of blocks ahead: their sums are being loaded while one is
+    // added and stored
+    constexpr int DEPTH = 4;
+    float *out = a.acc + ((int64_t)z * M + r0 + fr) * a.K8 + c0 + fc;
+    f32x4 old[DEPTH][T::TM];
+    auto fetch = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < T::TM; ++i) {
-                old[j & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                if (a.add && r0 + 16 * i + fr < M && c0 + 16 * j + fc < a.K8)
-                    old[j & 1][i] = *reinterpret_cast<const f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j);
-            }
-        };
-        fetch(0);
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-            if (j + 1 < T::TN)
-                fetch(j + 1);
-#pragma unroll
-            for (int i = 0; i < T::TM; ++i)
-                if (r0 + 16 * i + fr < M && c0 + 16 * j + fc < a.K8)
-                    *reinterpret_cast<f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j) = old[j & 1][i] + acc[i][j];
+        for (int i = 0; i < T::TM; ++i) {
+            old[j % DEPTH][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (a.add && r0 + 16 * i + fr < M && c0 + 16 * j + fc < a.K8)
+                old[j % DEPTH][i] = *reinterpret_cast<const f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j);
         }
-        return;
+    };
+#pragma unroll
+    for (int j = 0; j < DEPTH - 1 && j < T::TN; ++j)
+        fetch(j);
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) {
+        if (j + DEPTH - 1 < T::TN)
+            fetch(j + DEPTH - 1);
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+            if (r0 + 16 * i + fr < M && c0 + 16 * j + fc < a.K8)
+                *reinterpret_cast<f32x4 *>(out + (int64_t)(16 * i) * a.K8 + 16 * j) = old[j % DEPTH][i] + acc[i][j];
     }
-    const float alpha = a.head->alpha / g_scale<E>();
-    barrier_lds();
-    E *stg = smem + wave * T::WTM * T::WTN;
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-            V4 d;
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                d[v] = (E)(acc[i][j][v] * alpha);
-            *reinterpret_cast<V4 *>(stg + stage_off<T::WTN>(16 * i + fr, 16 * j + fc)) = d;
-        }
-    store_block<E, T::WTM, T::WTN>(stg, reinterpret_cast<E *>(a.dH), a.lddh, r0, c0, M, a.K, a.vec, a.map, lane);
 }
 // The splits' sums, in order, scaled, rounded and scattered.
 template <typename E>
 __global__ __launch_bounds__(256) void xent_dh_finish_kernel(DhArgs a)
 {
     const int64_t live = a.head->live, per = a.K8 / 4, total = live * per;
+    const int splits = dh_splits(a, (int)live);
     const float alpha = a.head->alpha / g_scale<E>();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per, c = (i - r * per) * 4;
         f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int z = 0; z < a.splits; ++z)
-            s += *reinterpret_cast<const f32x4 *>(a.acc + ((int64_t)z * a.acc_rows + r) * a.K8 + c);
+        for (int z = 0; z < splits; ++z)
+            s += *reinterpret_cast<const f32x4 *>(a.acc + (z * live + r) * a.K8 + c);
         E *dst = reinterpret_cast<E *>(a.dH) + (int64_t)a.map[r] * a.lddh + c;
         typename El<E>::v4 d;
 #pragma unroll
@@ -620,31 +660,46 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 }
 
 // ------------------------------------------------------------------- plans
-// Tile classes.  256×256 (one workgroup per CU) from 5/8 of the CUs on;
-// 128×128 (two per CU) below; 64×64 where even those are few; 64×128 for at
-// most 64 tokens, so that W is read once.
-enum Class { C256, C128, C64, C64X128 };
-const char *const CLASS_NAME[] = {"256x256", "128x128", "64x64", "64x128"};
-constexpr int CLASS_BM[] = {256, 128, 64, 64}, CLASS_BN[] = {256, 128, 64, 128};
-template <typename E, bool TA, bool TB>
-using T256 = Tile<E, 256, 256, 2, 2, 2, TA, TB>;
-template <typename E, bool TA, bool TB>
-using T128 = Tile<E, 128, 128, 2, 2, 2, TA, TB>;
-template <typename E, bool TA, bool TB>
-using T64 = Tile<E, 64, 64, 2, 2, 3, TA, TB>;
-template <typename E, bool TA, bool TB>
-using T64x128 = Tile<E, 64, 128, 1, 4, 3, TA, TB>;
-
-int64_t tiles(Class c, int64_t m, int64_t n) { return cdiv(m, CLASS_BM[c]) * cdiv(n, CLASS_BN[c]); }
-Class logits_class(int64_t M, int64_t V)
+// Tile classes: one workgroup per CU at 256×256 and 192×192, two of the smaller
+// ones; 64×128 for at most 64 tokens, so that W is read once.
+enum Class { C256, C192, C128, C64, C64X128, CLASSES };
+const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x128"};
+constexpr TileClass CLASS[] = {{256, 256, 1, 1.50, 1.50, 16.0},
+                               {192, 192, 1, 1.15, 1.15, 9.0},
+                               {128, 128, 2, 1.10, 0.50, 6.0},
+                               {64, 64, 2, 0.50, 0.27, 4.0},
+                               {64, 128, 2, 0.80, 0.45, 5.0}};
+template <typename E, bool TA, bool TB, typename F>
+bool with_tile(Class c, F f)
 {
-    if (M <= 64)
-        return tiles(C64X128, M, V) >= NUM_CU / 4 ? C64X128 : C64;
-    return tiles(C256, M, V) >= 160 ? C256 : tiles(C128, M, V) >= 80 ? C128 : C64;
+    switch (c) {
+    case C256:
+        return f(Tile<E, 256, 256, 2, 2, 2, TA, TB>{});
+    case C192:
+        return f(Tile<E, 192, 192, 2, 2, 2, TA, TB>{});
+    case C128:
+        return f(Tile<E, 128, 128, 2, 2, 2, TA, TB>{});
+    case C64X128:
+        if constexpr (!TA)
+            return f(Tile<E, 64, 128, 1, 4, 3, TA, TB, !TB>{});
+        [[fallthrough]];
+    default:
+        return f(Tile<E, 64, 64, 2, 2, 3, TA, TB>{});
+    }
 }
-// strip width (columns per pair) of the logits tiles
-int strip_of(Class c) { return c == C256 ? 128 : c == C128 ? 64 : 32; }
-
+int64_t tiles(Class c, int64_t m, int64_t n) { return cdiv(m, CLASS[c].bm) * cdiv(n, CLASS[c].bn); }
+Class best_class(int64_t m, int64_t n, int64_t k)
+{
+    int c = 0;
+    for (int i = 1; i < C64X128; ++i)
+        if (tile_time(CLASS[i], tiles((Class)i, m, n), cdiv(k, BK)) < tile_time(CLASS[c], tiles((Class)c, m, n), cdiv(k, BK)))
+            c = i;
+    return (Class)c;
+}
+Class logits_class(int64_t M, int64_t V, int64_t K)
+{
+    return M <= 64 && tiles(C64X128, M, V) >= NUM_CU / 4 ? C64X128 : best_class(M, V, K);
+}
 constexpr int64_t G_BYTES = (int64_t)512 << 20;  // of G at a time
 constexpr int64_t COMPACT_FLOP = (int64_t)1 << 38;
 
@@ -652,8 +707,8 @@ struct Plan {
     bool pack_w, compact;
     int64_t K8, piece, pieces;
     Class logits, dh, dw;
-    int splits;
-    int64_t split;  // contraction per split of dH
+    int slots;     // workgroups that fill the chip, of dH's class
+    int64_t room;  // rows of fp32 sums for dH
 };
 bool rows_ok(const void *p, int64_t ld, int64_t K)
 {
@@ -672,22 +727,17 @@ Plan make_plan(const void *H, const void *W, int64_t M, int64_t V, int64_t K, in
         most = std::min(V, std::max(G_BYTES / 2 / M, (int64_t)8192));
     if (p.pack_w)
         most = std::min(most, std::max(G_BYTES / 2 / p.K8, (int64_t)1024));
-    p.piece = most >= V ? V : round_up(most, 256);
+    p.piece = most >= V ? V : round_up(most, 768);  // whole tiles of 256 and of 192
     p.pieces = cdiv(V, p.piece);
-    p.logits = logits_class(M, p.piece);
-    p.dh = M <= 64 ? C64X128 : tiles(C256, M, K) >= 160 ? C256 : C128;
-    p.dw = tiles(C256, p.piece, K) >= 160 ? C256 : tiles(C128, p.piece, K) >= 80 ? C128 : C64;
-    // dH has M·K outputs and a contraction over the piece: few tiles are split
-    // along it until some 512 workgroups run, each with at least 8 K-tiles
-    p.splits = 1;
-    p.split = round_up(p.piece, BK);
-    const int64_t t = tiles(p.dh, M, K);
-    if (p.dh != C256 && t < 256) {
-        const int64_t want = cdiv(512, t), can = cdiv(p.piece, 8 * BK);
-        const int64_t s = want < can ? want : can;
-        p.split = round_up(cdiv(p.piece, s), BK);
-        p.splits = (int)cdiv(p.piece, p.split);
-    }
+    p.logits = logits_class(M, p.piece, K);
+    p.dw = best_class(p.piece, K, M);
+    // dH's contraction is long, so its class is the one that runs a K-tile
+    // fastest; the splits (dh_splits) take care of few tiles
+    // (up to 64 of them there is nothing to split)
+    p.dh = M <= 64 ? C64X128 : p.piece <= 64 * BK ? best_class(M, K, p.piece) : M * K >= (int64_t)1 << 20 ? C256 : C128;
+    p.slots = NUM_CU * CLASS[p.dh].per_cu;
+    const int64_t t = tiles(p.dh, M, K), most_splits = std::max((int64_t)1, p.piece / (8 * BK));
+    p.room = M * std::max((int64_t)2, std::min(most_splits, cdiv(p.slots, t)));
     return p;
 }
 
@@ -709,7 +759,7 @@ struct Buffers {
     void *hc, *wp, *G;
     float2 *part, *block_sum;
     float *at_target, *lse, *cp, *ct, *acc;
-    int64_t strips, Gld;
+    int64_t Gld;
 };
 Buffers lay_out(Space &s, const Plan &p, int64_t M, int64_t V, bool bwd)
 {
@@ -722,18 +772,16 @@ Buffers lay_out(Space &s, const Plan &p, int64_t M, int64_t V, bool bwd)
     if (p.pack_w)
         b.wp = s.take<uint16_t>(p.piece * p.K8);
     if (!bwd) {
-        b.strips = cdiv(V, strip_of(p.logits)) + 8;  // the last tile's strips past V included
-        b.part = s.take<float2>(b.strips * M);
+        b.part = s.take<float2>(cdiv(V, CLASS[p.logits].bn) * M);
         b.at_target = s.take<float>(M);
-        b.block_sum = s.take<float2>(cdiv(M, 64));
+        b.block_sum = s.take<float2>(cdiv(M, JOIN_ROWS));
     } else {
         b.lse = s.take<float>(M);
         b.cp = s.take<float>(M);
         b.ct = s.take<float>(M);
         b.Gld = round_up(p.piece, BK);
         b.G = s.take<uint16_t>(M * b.Gld);
-        if (p.pieces > 1 || p.splits > 1)
-            b.acc = s.take<float>(p.splits * M * p.K8);
+        b.acc = s.take<float>(p.room * p.K8);
     }
     return b;
 }
@@ -783,13 +831,13 @@ bool w_piece(const Plan &p, const Buffers &b, const void *W, int64_t ldw, int64_
         return true;
     }
     w = {b.wp, p.K8, (int)n};
-    return launch(xent_gather_kernel, copy_grid(n * p.K8 / 8), 256, stream,
-                  GatherArgs{src, ldw, b.wp, n, K, p.K8, nullptr, nullptr, false});
+    return launch(xent_pack_kernel, copy_grid(n * p.K8 / 8), 256, stream, src, ldw, (uint16_t *)b.wp, n, K, p.K8);
 }
-bool gather_h(const Plan &p, const Buffers &b, const void *H, int64_t ldh, int64_t M, int64_t K, void *stream)
+// the workgroups' share of the tokens: all CUs busy, PREP_ROWS at most
+void split_rows(PrepArgs &a, int64_t &grid)
 {
-    return launch(xent_gather_kernel, copy_grid(M * p.K8 / 8), 256, stream,
-                  GatherArgs{H, ldh, b.hc, M, K, p.K8, b.map, b.head, rows_ok(H, ldh, K)});
+    a.rows = (int)std::min((int64_t)PREP_ROWS, std::max((int64_t)4, cdiv(a.M, 2 * NUM_CU)));
+    grid = cdiv(a.M, a.rows);
 }
 
 template <typename E>
@@ -814,7 +862,7 @@ int forward(const void *H, const void *W, const int64_t *target, float *loss, fl
     if (M == 0) {
         if (reduction == TG_XENT_NONE)
             return TG_OK;
-        return launch(xent_total_kernel, 1, 1024, stream, (const float2 *)nullptr, 0, reduction, loss)
+        return launch(xent_zero_kernel, 1, 256, stream, (uint16_t *)loss, (int64_t)2, (int64_t)1, (int64_t)2)
                    ? TG_OK
                    : TG_ERR_LAUNCH;
     }
@@ -823,11 +871,13 @@ int forward(const void *H, const void *W, const int64_t *target, float *loss, fl
     float *row_loss = reduction == TG_XENT_NONE ? loss : nullptr;
     bool ok = true;
     if (p.compact) {
-        IndexArgs ia = {};
-        ia.target = target, ia.M = M, ia.V = V, ia.ignore = ignore;
-        ia.head = b.head, ia.map = b.map, ia.col = b.col, ia.loss = row_loss, ia.lse_out = lse;
-        ok = ok && launch(xent_index_kernel<false>, 1, INDEX_THREADS, stream, ia);
-        ok = ok && gather_h(p, b, H, ldh, M, K, stream);
+        PrepArgs a = {};
+        a.target = target, a.M = M, a.V = V, a.ignore = ignore;
+        a.head = b.head, a.map = b.map, a.col = b.col, a.loss = row_loss, a.lse_out = lse;
+        a.H = (const uint16_t *)H, a.ldh = ldh, a.hc = (uint16_t *)b.hc, a.K = K, a.K8 = p.K8, a.vec = rows_ok(H, ldh, K);
+        int64_t grid;
+        split_rows(a, grid);
+        ok = launch(xent_prep_kernel<false>, grid, PREP_THREADS, stream, a);
     }
     for (int64_t v0 = 0; ok && v0 < V; v0 += p.piece) {
         const int64_t n = v0 + p.piece < V ? p.piece : V - v0;
@@ -840,38 +890,24 @@ int forward(const void *H, const void *W, const int64_t *target, float *loss, fl
         a.V = (int)n, a.v0 = (int)v0;
         a.col = p.compact ? b.col : nullptr;
         a.target = target, a.Vall = V;
-        a.part = b.part, a.part_ld = M, a.at_target = b.at_target;
-        const int64_t grid = tiles(p.logits, M, n);
-        a.tiles_n = (int)cdiv(n, CLASS_BN[p.logits]);
-        switch (p.logits) {
-        case C256:
-            ok = ok && launch(xent_stats_kernel<E, T256<E, false, false>>, grid, 256, stream, a);
-            break;
-        case C128:
-            ok = ok && launch(xent_stats_kernel<E, T128<E, false, false>>, grid, 256, stream, a);
-            break;
-        case C64X128:
-            ok = ok && launch(xent_stats_kernel<E, T64x128<E, false, false>>, grid, 256, stream, a);
-            break;
-        default:
-            ok = ok && launch(xent_stats_kernel<E, T64<E, false, false>>, grid, 256, stream, a);
-        }
+        a.part = b.part, a.part_ld = M, a.at_target = b.at_target, a.arrived = &b.head->arrived;
+        a.tiles_n = (int)cdiv(n, CLASS[p.logits].bn);
+        ok = ok && with_tile<E, false, false>(p.logits, [&](auto t) {
+            return launch(xent_stats_kernel<E, decltype(t)>, tiles(p.logits, M, n), t.THREADS, stream, a);
+        });
     }
     JoinArgs j = {};
     j.part = b.part, j.part_ld = M;
-    j.strips = (int)cdiv(V, strip_of(p.logits));
+    j.tiles = (int)cdiv(V, CLASS[p.logits].bn);
     j.M = (int)M, j.reduction = reduction;
     j.head = p.compact ? b.head : nullptr;
     j.map = p.compact ? b.map : nullptr;
     j.col = p.compact ? b.col : nullptr;
     j.target = target, j.V = V, j.ignore = ignore;
     j.at_target = b.at_target, j.loss = row_loss, j.lse = lse;
-    const int64_t blocks = cdiv(M, 64);
     j.block_sum = reduction == TG_XENT_NONE ? nullptr : b.block_sum;
-    j.total = reduction != TG_XENT_NONE && blocks == 1 ? loss : nullptr;
-    ok = ok && launch(xent_join_kernel, blocks, 1024, stream, j);
-    if (reduction != TG_XENT_NONE && blocks > 1)
-        ok = ok && launch(xent_total_kernel, 1, 1024, stream, (const float2 *)b.block_sum, (int)blocks, reduction, loss);
+    j.arrived = &b.head->arrived, j.total = loss;
+    ok = ok && launch(xent_join_kernel, cdiv(M, JOIN_ROWS), 1024, stream, j);
     return ok ? TG_OK : TG_ERR_LAUNCH;
 }
 
@@ -897,23 +933,22 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
     }
     if (gfx950_status() != 1)
         return TG_ERR_DEVICE;
-    const auto zero = [&](void *d, int64_t ld, int64_t rows, const int64_t *t) {
-        return launch(xent_zero_kernel, rows < 8 * NUM_CU ? rows : 8 * NUM_CU, 256, stream, (uint16_t *)d, ld, rows, K,
-                      t, ignore);
-    };
     if (M == 0)
-        return !dW || V == 0 || K == 0 || zero(dW, lddw, V, nullptr) ? TG_OK : TG_ERR_LAUNCH;
+        return !dW || V == 0 || K == 0 ||
+                       launch(xent_zero_kernel, std::min(V, (int64_t)8 * NUM_CU), 256, stream, (uint16_t *)dW, lddw, V, K)
+                   ? TG_OK
+                   : TG_ERR_LAUNCH;
     Space s = {reinterpret_cast<char *>(ws)};
     const Buffers b = lay_out(s, p, M, V, true);
-    IndexArgs ia = {};
-    ia.target = target, ia.M = M, ia.V = V, ia.ignore = ignore;
-    ia.head = b.head, ia.map = b.map, ia.col = b.col;
-    ia.reduction = reduction, ia.dloss = dloss, ia.dlse = dlse, ia.lse = lse;
-    ia.lse_c = b.lse, ia.cp = b.cp, ia.ct = b.ct;
-    bool ok = launch(xent_index_kernel<true>, 1, INDEX_THREADS, stream, ia);
-    ok = ok && gather_h(p, b, H, ldh, M, K, stream);
-    if (dH)
-        ok = ok && zero(dH, lddh, M, target);
+    PrepArgs q = {};
+    q.target = target, q.M = M, q.V = V, q.ignore = ignore;
+    q.head = b.head, q.map = b.map, q.col = b.col;
+    q.H = (const uint16_t *)H, q.ldh = ldh, q.hc = (uint16_t *)b.hc, q.K = K, q.K8 = p.K8, q.vec = rows_ok(H, ldh, K);
+    q.reduction = reduction, q.dloss = dloss, q.dlse = dlse, q.lse = lse;
+    q.lse_c = b.lse, q.cp = b.cp, q.ct = b.ct, q.dH = (uint16_t *)dH, q.lddh = lddh;
+    int64_t grid;
+    split_rows(q, grid);
+    bool ok = launch(xent_prep_kernel<true>, grid, PREP_THREADS, stream, q);
     DhArgs d = {};
     for (int64_t v0 = 0; ok && v0 < V; v0 += p.piece) {
         const int64_t n = v0 + p.piece < V ? p.piece : V - v0;
@@ -926,41 +961,22 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
         a.head = b.head, a.V = (int)n, a.v0 = (int)v0, a.col = b.col;
         a.lse = b.lse, a.cp = b.cp, a.ct = b.ct;
         a.G = b.G, a.Gld = round_up(n, BK);
-        a.tiles_n = (int)cdiv(n, CLASS_BN[p.logits]);
-        const int64_t grid = tiles(p.logits, M, n);
-        switch (p.logits) {
-        case C256:
-            ok = ok && launch(xent_grad_kernel<E, T256<E, false, false>>, grid, 256, stream, a);
-            break;
-        case C128:
-            ok = ok && launch(xent_grad_kernel<E, T128<E, false, false>>, grid, 256, stream, a);
-            break;
-        case C64X128:
-            ok = ok && launch(xent_grad_kernel<E, T64x128<E, false, false>>, grid, 256, stream, a);
-            break;
-        default:
-            ok = ok && launch(xent_grad_kernel<E, T64<E, false, false>>, grid, 256, stream, a);
-        }
+        a.tiles_n = (int)cdiv(n, CLASS[p.logits].bn);
+        ok = ok && with_tile<E, false, false>(p.logits, [&](auto t) {
+            return launch(xent_grad_kernel<E, decltype(t)>, tiles(p.logits, M, n), t.THREADS, stream, a);
+        });
         if (dH) {
-            d = {};
             d.g = {b.G, a.Gld, (int)M};
             d.w = {w.p, w.ld, (int)K};
-            d.V = (int)n, d.split = (int)p.split, d.head = b.head;
-            d.acc = b.acc, d.acc_rows = M, d.K8 = p.K8, d.add = v0 > 0;
+            d.V = (int)n, d.piece = (int)p.piece, d.head = b.head;
+            d.acc = b.acc, d.room = p.room, d.K8 = p.K8, d.add = v0 > 0;
             d.map = b.map, d.dH = dH, d.lddh = lddh, d.K = (int)K;
             d.vec = lddh % 8 == 0 && (uintptr_t)dH % 16 == 0;
-            d.tiles_n = (int)cdiv(K, CLASS_BN[p.dh]), d.splits = p.splits;
-            const int64_t g = tiles(p.dh, M, K) * p.splits;
-            switch (p.dh) {
-            case C256:
-                ok = ok && launch(b.acc ? xent_dh_kernel<E, T256<E, false, true>, true> : xent_dh_kernel<E, T256<E, false, true>, false>, g, 256, stream, d);
-                break;
-            case C128:
-                ok = ok && launch(b.acc ? xent_dh_kernel<E, T128<E, false, true>, true> : xent_dh_kernel<E, T128<E, false, true>, false>, g, 256, stream, d);
-                break;
-            default:
-                ok = ok && launch(b.acc ? xent_dh_kernel<E, T64x128<E, false, true>, true> : xent_dh_kernel<E, T64x128<E, false, true>, false>, g, 256, stream, d);
-            }
+            d.bm = CLASS[p.dh].bm, d.tiles_n = (int)cdiv(K, CLASS[p.dh].bn), d.slots = p.slots;
+            const int64_t g = std::max(tiles(p.dh, M, K), (int64_t)p.slots);
+            ok = ok && with_tile<E, false, true>(p.dh, [&](auto t) {
+                return launch(xent_dh_kernel<E, decltype(t)>, g, t.THREADS, stream, d);
+            });
         }
         if (dW) {
             DwArgs x = {};
@@ -970,21 +986,13 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
             x.dW = reinterpret_cast<uint16_t *>(dW) + v0 * lddw, x.lddw = lddw;
             x.V = (int)n, x.K = (int)K;
             x.vec = lddw % 8 == 0 && (uintptr_t)dW % 16 == 0;
-            x.tiles_m = (int)cdiv(n, CLASS_BM[p.dw]), x.tiles_n = (int)cdiv(K, CLASS_BN[p.dw]);
-            const int64_t g = tiles(p.dw, n, K);
-            switch (p.dw) {
-            case C256:
-                ok = ok && launch(xent_dw_kernel<E, T256<E, true, true>>, g, 256, stream, x);
-                break;
-            case C128:
-                ok = ok && launch(xent_dw_kernel<E, T128<E, true, true>>, g, 256, stream, x);
-                break;
-            default:
-                ok = ok && launch(xent_dw_kernel<E, T64<E, true, true>>, g, 256, stream, x);
-            }
+            x.tiles_m = (int)cdiv(n, CLASS[p.dw].bm), x.tiles_n = (int)cdiv(K, CLASS[p.dw].bn);
+            ok = ok && with_tile<E, true, true>(p.dw, [&](auto t) {
+                return launch(xent_dw_kernel<E, decltype(t)>, tiles(p.dw, n, K), t.THREADS, stream, x);
+            });
         }
     }
-    if (ok && dH && b.acc)
+    if (ok && dH)
         ok = launch(xent_dh_finish_kernel<E>, copy_grid(M * p.K8 / 4), 256, stream, d);
     return ok ? TG_OK : TG_ERR_LAUNCH;
 }
@@ -1054,8 +1062,8 @@ extern "C" int tg_xent_plan(const void *H, const void *W, int64_t M, int64_t V, 
     if (name && name_len > 0) {
         const char *pre = p.compact ? "gather " : "", *pack = p.pack_w ? "pack " : "";
         if (backward_pass)
-            snprintf(name, (size_t)name_len, "%s%sgrad_%s dh_%s_s%d dw_%s", pre, pack, CLASS_NAME[p.logits],
-                     CLASS_NAME[p.dh], p.splits, CLASS_NAME[p.dw]);
+            snprintf(name, (size_t)name_len, "%s%sgrad_%s dh_%s dw_%s", pre, pack, CLASS_NAME[p.logits],
+                     CLASS_NAME[p.dh], CLASS_NAME[p.dw]);
         else
             snprintf(name, (size_t)name_len, "%s%sstats_%s", pre, pack, CLASS_NAME[p.logits]);
     }

@@ -47,8 +47,14 @@ def _pkg():
     return pkg
 
 
+_loaded = None
+
+
 def _lib():
-    return _pkg().load()
+    global _loaded
+    if _loaded is None:
+        _loaded = _pkg().load()
+    return _loaded
 
 
 def _p(x):
@@ -178,48 +184,54 @@ def _row_stride(t, name, width):
     return t.stride(0)
 
 
-def _forward(H, W, target, ignore_index, reduction, want_lse):
+@functools.lru_cache(maxsize=1024)
+def _xent_size(backward, h_aligned, w_aligned, M, V, K, ldh, ldw):
+    """Workspace bytes; of the pointers only their alignment counts."""
+    fn = _lib().tg_xent_bwd_workspace_bytes if backward else _lib().tg_xent_workspace_bytes
+    return fn(4096 if h_aligned else 4098, 4096 if w_aligned else 4098, M, V, K, ldh, ldw)
+
+
+def _xent_call(backward, H, W, lead, tail, args):
+    """Workspace, stream and device around one call of the library."""
     import torch
 
     M, K = H.shape
     V = W.shape[0]
     ldh, ldw = _row_stride(H, "H", K), _row_stride(W, "W", K)
-    lib = _lib()
     h, w = H.data_ptr(), W.data_ptr()
-    size = lib.tg_xent_workspace_bytes(h, w, M, V, K, ldh, ldw)
+    size = max(_xent_size(backward, h % 16 == 0, w % 16 == 0, M, V, K, ldh, ldw), 0)
     dev = H.device
-    loss = torch.empty((M,) if reduction == TG_XENT_NONE else (), dtype=torch.float32, device=dev)
-    lse = torch.empty((M,), dtype=torch.float32, device=dev) if want_lse else None
-    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
-    fn = lib.tg_xent_f16 if H.dtype == torch.float16 else lib.tg_xent_bf16
-    with torch.cuda.device(dev):
-        st = fn(h, w, target.data_ptr(), loss.data_ptr(), _p(lse), M, V, K, ldh, ldw, ignore_index, reduction,
-                ws.data_ptr(), max(size, 0), torch.cuda.current_stream(dev).cuda_stream)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    fn = getattr(_lib(), ("tg_xent_bwd_" if backward else "tg_xent_") + ("f16" if H.dtype == torch.float16 else "bf16"))
+    args = (h, w, *lead, M, V, K, ldh, ldw, *tail, *args, ws.data_ptr(), size,
+            torch.cuda.current_stream(dev).cuda_stream)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
     if st:
-        raise _pkg().TgError(st, "linear_cross_entropy")
+        raise _pkg().TgError(st, "linear_cross_entropy (backward)" if backward else "linear_cross_entropy")
+
+
+def _forward(H, W, target, ignore_index, reduction, want_lse):
+    import torch
+
+    M = H.shape[0]
+    loss = torch.empty((M,) if reduction == TG_XENT_NONE else (), dtype=torch.float32, device=H.device)
+    lse = torch.empty((M,), dtype=torch.float32, device=H.device) if want_lse else None
+    _xent_call(False, H, W, (target.data_ptr(), loss.data_ptr(), _p(lse)), (), (ignore_index, reduction))
     return loss, lse
 
 
 def _backward(H, W, target, lse, dloss, dlse, need_h, need_w, ignore_index, reduction):
     import torch
 
-    M, K = H.shape
-    V = W.shape[0]
-    ldh, ldw = _row_stride(H, "H", K), _row_stride(W, "W", K)
-    lib = _lib()
-    h, w = H.data_ptr(), W.data_ptr()
-    size = lib.tg_xent_bwd_workspace_bytes(h, w, M, V, K, ldh, ldw)
-    dev = H.device
-    dH = torch.empty((M, K), dtype=H.dtype, device=dev) if need_h else None
-    dW = torch.empty((V, K), dtype=W.dtype, device=dev) if need_w else None
-    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
-    fn = lib.tg_xent_bwd_f16 if H.dtype == torch.float16 else lib.tg_xent_bwd_bf16
-    with torch.cuda.device(dev):
-        st = fn(h, w, target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _p(dlse), _p(dH), _p(dW), M, V, K, ldh,
-                ldw, max(K, 1), max(K, 1), ignore_index, reduction, ws.data_ptr(), max(size, 0),
-                torch.cuda.current_stream(dev).cuda_stream)
-    if st:
-        raise _pkg().TgError(st, "linear_cross_entropy (backward)")
+    K = max(H.shape[1], 1)
+    dH = torch.empty(H.shape, dtype=H.dtype, device=H.device) if need_h else None
+    dW = torch.empty(W.shape, dtype=W.dtype, device=W.device) if need_w else None
+    _xent_call(True, H, W, (target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _p(dlse), _p(dH), _p(dW)), (K, K),
+               (ignore_index, reduction))
     return dH, dW
 
 
@@ -289,8 +301,6 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
         raise ValueError(f"{target.shape[0]} targets for {H.shape[0]} rows of H")
     if reduction not in _REDUCTIONS:
         raise ValueError("reduction is 'none', 'sum' or 'mean'")
-    _row_stride(H, "H", H.shape[1])
-    _row_stride(W, "W", W.shape[1])
     target = target.contiguous()
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         loss, lse = _xent_function().apply(H, W, target, ignore_index, _REDUCTIONS[reduction])
@@ -347,10 +357,14 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     fn = {torch.float32: lib.tg_newton_schulz_f32, torch.float16: lib.tg_newton_schulz_f16,
           torch.bfloat16: lib.tg_newton_schulz_bf16}[G.dtype]
     c = None if flat is None else (ctypes.c_float * max(1, len(flat)))(*flat)
-    with torch.cuda.device(G.device):
-        st = fn(g.data_ptr(), o.data_ptr(), batch, rows, cols, ldg, g.stride(0) if batch > 1 else rows * ldg, ldo,
-                o.stride(0) if batch > 1 else rows * ldo, steps, c, eps, ws.data_ptr(), max(size, 0),
-                torch.cuda.current_stream(G.device).cuda_stream)
+    args = (g.data_ptr(), o.data_ptr(), batch, rows, cols, ldg, g.stride(0) if batch > 1 else rows * ldg, ldo,
+            o.stride(0) if batch > 1 else rows * ldo, steps, c, eps, ws.data_ptr(), max(size, 0),
+            torch.cuda.current_stream(G.device).cuda_stream)
+    if torch.cuda.current_device() == G.device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(G.device):
+            st = fn(*args)
     if st:
         raise _pkg().TgError(st, "newton_schulz")
     return out
