@@ -93,6 +93,13 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const G *g, int64_t rows, 
         part[blockIdx.x] = ((sh[0] + sh[1]) + sh[2]) + sh[3];
 }
 
+// 1 / (norm + eps): 0 for a zero matrix without eps, which stays zero; NaN where
+// the norm is not finite, so that the whole result is.
+__device__ inline double inverse(double by)
+{
+    return by == 0.0 ? 0.0 : by < (double)INFINITY ? 1.0 / by : (double)NAN;
+}
+
 // X0 = G / (norm + eps) in fp32, and its binary16 image padded with zeros to
 // ldx columns.  With `out` (no steps) the result itself.
 template <typename G>
@@ -107,9 +114,7 @@ __global__ __launch_bounds__(256) void ns_scale_kernel(const G *g, int64_t rows,
         s += part[m * norm_blocks + i];
     for (int o = 32; o; o >>= 1)
         s += __shfl_xor(s, o);
-    const double by = sqrt(s) + (double)eps;
-    // a zero matrix without eps stays zero
-    const double inv = by > 0.0 || by != by ? 1.0 / by : 0.0;
+    const double inv = inverse(sqrt(s) + (double)eps);
     const G *p = g + (int64_t)m * stride;
     const int64_t per = ldx / 4, total = rows * per;
     for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
@@ -349,6 +354,207 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
                                             (int)a.ldx, true, nullptr, lane);
 }
 
+// ------------------------------------------------------------ small matrices
+// Both sides at most 128: one workgroup runs the whole iteration with X (fp32) in
+// registers and the operands in LDS; nothing but G and the result touches
+// memory.  As separate launches such a matrix pays some 4 us for each of 17
+// kernels that compute for well under one.  Eight waves (2×4, two to a SIMD), 64×32
+// of each 128×128 product per wave; the image is as wide as it is high, so the
+// shorter side is made the rows on loading (`flip`) and no other form is needed.
+//
+// LDS images are row-major, 128 columns, chunk c of row r at c ^ (r mod 16): the
+// sixteen rows of a K-major fragment read fall on sixteen bank groups; the
+// transposed reads of X (two rows to a 32-byte group) take two passes.
+constexpr int SMALL = 128;
+__host__ __device__ constexpr int small_off(int r, int c) { return r * SMALL + (((c >> 3) ^ (r & 15)) << 3) + (c & 7); }
+struct SmallArgs {
+    const void *g;
+    int64_t ld, stride;
+    __bf16 *out;
+    int64_t ldo, o_stride;
+    int s, l;      // rows and columns of the image
+    bool flip;     // the image is G transposed
+    int steps;
+    float eps;
+    float k[3 * TG_NS_MAX_STEPS];
+};
+template <typename G>
+__global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
+{
+    using V8 = El<half_t>::v8;
+    constexpr int TM = 4, TN = 2;
+    __shared__ __attribute__((aligned(1024))) half_t xi[SMALL * SMALL], oi[SMALL * SMALL], pi[SMALL * SMALL];
+    __shared__ __attribute__((aligned(16))) float d[SMALL], e[SMALL];
+    __shared__ double sums[8];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, fh = lane >> 4;
+    const int r0 = (wave >> 2) * 64, c0 = (wave & 3) * 32;
+    const G *g = reinterpret_cast<const G *>(a.g) + (int64_t)blockIdx.x * a.stride;
+
+    // X in the accumulators' layout: block (i, j), row fr, columns 4·fh .. +3
+    f32x4 x[TM][TN];
+    double s2 = 0.0;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int r = r0 + 16 * i + fr, c = c0 + 16 * j + 4 * fh + v;
+                float f = 0.0f;
+                if (r < a.s && c < a.l)
+                    f = (float)g[a.flip ? c * a.ld + r : r * a.ld + c];
+                x[i][j][v] = f;
+                s2 += (double)f * (double)f;
+            }
+    for (int o = 32; o; o >>= 1)
+        s2 += __shfl_xor(s2, o);
+    if (lane == 0)
+        sums[wave] = s2;
+    if (threadIdx.x < SMALL)
+        d[threadIdx.x] = e[threadIdx.x] = 0.0f;
+    __syncthreads();
+    s2 = 0.0;
+    for (int w = 0; w < 8; ++w)
+        s2 += sums[w];
+    const double inv = inverse(sqrt(s2) + (double)a.eps);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                x[i][j][v] = (float)((double)x[i][j][v] * inv);
+
+    auto kmajor = [&](const half_t *img, int row, int kk) {
+        return *reinterpret_cast<const V8 *>(img + small_off(row + fr, kk * 32 + 8 * fh));
+    };
+    auto trans = [&](const half_t *img, int col, int kk) {
+        const int k = kk * 32 + 8 * fh + (fr >> 2), c = col + 4 * (fr & 3);
+        union {
+            s16x4 h[2];
+            V8 v;
+        } u;
+        u.h[0] = lds_read_tr(img + small_off(k, c));
+        u.h[1] = lds_read_tr(img + small_off(k + 4, c));
+        return u.v;
+    };
+    // acc = the wave's block of A·Bᵀ (B K-major) or A·B (transposed reads)
+    auto product = [&](const half_t *ai, const half_t *bi, auto transposed, f32x4(&acc)[TM][TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < SMALL / 32; ++kk) {
+            V8 fa[TM], fb[TN];
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                fa[i] = kmajor(ai, r0 + 16 * i, kk);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                fb[j] = decltype(transposed)::value ? trans(bi, c0 + 16 * j, kk) : kmajor(bi, c0 + 16 * j, kk);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = El<half_t>::mfma(fb[j], fa[i], acc[i][j]);
+        }
+    };
+    auto put = [&](half_t *img, int i, int j, half4 h) {
+        *reinterpret_cast<half4 *>(img + small_off(r0 + 16 * i + fr, c0 + 16 * j + 4 * fh)) = h;
+    };
+#pragma unroll 1
+    for (int t = 0; t < a.steps; ++t) {
+        const float ka = a.k[3 * t], kb = a.k[3 * t + 1], kc = a.k[3 * t + 2];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                half4 h;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    h[v] = (half_t)(x[i][j][v] * X_SCALE);
+                put(xi, i, j, h);
+            }
+        __syncthreads();
+        f32x4 acc[TM][TN];
+        half4 o[TM][TN];
+        product(xi, xi, std::false_type{}, acc);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    o[i][j][v] = (half_t)(acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE)));
+                if (r0 + 16 * i == c0 + 16 * j)  // a block of the diagonal
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (fr == 4 * fh + v) {
+                            d[r0 + 16 * i + fr] = acc[i][j][v] * (1.0f / (X_SCALE * X_SCALE));
+                            o[i][j][v] = (half_t)0.0f;
+                        }
+                put(oi, i, j, o[i][j]);
+            }
+        __syncthreads();
+        product(oi, oi, std::false_type{}, acc);
+        float dr[TM];
+        f32x4 dc[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            dr[i] = d[r0 + 16 * i + fr];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            dc[j] = *reinterpret_cast<const f32x4 *>(d + c0 + 16 * j + 4 * fh);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                half4 h;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float f = (float)o[i][j][v], y = acc[i][j][v] * (1.0f / S_SCALE);
+                    h[v] = (half_t)(kb * f + kc * ((dr[i] + dc[j][v]) * f + y));
+                }
+                if (r0 + 16 * i == c0 + 16 * j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (fr == 4 * fh + v) {
+                            e[r0 + 16 * i + fr] =
+                                kb * dr[i] + kc * (dr[i] * dr[i] + acc[i][j][v] * (1.0f / (S_SCALE * S_SCALE)));
+                            h[v] = (half_t)0.0f;
+                        }
+                put(pi, i, j, h);
+            }
+        __syncthreads();
+        product(pi, xi, std::true_type{}, acc);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const float f = ka + e[r0 + 16 * i + fr];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    x[i][j][v] = f * x[i][j][v] + acc[i][j][v] * (1.0f / (S_SCALE * X_SCALE));
+        }
+        __syncthreads();  // every wave has read X's image
+    }
+    __bf16 *out = a.out + (int64_t)blockIdx.x * a.o_stride;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int r = r0 + 16 * i + fr, c = c0 + 16 * j + 4 * fh + v;
+                if (r < a.s && c < a.l)
+                    out[a.flip ? c * a.ldo + r : r * a.ldo + c] = (__bf16)x[i][j][v];
+            }
+}
+
 // -------------------------------------------------------------------- plans
 // Tile classes, chosen by tile_time for the whole batch.  One 256×256 or
 // 192×192 workgroup per CU, two of the smaller ones.  192×192 is there for the
@@ -377,7 +583,7 @@ using T64 = Tile<half_t, 64, 64, 2, 2, 3, TA, TB>;
 
 struct Plan {
     int64_t s, l, ldx, lds;
-    bool tall;
+    bool tall, small;
     Class gram, square, upd;
     int norm_blocks;
 };
@@ -390,6 +596,7 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
 {
     Plan p;
     p.tall = rows > cols;
+    p.small = rows <= SMALL && cols <= SMALL;
     p.s = std::min(rows, cols), p.l = std::max(rows, cols);
     p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
     const auto best = [&](const TileClass *cls, auto count, int64_t k) {
@@ -415,7 +622,9 @@ struct Buffers {
 };
 Buffers lay_out(char *base, const Plan &p, int64_t batch, int64_t rows)
 {
-    Buffers b;
+    Buffers b = {};
+    if (p.small)
+        return b;
     const auto take = [&](auto *&ptr, int64_t n) {
         using X = std::remove_reference_t<decltype(*ptr)>;
         ptr = base ? reinterpret_cast<X *>(base + b.used) : nullptr;
@@ -501,12 +710,19 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         return TG_ERR_INVALID_ARG;
     const Plan p = make_plan(batch, rows, cols);
     const Buffers b = lay_out(reinterpret_cast<char *>(ws), p, batch, rows);
-    if (!g || !o || !ws || (uintptr_t)ws % 256 != 0 || ws_bytes < b.used)
+    if (!g || !o || (b.used > 0 && (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < b.used)))
         return TG_ERR_INVALID_ARG;
     if (gfx950_status() != 1)
         return TG_ERR_DEVICE;
     const G *src = reinterpret_cast<const G *>(g);
     __bf16 *out = reinterpret_cast<__bf16 *>(o);
+    static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
+    if (p.small) {
+        SmallArgs a = {g, ldg, g_stride, out, ldo, o_stride, (int)p.s, (int)p.l, p.tall, steps, eps, {}};
+        for (int i = 0; i < 3 * steps; ++i)
+            a.k[i] = coefficients ? coefficients[i] : standard[i % 3];
+        return launch(ns_small_kernel<G>, batch, 512, stream, a) ? TG_OK : TG_ERR_LAUNCH;
+    }
     bool ok = launch(ns_norm_kernel<G>, batch * p.norm_blocks, 256, stream, src, rows, cols, ldg, g_stride,
                      p.norm_blocks, b.part);
     const int64_t chunks = cdiv(rows * p.ldx / 4, 256);
@@ -515,7 +731,6 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
                       p.norm_blocks, (const double *)b.part, eps, scale_blocks, b.x, b.xh[0], p.ldx,
                       steps == 0 ? out : nullptr, ldo, o_stride);
     for (int t = 0; ok && t < steps; ++t) {
-        static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
         const float *k = coefficients ? coefficients + 3 * t : standard;
         const half_t *xh = b.xh[t & 1];
         SymArgs a = {};
@@ -594,7 +809,9 @@ extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, 
     if (st != TG_OK || batch == 0 || rows == 0 || cols == 0)
         return st;
     const Plan p = make_plan(batch, rows, cols);
-    if (name && name_len > 0)
+    if (name && name_len > 0 && p.small)
+        snprintf(name, (size_t)name_len, "small");
+    else if (name && name_len > 0)
         snprintf(name, (size_t)name_len, "%s gram_%s square_%s update_%s", p.tall ? "tall" : "wide",
                  CLASS_NAME[p.gram], CLASS_NAME[p.square], CLASS_NAME[p.upd]);
     return TG_OK;
