@@ -358,15 +358,33 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 // Both sides at most 128: one workgroup runs the whole iteration with X (fp32) in
 // registers and the operands in LDS; nothing but G and the result touches
 // memory.  As separate launches such a matrix pays some 4 us for each of 17
-// kernels that compute for well under one.  Eight waves (2×4, two to a SIMD), 64×32
-// of each 128×128 product per wave; the image is as wide as it is high, so the
-// shorter side is made the rows on loading (`flip`) and no other form is needed.
+// kernels that compute for well under one.  The IM×IM image is as wide as it is
+// high, so the shorter side is made the rows on loading (`flip`) and no other
+// form is needed.  128: eight waves (2×4, two to a SIMD) of 64×32; 64: four of
+// 32×32.
 //
-// LDS images are row-major, 128 columns, chunk c of row r at c ^ (r mod 16): the
-// sixteen rows of a K-major fragment read fall on sixteen bank groups; the
-// transposed reads of X (two rows to a 32-byte group) take two passes.
-constexpr int SMALL = 128;
-__host__ __device__ constexpr int small_off(int r, int c) { return r * SMALL + (((c >> 3) ^ (r & 15)) << 3) + (c & 7); }
+// The rounding of X's operand spreads evenly over the s directions of the
+// short side, and a direction whose singular value is small beside the norm is
+// amplified by up to 485 afterwards: with 64 and more of them that stays below
+// the result's own rounding, with a few it does not (a 2×2 matrix of condition
+// 100 came out 6e-3 off).  The 64×64 form therefore holds each operand as the
+// sum of two binary16 values and takes three products for each (the fourth, of
+// the two low parts, is below fp32).
+//
+// LDS images are row-major; chunk c of row r at c ^ swz(r), so that the sixteen
+// rows of a K-major fragment read fall on sixteen bank groups; the transposed
+// reads of X (two rows to a 32-byte group) take two passes.
+template <int IM>
+struct Small {
+    static constexpr int WM = 2, WN = IM == 128 ? 4 : 2, WAVES = WM * WN;
+    static constexpr int TM = IM / WM / 16, TN = IM / WN / 16;
+    static constexpr int PARTS = IM == 128 ? 1 : 2;
+    static_assert(IM == 128 || IM == 64, "two forms");
+    __host__ __device__ static constexpr int off(int r, int c)
+    {
+        return r * IM + (((c >> 3) ^ (IM == 128 ? r & 15 : (r >> 1) & 7)) << 3) + (c & 7);
+    }
+};
 struct SmallArgs {
     const void *g;
     int64_t ld, stride;
@@ -378,18 +396,19 @@ struct SmallArgs {
     float eps;
     float k[3 * TG_NS_MAX_STEPS];
 };
-template <typename G>
-__global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
+template <typename G, int IM>
+__global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallArgs a)
 {
     using V8 = El<half_t>::v8;
-    constexpr int TM = 4, TN = 2;
-    __shared__ __attribute__((aligned(1024))) half_t xi[SMALL * SMALL], oi[SMALL * SMALL], pi[SMALL * SMALL];
-    __shared__ __attribute__((aligned(16))) float d[SMALL], e[SMALL];
-    __shared__ double sums[8];
+    using S = Small<IM>;
+    constexpr int TM = S::TM, TN = S::TN, PARTS = S::PARTS;
+    __shared__ __attribute__((aligned(1024))) half_t xi[PARTS * IM * IM], oi[PARTS * IM * IM], pi[PARTS * IM * IM];
+    __shared__ __attribute__((aligned(16))) float d[IM], e[IM];
+    __shared__ double sums[S::WAVES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fh = lane >> 4;
-    const int r0 = (wave >> 2) * 64, c0 = (wave & 3) * 32;
+    const int r0 = wave / S::WN * (IM / S::WM), c0 = wave % S::WN * (IM / S::WN);
     const G *g = reinterpret_cast<const G *>(a.g) + (int64_t)blockIdx.x * a.stride;
 
     // X in the accumulators' layout: block (i, j), row fr, columns 4·fh .. +3
@@ -412,11 +431,9 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
         s2 += __shfl_xor(s2, o);
     if (lane == 0)
         sums[wave] = s2;
-    if (threadIdx.x < SMALL)
-        d[threadIdx.x] = e[threadIdx.x] = 0.0f;
     __syncthreads();
     s2 = 0.0;
-    for (int w = 0; w < 8; ++w)
+    for (int w = 0; w < S::WAVES; ++w)
         s2 += sums[w];
     const double inv = inverse(sqrt(s2) + (double)a.eps);
 #pragma unroll
@@ -428,7 +445,7 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
                 x[i][j][v] = (float)((double)x[i][j][v] * inv);
 
     auto kmajor = [&](const half_t *img, int row, int kk) {
-        return *reinterpret_cast<const V8 *>(img + small_off(row + fr, kk * 32 + 8 * fh));
+        return *reinterpret_cast<const V8 *>(img + S::off(row + fr, kk * 32 + 8 * fh));
     };
     auto trans = [&](const half_t *img, int col, int kk) {
         const int k = kk * 32 + 8 * fh + (fr >> 2), c = col + 4 * (fr & 3);
@@ -436,8 +453,8 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
             s16x4 h[2];
             V8 v;
         } u;
-        u.h[0] = lds_read_tr(img + small_off(k, c));
-        u.h[1] = lds_read_tr(img + small_off(k + 4, c));
+        u.h[0] = lds_read_tr(img + S::off(k, c));
+        u.h[1] = lds_read_tr(img + S::off(k + 4, c));
         return u.v;
     };
     // acc = the wave's block of A·Bᵀ (B K-major) or A·B (transposed reads)
@@ -448,23 +465,50 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
             for (int j = 0; j < TN; ++j)
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kk = 0; kk < SMALL / 32; ++kk) {
-            V8 fa[TM], fb[TN];
+        for (int kk = 0; kk < IM / 32; ++kk) {
+            V8 fa[PARTS][TM], fb[PARTS][TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-                fa[i] = kmajor(ai, r0 + 16 * i, kk);
+            for (int p = 0; p < PARTS; ++p) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                fb[j] = decltype(transposed)::value ? trans(bi, c0 + 16 * j, kk) : kmajor(bi, c0 + 16 * j, kk);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int i = 0; i < TM; ++i)
+                    fa[p][i] = kmajor(ai + p * IM * IM, r0 + 16 * i, kk);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    acc[i][j] = El<half_t>::mfma(fb[j], fa[i], acc[i][j]);
+                    fb[p][j] = decltype(transposed)::value ? trans(bi + p * IM * IM, c0 + 16 * j, kk)
+                                                           : kmajor(bi + p * IM * IM, c0 + 16 * j, kk);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    acc[i][j] = El<half_t>::mfma(fb[0][j], fa[0][i], acc[i][j]);
+                    if constexpr (PARTS == 2) {
+                        acc[i][j] = El<half_t>::mfma(fb[1][j], fa[0][i], acc[i][j]);
+                        acc[i][j] = El<half_t>::mfma(fb[0][j], fa[1][i], acc[i][j]);
+                    }
+                }
         }
     };
-    auto put = [&](half_t *img, int i, int j, half4 h) {
-        *reinterpret_cast<half4 *>(img + small_off(r0 + 16 * i + fr, c0 + 16 * j + 4 * fh)) = h;
+    // v as the operand's image holds it; returns the value held
+    auto put = [&](half_t *img, int i, int j, const f32x4 &v) {
+        half4 h;
+        f32x4 held;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = (half_t)v[k];
+            held[k] = (float)h[k];
+        }
+        const int at = S::off(r0 + 16 * i + fr, c0 + 16 * j + 4 * fh);
+        *reinterpret_cast<half4 *>(img + at) = h;
+        if constexpr (PARTS == 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[k] = (half_t)(v[k] - held[k]);
+                held[k] += (float)h[k];
+            }
+            *reinterpret_cast<half4 *>(img + IM * IM + at) = h;
+        }
+        return held;
     };
 #pragma unroll 1
     for (int t = 0; t < a.steps; ++t) {
@@ -473,15 +517,14 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                half4 h;
+                f32x4 v;
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    h[v] = (half_t)(x[i][j][v] * X_SCALE);
-                put(xi, i, j, h);
+                for (int k = 0; k < 4; ++k)
+                    v[k] = x[i][j][k] * X_SCALE;
+                put(xi, i, j, v);
             }
         __syncthreads();
-        f32x4 acc[TM][TN];
-        half4 o[TM][TN];
+        f32x4 acc[TM][TN], o[TM][TN];
         product(xi, xi, std::false_type{}, acc);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -489,15 +532,15 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
             for (int j = 0; j < TN; ++j) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    o[i][j][v] = (half_t)(acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE)));
+                    o[i][j][v] = acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE));
                 if (r0 + 16 * i == c0 + 16 * j)  // a block of the diagonal
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         if (fr == 4 * fh + v) {
                             d[r0 + 16 * i + fr] = acc[i][j][v] * (1.0f / (X_SCALE * X_SCALE));
-                            o[i][j][v] = (half_t)0.0f;
+                            o[i][j][v] = 0.0f;
                         }
-                put(oi, i, j, o[i][j]);
+                o[i][j] = put(oi, i, j, o[i][j]);
             }
         __syncthreads();
         product(oi, oi, std::false_type{}, acc);
@@ -513,11 +556,11 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                half4 h;
+                f32x4 h;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float f = (float)o[i][j][v], y = acc[i][j][v] * (1.0f / S_SCALE);
-                    h[v] = (half_t)(kb * f + kc * ((dr[i] + dc[j][v]) * f + y));
+                    const float f = o[i][j][v], y = acc[i][j][v] * (1.0f / S_SCALE);
+                    h[v] = kb * f + kc * ((dr[i] + dc[j][v]) * f + y);
                 }
                 if (r0 + 16 * i == c0 + 16 * j)
 #pragma unroll
@@ -525,7 +568,7 @@ __global__ __launch_bounds__(512) void ns_small_kernel(SmallArgs a)
                         if (fr == 4 * fh + v) {
                             e[r0 + 16 * i + fr] =
                                 kb * dr[i] + kc * (dr[i] * dr[i] + acc[i][j][v] * (1.0f / (S_SCALE * S_SCALE)));
-                            h[v] = (half_t)0.0f;
+                            h[v] = 0.0f;
                         }
                 put(pi, i, j, h);
             }
@@ -596,7 +639,7 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
 {
     Plan p;
     p.tall = rows > cols;
-    p.small = rows <= SMALL && cols <= SMALL;
+    p.small = std::max(rows, cols) <= 128;
     p.s = std::min(rows, cols), p.l = std::max(rows, cols);
     p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
     const auto best = [&](const TileClass *cls, auto count, int64_t k) {
@@ -721,7 +764,9 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         SmallArgs a = {g, ldg, g_stride, out, ldo, o_stride, (int)p.s, (int)p.l, p.tall, steps, eps, {}};
         for (int i = 0; i < 3 * steps; ++i)
             a.k[i] = coefficients ? coefficients[i] : standard[i % 3];
-        return launch(ns_small_kernel<G>, batch, 512, stream, a) ? TG_OK : TG_ERR_LAUNCH;
+        const bool ok = p.l <= 64 ? launch(ns_small_kernel<G, 64>, batch, Small<64>::WAVES * 64, stream, a)
+                                  : launch(ns_small_kernel<G, 128>, batch, Small<128>::WAVES * 64, stream, a);
+        return ok ? TG_OK : TG_ERR_LAUNCH;
     }
     bool ok = launch(ns_norm_kernel<G>, batch * p.norm_blocks, 256, stream, src, rows, cols, ldg, g_stride,
                      p.norm_blocks, b.part);
@@ -810,7 +855,7 @@ extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, 
         return st;
     const Plan p = make_plan(batch, rows, cols);
     if (name && name_len > 0 && p.small)
-        snprintf(name, (size_t)name_len, "small");
+        snprintf(name, (size_t)name_len, "small_%d", p.l <= 64 ? 64 : 128);
     else if (name && name_len > 0)
         snprintf(name, (size_t)name_len, "%s gram_%s square_%s update_%s", p.tall ? "tall" : "wide",
                  CLASS_NAME[p.gram], CLASS_NAME[p.square], CLASS_NAME[p.upd]);

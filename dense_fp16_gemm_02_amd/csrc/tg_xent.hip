@@ -675,8 +675,10 @@ bool with_tile(Class c, F f)
     switch (c) {
     case C256:
         return f(Tile<E, 256, 256, 2, 2, 2, TA, TB>{});
-    case C192:
-        return f(Tile<E, 192, 192, 2, 2, 2, TA, TB>{});
+    case C192:  // (not dH's: its splits fill the chip at any tile size)
+        if constexpr (TA == TB)
+            return f(Tile<E, 192, 192, 2, 2, 2, TA, TB>{});
+        [[fallthrough]];
     case C128:
         return f(Tile<E, 128, 128, 2, 2, 2, TA, TB>{});
     case C64X128:
@@ -688,11 +690,11 @@ bool with_tile(Class c, F f)
     }
 }
 int64_t tiles(Class c, int64_t m, int64_t n) { return cdiv(m, CLASS[c].bm) * cdiv(n, CLASS[c].bn); }
-Class best_class(int64_t m, int64_t n, int64_t k)
+Class best_class(int64_t m, int64_t n, int64_t k, bool dh = false)
 {
     int c = 0;
     for (int i = 1; i < C64X128; ++i)
-        if (tile_time(CLASS[i], tiles((Class)i, m, n), cdiv(k, BK)) < tile_time(CLASS[c], tiles((Class)c, m, n), cdiv(k, BK)))
+        if (!(dh && i == C192) && tile_time(CLASS[i], tiles((Class)i, m, n), cdiv(k, BK)) < tile_time(CLASS[c], tiles((Class)c, m, n), cdiv(k, BK)))
             c = i;
     return (Class)c;
 }
@@ -734,7 +736,7 @@ Plan make_plan(const void *H, const void *W, int64_t M, int64_t V, int64_t K, in
     // dH's contraction is long, so its class is the one that runs a K-tile
     // fastest; the splits (dh_splits) take care of few tiles
     // (up to 64 of them there is nothing to split)
-    p.dh = M <= 64 ? C64X128 : p.piece <= 64 * BK ? best_class(M, K, p.piece) : M * K >= (int64_t)1 << 20 ? C256 : C128;
+    p.dh = M <= 64 ? C64X128 : p.piece <= 64 * BK ? best_class(M, K, p.piece, true) : M * K >= (int64_t)1 << 20 ? C256 : C128;
     p.slots = NUM_CU * CLASS[p.dh].per_cu;
     const int64_t t = tiles(p.dh, M, K), most_splits = std::max((int64_t)1, p.piece / (8 * BK));
     p.room = M * std::max((int64_t)2, std::min(most_splits, cdiv(p.slots, t)));
@@ -857,11 +859,11 @@ int forward(const void *H, const void *W, const int64_t *target, float *loss, fl
         if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < need)
             return TG_ERR_INVALID_ARG;
     }
+    if (M == 0 && reduction == TG_XENT_NONE)
+        return TG_OK;
     if (gfx950_status() != 1)
         return TG_ERR_DEVICE;
     if (M == 0) {
-        if (reduction == TG_XENT_NONE)
-            return TG_OK;
         return launch(xent_zero_kernel, 1, 256, stream, (uint16_t *)loss, (int64_t)2, (int64_t)1, (int64_t)2)
                    ? TG_OK
                    : TG_ERR_LAUNCH;
@@ -931,11 +933,12 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
         if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < need)
             return TG_ERR_INVALID_ARG;
     }
+    if ((M == 0 && (!dW || V == 0 || K == 0)) || (!dH && !dW))
+        return TG_OK;
     if (gfx950_status() != 1)
         return TG_ERR_DEVICE;
     if (M == 0)
-        return !dW || V == 0 || K == 0 ||
-                       launch(xent_zero_kernel, std::min(V, (int64_t)8 * NUM_CU), 256, stream, (uint16_t *)dW, lddw, V, K)
+        return launch(xent_zero_kernel, std::min(V, (int64_t)8 * NUM_CU), 256, stream, (uint16_t *)dW, lddw, V, K)
                    ? TG_OK
                    : TG_ERR_LAUNCH;
     Space s = {reinterpret_cast<char *>(ws)};

@@ -1,0 +1,218 @@
+"""Newton–Schulz update on the GPU against the 64-bit iteration.
+
+One step is held elementwise to the bound of its roundings
+(projection_oracle.newton_schulz_one_step_bound).  Five steps are held in the
+2-norm, per matrix, to 2^-8: what a result with every element off by the half
+step of a bfloat16 would be off by.  (The operands' binary16 roundings, 2^-12
+root mean square over a step and its few products, come to some 2^-11 of the
+norm: a fourth of that.)  The images of permutation matrices have closed forms
+and are held to single roundings."""
+import math
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+tg = pytest.importorskip("dense_fp16_gemm_02_amd")
+
+import projection_oracle as po  # noqa: E402
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+DT = {"f32": F32, "f16": F16, "bf16": BF16}
+C = (3.4445, -4.7750, 2.0315)
+
+
+def say(*a):
+    print("[gpu-case]", *a, file=sys.stderr, flush=True)
+
+
+def matrix(b, m, n, dt, seed=0, kind="noise", scale=1e-2):
+    gen = torch.Generator(device="cuda").manual_seed(seed + 31 * b + 7 * m + n)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    G = rnd(b, m, n)
+    if kind == "spikes":
+        r = min(8, m, n)
+        G = 0.2 * G + torch.matmul(rnd(b, m, r), rnd(b, r, n))
+    return (G * scale).to(dt)
+
+
+def norm_check(O, G, **kw):
+    want = po.newton_schulz(G, **kw)
+    off = (O.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1).clamp(min=1e-300)
+    assert bool((off <= 2.0 ** -8).all()), off
+    return off
+
+
+SIZES = [
+    (1, 1, 1), (1, 1, 200), (1, 200, 1), (3, 2, 2), (2, 16, 16), (1, 33, 77), (2, 100, 128), (4, 128, 128),
+    (1, 128, 129), (1, 129, 128), (2, 64, 300), (2, 300, 64), (1, 200, 1000), (1, 1000, 200), (1, 515, 513),
+    (1, 1000, 1000), (3, 700, 900), (2, 1300, 2000), (1, 2000, 1300), (1, 4097, 300), (1, 2500, 2500),
+    (4, 1536, 1600), (1, 4096, 4096), (2, 5000, 2304),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("b,m,n", SIZES)
+def test_five_steps(b, m, n, dt):
+    G = matrix(b, m, n, DT[dt])
+    say(b, m, n, dt, tg.tg_newton_schulz_plan(b, m, n))
+    O = tg.newton_schulz(G)
+    torch.cuda.synchronize()
+    assert O.dtype == BF16 and O.shape == G.shape
+    norm_check(O, G)
+
+
+@pytest.mark.parametrize("b,m,n", [(1, 100, 120), (1, 90, 300), (1, 300, 90), (2, 500, 700), (1, 1100, 900),
+                                   (1, 2300, 1100)])
+def test_one_step_elementwise(b, m, n):
+    for kind in ("noise", "spikes"):
+        G = matrix(b, m, n, BF16, seed=1, kind=kind)
+        say(b, m, n, kind)
+        O = tg.newton_schulz(G, steps=1)
+        want, tol = po.newton_schulz_one_step_bound(G)
+        bad = ~((O.double() - want).abs() <= tol)
+        assert not bool(bad.any()), (int(bad.sum()), float(((O.double() - want).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("n", [8, 64, 128, 192, 300, 1000])
+def test_permutations_keep_their_form(n):
+    """X = P/√n stays a multiple of P: the Gram matrix is diagonal, so only f32
+    arithmetic is met, and one rounding at the end."""
+    perm = torch.randperm(n, device="cuda")
+    G = torch.zeros(n, n, device="cuda", dtype=F32)
+    G[torch.arange(n, device="cuda"), perm] = 3.0
+    x = 1.0 / math.sqrt(n)
+    for _ in range(5):
+        x = C[0] * x + C[1] * x ** 3 + C[2] * x ** 5
+    O = tg.newton_schulz(G, eps=0.0)
+    on = O[torch.arange(n, device="cuda"), perm].double()
+    # X's image in the Gram product is rounded to 11 bits: relative 2·2^-12 of A per
+    # step (half a step at most 2^-11 of X), times the iteration's own slope
+    assert float((on / x - 1).abs().max()) <= 2.0 ** -8 + 40 * 2.0 ** -11
+    O[torch.arange(n, device="cuda"), perm] = 0
+    assert not O.any()
+
+
+def test_singular_values_and_vectors():
+    G = matrix(1, 300, 200, F32, seed=2)[0]
+    O = tg.newton_schulz(G).double()
+    s = torch.linalg.svdvals(O)
+    assert 0.6 < float(s.min()) and float(s.max()) < 1.3
+    U, _, Vh = torch.linalg.svd(G.double(), full_matrices=False)
+    core = U.t() @ O @ Vh.t()
+    off = core - torch.diag(core.diagonal())
+    assert float(off.norm() / core.norm()) <= 2.0 ** -8  # it acts on singular values alone
+
+
+def test_spectra_far_from_flat():
+    for b, m, n in ((1, 100, 128), (1, 600, 800), (1, 800, 600), (1, 2048, 2048)):
+        norm_check(tg.newton_schulz(matrix(b, m, n, BF16, seed=3, kind="spikes")),
+                   matrix(b, m, n, BF16, seed=3, kind="spikes"))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e4, 1e25])
+def test_scales(scale):
+    """Beyond f32's squares: the norm is taken in 64 bits."""
+    for b, m, n in ((1, 60, 70), (1, 200, 300)):
+        G = matrix(b, m, n, F32, seed=4, scale=scale)
+        norm_check(tg.newton_schulz(G, eps=0.0), G, eps=0.0)
+
+
+def test_coefficients_steps_and_eps():
+    co = [(3.4445, -4.7750, 2.0315), (3.0, -3.0, 1.0), (1.875, -1.25, 0.375)]
+    for b, m, n in ((1, 100, 90), (2, 200, 333)):
+        G = matrix(b, m, n, F16, seed=5)
+        norm_check(tg.newton_schulz(G, steps=3, coefficients=co), G, steps=3, coefficients=co)
+        norm_check(tg.newton_schulz(G, steps=2, coefficients=(1.5, -0.5, 0.0), eps=0.5), G, steps=2,
+                   coefficients=(1.5, -0.5, 0.0), eps=0.5)
+        X0 = po.newton_schulz(G, steps=0)
+        O = tg.newton_schulz(G, steps=0)
+        assert bool(((O.double() - X0).abs() <= (2.0 ** -8 + 2.0 ** -20) * X0.abs()).all())
+    with pytest.raises(ValueError, match="coefficients"):
+        tg.newton_schulz(G, steps=2, coefficients=co)
+    with pytest.raises(ValueError, match="steps"):
+        tg.newton_schulz(G, steps=40)
+
+
+@pytest.mark.parametrize("m,n", [(40, 50), (200, 150), (150, 200), (700, 600)])
+def test_zero_nan_and_infinity_stay_in_their_matrix(m, n):
+    G = matrix(5, m, n, F32, seed=6)
+    alone = tg.newton_schulz(G)
+    G2 = G.clone()
+    G2[0] = 0
+    G2[2, m // 2, n // 3] = float("nan")
+    G2[3, 1, 2] = float("inf")
+    O = tg.newton_schulz(G2)
+    assert not O[0].any() and torch.isnan(O[2]).all() and torch.isnan(O[3]).all()
+    assert torch.equal(O[1], alone[1]) and torch.equal(O[4], alone[4])
+    assert torch.isnan(tg.newton_schulz(G2, steps=0)[3]).all()
+    assert not tg.newton_schulz(G2[0], eps=0.0).any()
+
+
+@pytest.mark.parametrize("m,n", [(60, 50), (300, 170), (170, 300), (900, 640)])
+def test_strides_and_windows(m, n):
+    b = 3
+    big = torch.full((b, m + 3, n + 13), float("nan"), dtype=BF16, device="cuda")
+    G = big[:, 2:2 + m, 5:5 + n]
+    G.copy_(matrix(b, m, n, BF16, seed=7))
+    want = tg.newton_schulz(G.contiguous())
+    assert torch.equal(tg.newton_schulz(G), want)
+    room = torch.full((b, m + 3, n + 13), 9.0, dtype=BF16, device="cuda")
+    out = room[:, 2:2 + m, 5:5 + n]
+    assert tg.newton_schulz(G, out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, want)
+    out.fill_(9.0)
+    assert bool((room == 9.0).all())
+    # in place, and a single matrix of the batch
+    same = G.contiguous()
+    tg.newton_schulz(same, out=same)
+    assert torch.equal(same, want)
+    norm_check(tg.newton_schulz(G[1])[None], G[1:2])
+
+
+def test_repeated_calls_give_the_same_bits_and_streams_overlap():
+    cases = [matrix(b, m, n, F32, seed=8) for b, m, n in ((2, 100, 100), (1, 700, 500), (1, 1500, 1600), (1, 300, 2000))]
+    alone = [tg.newton_schulz(G) for G in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        got = []
+        for s, G in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(tg.newton_schulz(G))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, g) for a, g in zip(alone, got))
+
+
+@pytest.mark.parametrize("b,m,n", [(2, 100, 120), (1, 300, 500), (1, 900, 640)])
+def test_captured_and_replayed(b, m, n):
+    G = matrix(b, m, n, BF16, seed=9)
+    out = torch.zeros_like(G)
+    tg.newton_schulz(G, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tg.newton_schulz(G, out=out)
+    for seed in (10, 11, 12):
+        new = matrix(b, m, n, BF16, seed=seed)
+        G.copy_(new)
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, tg.newton_schulz(new))  # eager work between the replays
+
+
+def test_python_refusals():
+    G = matrix(2, 20, 30, BF16)
+    with pytest.raises(ValueError, match="contiguous"):
+        tg.newton_schulz(G[0].t())
+    with pytest.raises(ValueError, match="matrix"):
+        tg.newton_schulz(G[0, 0])
+    with pytest.raises(ValueError, match="out must"):
+        tg.newton_schulz(G, out=torch.empty_like(G, dtype=F32))
+    with pytest.raises(ValueError, match="overlapping"):
+        tg.newton_schulz(G, out=G[:1].expand(2, 20, 30))
+    assert tg.newton_schulz(G[:0]).shape == (0, 20, 30)
+    assert tg.newton_schulz(G[:, :0]).shape == (2, 0, 30)
