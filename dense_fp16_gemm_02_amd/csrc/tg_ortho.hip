@@ -155,31 +155,19 @@ struct SymArgs {
     const half_t *o;     // square: A's off-diagonal part and diagonal
     const float *d;
     float b, c;
-    int tri, total;      // tiles per matrix, in all
+    int tri, total;      // tiles per matrix, workgroups
+    float *part;         // gram in splits: [matrix][tile][split], each a tile in the accumulators' order
+    int splits, per_split;  // and the K of one (a multiple of 64)
 };
 template <typename T, bool SQUARE>
-__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void ns_sym_kernel(
-    SymArgs a)
+__device__ __attribute__((always_inline)) void sym_epilogue(const SymArgs &a, half_t *smem, int m, int tm, int tn,
+                                                            f32x4 (&acc)[T::TM][T::TN])
 {
-    static_assert(T::BM == T::BN && T::WTM == T::WTN, "symmetric tiles");
-    __shared__ __attribute__((aligned(1024))) half_t smem[T::LDS_ELEMS];
-    const int logical = xcd_contiguous(blockIdx.x, a.total);
-    const int m = logical / a.tri;
-    int tm, tn;
-    triangle_tile(logical - m * a.tri, tm, tn);
-    tm = __builtin_amdgcn_readfirstlane(tm), tn = __builtin_amdgcn_readfirstlane(tn);
-    const int m0 = tm * T::BM, n0 = tn * T::BN;
-    Operand x = a.x;
-    x.p = reinterpret_cast<const half_t *>(x.p) + (int64_t)m * a.x_stride;
-    f32x4 acc[T::TM][T::TN];
-    T::clear(acc);
-    T::run(smem, x, x, m0, n0, a.K, acc);
-
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / T::WN, wn = wave % T::WN;
     const int fr = lane & 15, fc = 4 * (lane >> 4);
-    const int r0 = m0 + wm * T::WTM, c0 = n0 + wn * T::WTN;
+    const int r0 = tm * T::BM + wm * T::WTM, c0 = tn * T::BN + wn * T::WTN;
     half_t *out = a.out + (int64_t)m * a.s * a.lds;
     float *__restrict__ diag = a.diag + (int64_t)m * a.lds;
     const half_t *__restrict__ o = SQUARE ? a.o + (int64_t)m * a.s * a.lds : nullptr;
@@ -242,6 +230,70 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     store_block<half_t, T::WTM, T::WTN, true>(stg, out, a.lds, r0, c0, a.s, (int)a.lds, true, nullptr, lane);
     if (tm != tn)
         store_block_transposed<half_t, T::WTM, T::WTN>(stg, out, a.lds, c0, r0, a.s, (int)a.lds, lane);
+}
+__device__ inline void sym_tile(const SymArgs &a, int logical, int &m, int &tm, int &tn)
+{
+    m = logical / a.tri;
+    triangle_tile(logical - m * a.tri, tm, tn);
+    tm = uniform(tm), tn = uniform(tn);
+}
+template <typename T, bool SQUARE>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void ns_sym_kernel(
+    SymArgs a)
+{
+    static_assert(T::BM == T::BN && T::WTM == T::WTN, "symmetric tiles");
+    __shared__ __attribute__((aligned(1024))) half_t smem[T::LDS_ELEMS];
+    int m, tm, tn;
+    sym_tile(a, xcd_contiguous(blockIdx.x, a.total), m, tm, tn);
+    Operand x = a.x;
+    x.p = reinterpret_cast<const half_t *>(x.p) + (int64_t)m * a.x_stride;
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    T::run(smem, x, x, tm * T::BM, tn * T::BN, a.K, acc);
+    sym_epilogue<T, SQUARE>(a, smem, m, tm, tn, acc);
+}
+// A short side of few tiles and a long one: the contraction in splits, one
+// workgroup each, and a second kernel that adds them in order and stores the tile.
+template <typename T>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(2) void ns_gram_split_kernel(SymArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) half_t smem[T::LDS_ELEMS];
+    const int logical = xcd_contiguous(blockIdx.x, a.total);
+    const int z = logical % a.splits;
+    int m, tm, tn;
+    sym_tile(a, logical / a.splits, m, tm, tn);
+    const int from = z * a.per_split, len = imax(imin(a.per_split, a.K - from), 0);
+    Operand x = a.x;
+    x.p = reinterpret_cast<const half_t *>(x.p) + (int64_t)m * a.x_stride + (T::TA ? (int64_t)from * x.ld : from);
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    if (len > 0)
+        T::run(smem, x, x, tm * T::BM, tn * T::BN, len, acc);
+    f32x4 *out = reinterpret_cast<f32x4 *>(a.part + (int64_t)logical * T::BM * T::BN) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j)
+            out[(i * T::TN + j) * T::THREADS] = acc[i][j];
+}
+template <typename T>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(2) void ns_gram_join_kernel(SymArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) half_t smem[T::BM * T::BN];
+    int m, tm, tn;
+    sym_tile(a, blockIdx.x, m, tm, tn);
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    const f32x4 *in =
+        reinterpret_cast<const f32x4 *>(a.part + (int64_t)blockIdx.x * a.splits * T::BM * T::BN) + threadIdx.x;
+#pragma unroll 2
+    for (int z = 0; z < a.splits; ++z, in += T::BM * T::BN / 4)
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::TN; ++j)
+                acc[i][j] += in[(i * T::TN + j) * T::THREADS];
+    sym_epilogue<T, false>(a, smem, m, tm, tn, acc);
 }
 
 // ------------------------------------------------------------------- update
@@ -628,6 +680,8 @@ struct Plan {
     int64_t s, l, ldx, lds;
     bool tall, small;
     Class gram, square, upd;
+    int splits;       // of the gram product's contraction
+    int64_t per_split;
     int norm_blocks;
 };
 int64_t triangle(int64_t s, int b)
@@ -652,6 +706,22 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
     const auto sym = [&](int b) { return batch * triangle(p.s, b); };
     p.gram = best(SYM_CLASS, sym, p.l);
     p.square = best(SYM_CLASS, sym, p.s);
+    // splits that fill the slots of a small class, at least 4 K-tiles each, where
+    // with the second kernel (some 5 us and the partial tiles twice through the
+    // caches) they are faster than the best class without
+    p.splits = 1, p.per_split = p.l;
+    const int64_t kt = cdiv(p.l, BK);
+    double t = tile_time(SYM_CLASS[p.gram], sym(SYM_CLASS[p.gram].bm), kt);
+    for (const Class c : {C128, C64}) {
+        const TileClass &k = SYM_CLASS[c];
+        const int64_t n = sym(k.bm), splits = std::min((int64_t)NUM_CU * k.per_cu / n, kt / 4);
+        if (splits < 2)
+            continue;
+        const int64_t per = cdiv(kt, splits), used = cdiv(kt, per);
+        const double with = tile_time(k, n * used, per) + 5.0 + (double)(n * used * k.bm * k.bm) * 8.0 / 4e6;
+        if (with < t)
+            t = with, p.gram = c, p.splits = (int)used, p.per_split = per * BK;
+    }
     p.upd = best(UPD_CLASS, [&](int b) { return batch * cdiv(rows, b) * cdiv(cols, b); }, p.s);
     const int64_t want = cdiv(rows * cols, 8192);
     p.norm_blocks = (int)std::max((int64_t)1, std::min(want, std::max((int64_t)1, std::min((int64_t)NORM_BLOCKS, 4096 / batch))));
@@ -659,7 +729,7 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
 }
 struct Buffers {
     double *part;
-    float *x, *d, *e;
+    float *x, *d, *e, *gram;
     half_t *xh[2], *o, *p;
     int64_t used = 0;
 };
@@ -679,6 +749,9 @@ Buffers lay_out(char *base, const Plan &p, int64_t batch, int64_t rows)
     take(b.xh[1], batch * rows * p.ldx);
     take(b.o, batch * p.s * p.lds);
     take(b.p, batch * p.s * p.lds);
+    take(b.gram, p.splits > 1 ? batch * triangle(p.s, SYM_CLASS[p.gram].bm) * p.splits * SYM_CLASS[p.gram].bm *
+                                    SYM_CLASS[p.gram].bm
+                              : 0);
     take(b.d, batch * p.lds);
     take(b.e, batch * p.lds);
     return b;
@@ -727,6 +800,15 @@ bool launch_sym(SymArgs a, int64_t batch, void *stream)
     a.tri = (int)triangle(a.s, Tl::BM);
     a.total = (int)(batch * a.tri);
     return launch(ns_sym_kernel<Tl, SQUARE>, a.total, Tl::THREADS, stream, a);
+}
+template <template <bool, bool> class T, bool TRANS>
+bool launch_gram_split(SymArgs a, int64_t batch, void *stream)
+{
+    using Tl = T<TRANS, TRANS>;
+    a.tri = (int)triangle(a.s, Tl::BM);
+    a.total = (int)(batch * a.tri * a.splits);
+    return launch(ns_gram_split_kernel<Tl>, a.total, Tl::THREADS, stream, a) &&
+           launch(ns_gram_join_kernel<T<false, false>>, batch * a.tri, Tl::THREADS, stream, a);
 }
 template <bool SQUARE, bool TRANS>
 bool launch_sym_class(Class c, const SymArgs &a, int64_t batch, void *stream)
@@ -783,8 +865,14 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         a.x_stride = rows * p.ldx;
         a.K = (int)(p.tall ? rows : round_up(cols, 8));
         a.s = (int)p.s, a.out = b.o, a.lds = p.lds, a.diag = b.d;
-        ok = p.tall ? launch_sym_class<false, true>(p.gram, a, batch, stream)
-                    : launch_sym_class<false, false>(p.gram, a, batch, stream);
+        a.part = b.gram, a.splits = p.splits, a.per_split = (int)p.per_split;
+        if (p.splits > 1 && p.gram == C128)
+            ok = p.tall ? launch_gram_split<T128, true>(a, batch, stream) : launch_gram_split<T128, false>(a, batch, stream);
+        else if (p.splits > 1)
+            ok = p.tall ? launch_gram_split<T64, true>(a, batch, stream) : launch_gram_split<T64, false>(a, batch, stream);
+        else
+            ok = p.tall ? launch_sym_class<false, true>(p.gram, a, batch, stream)
+                        : launch_sym_class<false, false>(p.gram, a, batch, stream);
         SymArgs q = {};
         q.x = {b.o, p.lds, (int)p.s};
         q.x_stride = p.s * p.lds;
@@ -857,7 +945,7 @@ extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, 
     if (name && name_len > 0 && p.small)
         snprintf(name, (size_t)name_len, "small_%d", p.l <= 64 ? 64 : 128);
     else if (name && name_len > 0)
-        snprintf(name, (size_t)name_len, "%s gram_%s square_%s update_%s", p.tall ? "tall" : "wide",
-                 CLASS_NAME[p.gram], CLASS_NAME[p.square], CLASS_NAME[p.upd]);
+        snprintf(name, (size_t)name_len, "%s gram_%s%s square_%s update_%s", p.tall ? "tall" : "wide",
+                 CLASS_NAME[p.gram], p.splits > 1 ? "_split" : "", CLASS_NAME[p.square], CLASS_NAME[p.upd]);
     return TG_OK;
 }

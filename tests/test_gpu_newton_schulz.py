@@ -48,7 +48,8 @@ SIZES = [
     (1, 1, 1), (1, 1, 200), (1, 200, 1), (3, 2, 2), (2, 16, 16), (1, 33, 77), (2, 100, 128), (4, 128, 128),
     (1, 128, 129), (1, 129, 128), (2, 64, 300), (2, 300, 64), (1, 200, 1000), (1, 1000, 200), (1, 515, 513),
     (1, 1000, 1000), (3, 700, 900), (2, 1300, 2000), (1, 2000, 1300), (1, 4097, 300), (1, 2500, 2500),
-    (4, 1536, 1600), (1, 4096, 4096), (2, 5000, 2304),
+    (4, 1536, 1600), (1, 4096, 4096), (2, 5000, 2304), (1, 16, 14336), (1, 14336, 16), (2, 300, 5000), (1, 900, 6001),
+    (1, 6001, 900), (1, 1100, 9000),
 ]
 
 

@@ -122,6 +122,7 @@ def test_every_tile_class_is_reached():
     for what in ("gram", "square", "update"):
         for c in ("256x256", "192x192", "128x128", "64x64"):
             assert f"{what}_{c}" in seen, (what, c)
+    assert {"gram_64x64_split", "gram_128x128_split"} <= seen
     assert {"small_64", "tall", "wide"} <= seen and tg.tg_newton_schulz_plan(1, 65, 3)[1] == "small_128"
 
 
