@@ -669,9 +669,19 @@ constexpr TileClass CLASS[] = {{256, 256, 1, 1.50, 1.50, 16.0},
                                {128, 128, 2, 1.10, 0.50, 6.0},
                                {64, 64, 2, 0.50, 0.27, 4.0},
                                {64, 128, 2, 0.80, 0.45, 5.0}};
+// `stream`: one row of tiles and a W larger than the 256 MB last-level cache, so
+// that each element of W comes from memory, once (100×50001×4096 92 -> 80 us,
+// 250×131072×2048 149 -> 126; a W that the cache still holds is read faster
+// without: 200×50001×1000 38 against 43).
 template <typename E, bool TA, bool TB, typename F>
-bool with_tile(Class c, F f)
+bool with_tile(Class c, bool stream, F f)
 {
+    if constexpr (!TA && !TB) {
+        if (stream && c == C256)
+            return f(Tile<E, 256, 256, 2, 2, 2, TA, TB, true>{});
+        if (stream && c == C128)
+            return f(Tile<E, 128, 128, 2, 2, 2, TA, TB, true>{});
+    }
     switch (c) {
     case C256:
         return f(Tile<E, 256, 256, 2, 2, 2, TA, TB>{});
@@ -709,6 +719,7 @@ struct Plan {
     bool pack_w, compact;
     int64_t K8, piece, pieces;
     Class logits, dh, dw;
+    bool stream;   // the logits' products
     int slots;     // workgroups that fill the chip, of dH's class
     int64_t room;  // rows of fp32 sums for dH
 };
@@ -732,6 +743,7 @@ Plan make_plan(const void *H, const void *W, int64_t M, int64_t V, int64_t K, in
     p.piece = most >= V ? V : round_up(most, 768);  // whole tiles of 256 and of 192
     p.pieces = cdiv(V, p.piece);
     p.logits = logits_class(M, p.piece, K);
+    p.stream = M <= CLASS[p.logits].bm && V * K * 2 > (int64_t)256 << 20;
     p.dw = best_class(p.piece, K, M);
     // dH's contraction is long, so its class is the one that runs a K-tile
     // fastest; the splits (dh_splits) take care of few tiles
@@ -894,7 +906,7 @@ int forward(const void *H, const void *W, const int64_t *target, float *loss, fl
         a.target = target, a.Vall = V;
         a.part = b.part, a.part_ld = M, a.at_target = b.at_target, a.arrived = &b.head->arrived;
         a.tiles_n = (int)cdiv(n, CLASS[p.logits].bn);
-        ok = ok && with_tile<E, false, false>(p.logits, [&](auto t) {
+        ok = ok && with_tile<E, false, false>(p.logits, p.stream, [&](auto t) {
             return launch(xent_stats_kernel<E, decltype(t)>, tiles(p.logits, M, n), t.THREADS, stream, a);
         });
     }
@@ -965,7 +977,7 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
         a.lse = b.lse, a.cp = b.cp, a.ct = b.ct;
         a.G = b.G, a.Gld = round_up(n, BK);
         a.tiles_n = (int)cdiv(n, CLASS[p.logits].bn);
-        ok = ok && with_tile<E, false, false>(p.logits, [&](auto t) {
+        ok = ok && with_tile<E, false, false>(p.logits, p.stream, [&](auto t) {
             return launch(xent_grad_kernel<E, decltype(t)>, tiles(p.logits, M, n), t.THREADS, stream, a);
         });
         if (dH) {
@@ -977,7 +989,7 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
             d.vec = lddh % 8 == 0 && (uintptr_t)dH % 16 == 0;
             d.bm = CLASS[p.dh].bm, d.tiles_n = (int)cdiv(K, CLASS[p.dh].bn), d.slots = p.slots;
             const int64_t g = std::max(tiles(p.dh, M, K), (int64_t)p.slots);
-            ok = ok && with_tile<E, false, true>(p.dh, [&](auto t) {
+            ok = ok && with_tile<E, false, true>(p.dh, false, [&](auto t) {
                 return launch(xent_dh_kernel<E, decltype(t)>, g, t.THREADS, stream, d);
             });
         }
@@ -990,7 +1002,7 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
             x.V = (int)n, x.K = (int)K;
             x.vec = lddw % 8 == 0 && (uintptr_t)dW % 16 == 0;
             x.tiles_m = (int)cdiv(n, CLASS[p.dw].bm), x.tiles_n = (int)cdiv(K, CLASS[p.dw].bn);
-            ok = ok && with_tile<E, true, true>(p.dw, [&](auto t) {
+            ok = ok && with_tile<E, true, true>(p.dw, false, [&](auto t) {
                 return launch(xent_dw_kernel<E, decltype(t)>, tiles(p.dw, n, K), t.THREADS, stream, x);
             });
         }
@@ -1064,11 +1076,12 @@ extern "C" int tg_xent_plan(const void *H, const void *W, int64_t M, int64_t V, 
         *pieces = p.pieces;
     if (name && name_len > 0) {
         const char *pre = p.compact ? "gather " : "", *pack = p.pack_w ? "pack " : "";
+        const char *how = p.stream && (p.logits == C256 || p.logits == C128) ? "_stream" : "";
         if (backward_pass)
-            snprintf(name, (size_t)name_len, "%s%sgrad_%s dh_%s dw_%s", pre, pack, CLASS_NAME[p.logits],
+            snprintf(name, (size_t)name_len, "%s%sgrad_%s%s dh_%s dw_%s", pre, pack, CLASS_NAME[p.logits], how,
                      CLASS_NAME[p.dh], CLASS_NAME[p.dw]);
         else
-            snprintf(name, (size_t)name_len, "%s%sstats_%s", pre, pack, CLASS_NAME[p.logits]);
+            snprintf(name, (size_t)name_len, "%s%sstats_%s%s", pre, pack, CLASS_NAME[p.logits], how);
     }
     return TG_OK;
 }

@@ -61,6 +61,7 @@ SHAPES = [
     (1, 1, 1), (1, 2, 8), (2, 1, 3), (1, 100, 64), (3, 7, 5), (63, 129, 64), (64, 128, 72), (65, 130, 200),
     (100, 77, 65), (128, 4096, 8), (17, 16385, 40), (64, 20000, 264), (1, 33000, 520), (200, 1000, 1001),
     (333, 5001, 248), (576, 16000, 64), (700, 700, 700), (1300, 9000, 192), (2049, 12001, 136), (3000, 131072, 64),
+    (100, 34000, 4104), (250, 140001, 1032),  # streamed weights of more than the last-level cache
 ]
 
 

@@ -94,6 +94,9 @@ def test_logits_are_not_kept():
     ((A, A, 1, 28672, 8192, 8192, 8192), False, "stats_64x128"),
     ((A, A, 1000, 1000, 1000, 1000, 1000), False, "stats_64x64"),
     ((A, A, 333, 50001, 1000, 1000, 1000), True, "grad_128x128"),
+    ((A, A, 100, 50001, 4096, 4096, 4096), True, "grad_128x128_stream"),
+    ((A, A, 250, 131072, 2048, 2048, 2048), False, "stats_256x256_stream"),
+    ((A, A, 100, 50001, 1024, 1024, 1024), True, "grad_128x128 "),
     ((A + 2, A, 16, 100, 64, 64, 64), False, "gather"),      # H not aligned
     ((A, A + 2, 16, 100, 64, 64, 64), False, "pack"),        # W not aligned
     ((A, A, 16, 100, 63, 64, 64), True, "pack"),             # K not a multiple of 8
