@@ -466,19 +466,33 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallAr
     // X in the accumulators' layout: block (i, j), row fr, columns 4·fh .. +3
     f32x4 x[TM][TN];
     double s2 = 0.0;
+    typedef G four __attribute__((ext_vector_type(4)));
+    const bool rows4 = !a.flip && a.ld % 4 == 0 && (uintptr_t)g % sizeof(four) == 0;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int r = r0 + 16 * i + fr, c = c0 + 16 * j + 4 * fh;
+            x[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (rows4 && r < a.s && c + 4 <= a.l) {
+                const four v = *reinterpret_cast<const four *>(g + r * a.ld + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[i][j][k] = (float)v[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (r < a.s && c + k < a.l)
+                        x[i][j][k] = (float)g[a.flip ? (c + k) * a.ld + r : r * a.ld + c + k];
+            }
+        }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int r = r0 + 16 * i + fr, c = c0 + 16 * j + 4 * fh + v;
-                float f = 0.0f;
-                if (r < a.s && c < a.l)
-                    f = (float)g[a.flip ? c * a.ld + r : r * a.ld + c];
-                x[i][j][v] = f;
-                s2 += (double)f * (double)f;
-            }
+            for (int v = 0; v < 4; ++v)
+                s2 += (double)x[i][j][v] * (double)x[i][j][v];
     for (int o = 32; o; o >>= 1)
         s2 += __shfl_xor(s2, o);
     if (lane == 0)
@@ -638,16 +652,25 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallAr
         __syncthreads();  // every wave has read X's image
     }
     __bf16 *out = a.out + (int64_t)blockIdx.x * a.o_stride;
+    const bool out4 = !a.flip && a.ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < TN; ++j) {
+            const int r = r0 + 16 * i + fr, c = c0 + 16 * j + 4 * fh;
+            El<__bf16>::v4 h;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int r = r0 + 16 * i + fr, c = c0 + 16 * j + 4 * fh + v;
-                if (r < a.s && c < a.l)
-                    out[a.flip ? c * a.ldo + r : r * a.ldo + c] = (__bf16)x[i][j][v];
+            for (int k = 0; k < 4; ++k)
+                h[k] = (__bf16)x[i][j][k];
+            if (out4 && r < a.s && c + 4 <= a.l) {
+                *reinterpret_cast<El<__bf16>::v4 *>(out + r * a.ldo + c) = h;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (r < a.s && c + k < a.l)
+                        out[a.flip ? (c + k) * a.ldo + r : r * a.ldo + c + k] = h[k];
             }
+        }
 }
 
 // -------------------------------------------------------------------- plans

@@ -309,6 +309,19 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
     return (loss, lse) if return_lse else loss
 
 
+@functools.lru_cache(maxsize=1024)
+def _ns_size(batch, rows, cols):
+    return _lib().tg_newton_schulz_workspace_bytes(batch, rows, cols)
+
+
+@functools.lru_cache(maxsize=64)
+def _coefficients(triples, steps):
+    """The C array of 3·steps coefficients."""
+    if len(triples) != steps or any(len(t) != 3 for t in triples):
+        raise ValueError("coefficients is one (a, b, c), or one for each step")
+    return (ctypes.c_float * max(1, 3 * steps))(*(float(x) for t in triples for x in t))
+
+
 def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=None):
     """Orthogonalised update: X ← a·X + (b·A + c·A²)·X, A = X·Xᵀ, ``steps`` times
     from X = G / (‖G‖_F + eps), for a matrix or a batch of matrices.
@@ -334,12 +347,10 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
         raise ValueError("G must be a matrix or a batch of matrices")
     if not 0 <= steps <= TG_NS_MAX_STEPS:
         raise ValueError(f"steps is 0 to {TG_NS_MAX_STEPS}")
-    flat = None
+    c = None
     if coefficients is not None:
-        flat = [float(x) for c in coefficients for x in c] if steps and hasattr(coefficients[0], "__len__") \
-            else [float(x) for x in coefficients] * steps
-        if len(flat) != 3 * steps:
-            raise ValueError("coefficients is one (a, b, c), or one for each step")
+        per_step = steps > 0 and hasattr(coefficients[0], "__len__")
+        c = _coefficients(tuple(map(tuple, coefficients)) if per_step else (tuple(coefficients),) * steps, steps)
     if out is None:
         out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
     elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
@@ -352,13 +363,12 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     if batch > 1 and o.stride(0) < (rows - 1) * ldo + cols:
         raise ValueError("out has overlapping matrices")
     lib = _lib()
-    size = lib.tg_newton_schulz_workspace_bytes(batch, rows, cols)
-    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=G.device)
+    size = _ns_size(batch, rows, cols)
+    ws = torch.empty(size, dtype=torch.uint8, device=G.device) if size > 0 else None
     fn = {torch.float32: lib.tg_newton_schulz_f32, torch.float16: lib.tg_newton_schulz_f16,
           torch.bfloat16: lib.tg_newton_schulz_bf16}[G.dtype]
-    c = None if flat is None else (ctypes.c_float * max(1, len(flat)))(*flat)
     args = (g.data_ptr(), o.data_ptr(), batch, rows, cols, ldg, g.stride(0) if batch > 1 else rows * ldg, ldo,
-            o.stride(0) if batch > 1 else rows * ldo, steps, c, eps, ws.data_ptr(), max(size, 0),
+            o.stride(0) if batch > 1 else rows * ldo, steps, c, eps, _p(ws), max(size, 0),
             torch.cuda.current_stream(G.device).cuda_stream)
     if torch.cuda.current_device() == G.device.index:
         st = fn(*args)
