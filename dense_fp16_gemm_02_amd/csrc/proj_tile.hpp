@@ -652,6 +652,9 @@ inline int gfx950_status()
     return s;
 }
 
+// A launch holds fewer than 2^32 threads; workgroups here have at most 512 where
+// their number grows with the problem.
+constexpr int64_t MAX_GRID = (int64_t)1 << 23;
 template <typename... P, typename... A>
 inline bool launch(void (*fn)(P...), int64_t grid, int threads, void *stream, A... args)
 {
@@ -661,6 +664,8 @@ inline bool launch(void (*fn)(P...), int64_t grid, int threads, void *stream, A.
         int i = 0;
         ((argv[i++] = (void *)&x), ...);
     }, held);
+    if (grid * threads >= (int64_t)1 << 32)
+        return false;
     return hipLaunchKernel(reinterpret_cast<const void *>(fn), dim3((unsigned)grid), dim3(threads), argv, 0,
                            (hipStream_t)stream) == hipSuccess;
 }

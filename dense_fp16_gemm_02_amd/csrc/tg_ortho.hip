@@ -406,35 +406,190 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
                                             (int)a.ldx, true, nullptr, lane);
 }
 
-// ------------------------------------------------------------ small matrices
-// Both sides at most 128: one workgroup runs the whole iteration with X (fp32) in
-// registers and the operands in LDS; nothing but G and the result touches
-// memory.  As separate launches such a matrix pays some 4 us for each of 17
-// kernels that compute for well under one.  The IM×IM image is as wide as it is
-// high, so the shorter side is made the rows on loading (`flip`) and no other
-// form is needed.  128: eight waves (2×4, two to a SIMD) of 64×32; 64: four of
-// 32×32.
+// --------------------------------------------------- short sides of up to 128
+// With s at most 128 the s×s operands fit one workgroup's LDS, and launches, not
+// arithmetic, are what the chain of products above costs (some 4 us each for well
+// under one of work).  Two forms:
+//
+//   both sides at most 128   one workgroup runs the whole iteration, X (fp32)
+//                            in registers, the operands in LDS: 128x128 27 us
+//                            with the chain 65, 64x64 18 us;
+//   a long side              two launches per step, and X read and written once
+//                            in it.  The strip kernel takes X in strips of 64
+//                            columns: update, store, and the strip's part of the
+//                            next Gram matrix, from the image it already holds.
+//                            The core kernel adds the parts and, in the workgroup
+//                            that finishes last, does the square: 1x64x4096 66 us
+//                            with the chain 95, of which the core's wait for
+//                            memory, three trips there one after the other, is
+//                            the longest part (8 us of each step's 13).
+//
+// X is held with the shorter side as rows (`flip`: G and the result are
+// transposed on the way), so that no other form is needed.  Images are IM rows,
+// 64 or 128.
 //
 // The rounding of X's operand spreads evenly over the s directions of the
 // short side, and a direction whose singular value is small beside the norm is
 // amplified by up to 485 afterwards: with 64 and more of them that stays below
 // the result's own rounding, with a few it does not (a 2×2 matrix of condition
-// 100 came out 6e-3 off).  The 64×64 form therefore holds each operand as the
-// sum of two binary16 values and takes three products for each (the fourth, of
-// the two low parts, is below fp32).
+// 100 came out 6e-3 off).  The forms for 64 rows therefore hold each operand as
+// the sum of two binary16 values and take three products for each (the fourth,
+// of the two low parts, is below fp32).
 //
-// LDS images are row-major; chunk c of row r at c ^ swz(r), so that the sixteen
-// rows of a K-major fragment read fall on sixteen bank groups; the transposed
-// reads of X (two rows to a 32-byte group) take two passes.
+// LDS images are row-major, C columns; chunk c of row r at c ^ swz(r), so that the
+// sixteen rows of a K-major fragment read fall on sixteen bank groups; the
+// transposed reads of X (two rows to a 32-byte group) take two passes.
+using V8h = El<half_t>::v8;
+template <int C>
+__host__ __device__ constexpr int image_off(int r, int c)
+{
+    return r * C + (((c >> 3) ^ (C == 128 ? r & 15 : (r >> 1) & 7)) << 3) + (c & 7);
+}
+template <int C>
+__device__ inline V8h image_kmajor(const half_t *img, int row, int kk, int fr, int fh)
+{
+    return *reinterpret_cast<const V8h *>(img + image_off<C>(row + fr, kk * 32 + 8 * fh));
+}
+template <int C>
+__device__ inline V8h image_trans(const half_t *img, int col, int kk, int fr, int fh)
+{
+    const int k = kk * 32 + 8 * fh + (fr >> 2), c = col + 4 * (fr & 3);
+    union {
+        s16x4 h[2];
+        V8h v;
+    } u;
+    u.h[0] = lds_read_tr(img + image_off<C>(k, c));
+    u.h[1] = lds_read_tr(img + image_off<C>(k + 4, c));
+    return u.v;
+}
+// acc += the block at row r0, column c0 of A·Bᵀ (B K-major) or A·B (TRANS), over
+// 32·KK of K; a_part, b_part: where the low parts begin.
+template <int PARTS, int CA, int CB, bool TRANS, int KK, int TM, int TN>
+__device__ inline void image_product(const half_t *ai, int a_part, const half_t *bi, int b_part, int r0, int c0,
+                                     int fr, int fh, f32x4 (&acc)[TM][TN])
+{
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+        V8h fa[PARTS][TM], fb[PARTS][TN];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                fa[p][i] = image_kmajor<CA>(ai + p * a_part, r0 + 16 * i, kk, fr, fh);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                fb[p][j] = TRANS ? image_trans<CB>(bi + p * b_part, c0 + 16 * j, kk, fr, fh)
+                                 : image_kmajor<CB>(bi + p * b_part, c0 + 16 * j, kk, fr, fh);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                acc[i][j] = El<half_t>::mfma(fb[0][j], fa[0][i], acc[i][j]);
+                if constexpr (PARTS == 2) {
+                    acc[i][j] = El<half_t>::mfma(fb[1][j], fa[0][i], acc[i][j]);
+                    acc[i][j] = El<half_t>::mfma(fb[0][j], fa[1][i], acc[i][j]);
+                }
+            }
+    }
+}
+// v at row r, columns c .. c+3 as the operand's image holds it; returns the value
+// held.
+template <int PARTS, int C>
+__device__ inline f32x4 image_put(half_t *img, int part, int r, int c, const f32x4 &v)
+{
+    half4 h;
+    f32x4 held;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        h[k] = (half_t)v[k];
+        held[k] = (float)h[k];
+    }
+    *reinterpret_cast<half4 *>(img + image_off<C>(r, c)) = h;
+    if constexpr (PARTS == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = (half_t)(v[k] - held[k]);
+            held[k] += (float)h[k];
+        }
+        *reinterpret_cast<half4 *>(img + part + image_off<C>(r, c)) = h;
+    }
+    return held;
+}
+template <int TM, int TN>
+__device__ inline void zero_blocks(f32x4 (&acc)[TM][TN])
+{
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// The s×s part of a step for one workgroup: waves 2 × WN over the IM×IM image.
 template <int IM>
 struct Small {
     static constexpr int WM = 2, WN = IM == 128 ? 4 : 2, WAVES = WM * WN;
     static constexpr int TM = IM / WM / 16, TN = IM / WN / 16;
-    static constexpr int PARTS = IM == 128 ? 1 : 2;
+    static constexpr int PARTS = IM == 128 ? 1 : 2, PART = IM * IM;
     static_assert(IM == 128 || IM == 64, "two forms");
-    __host__ __device__ static constexpr int off(int r, int c)
+    struct Core {
+        half_t oi[PARTS * PART], pi[PARTS * PART];
+        float d[IM], e[IM];
+    };
+    // acc: X·Xᵀ of the X_SCALE images.  Leaves P and e in `m`; two barriers, and
+    // the caller passes one before it reads them.
+    __device__ static void square(Core &m, f32x4 (&acc)[TM][TN], float kb, float kc, int r0, int c0, int fr, int fh)
     {
-        return r * IM + (((c >> 3) ^ (IM == 128 ? r & 15 : (r >> 1) & 7)) << 3) + (c & 7);
+        f32x4 o[TM][TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    o[i][j][v] = acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE));
+                if (r0 + 16 * i == c0 + 16 * j)  // a block of the diagonal
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (fr == 4 * fh + v) {
+                            m.d[r0 + 16 * i + fr] = acc[i][j][v] * (1.0f / (X_SCALE * X_SCALE));
+                            o[i][j][v] = 0.0f;
+                        }
+                o[i][j] = image_put<PARTS, IM>(m.oi, PART, r0 + 16 * i + fr, c0 + 16 * j + 4 * fh, o[i][j]);
+            }
+        __syncthreads();
+        zero_blocks(acc);
+        image_product<PARTS, IM, IM, false, IM / 32>(m.oi, PART, m.oi, PART, r0, c0, fr, fh, acc);
+        float dr[TM];
+        f32x4 dc[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            dr[i] = m.d[r0 + 16 * i + fr];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            dc[j] = *reinterpret_cast<const f32x4 *>(m.d + c0 + 16 * j + 4 * fh);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                f32x4 h;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float f = o[i][j][v], y = acc[i][j][v] * (1.0f / S_SCALE);
+                    h[v] = kb * f + kc * ((dr[i] + dc[j][v]) * f + y);
+                }
+                if (r0 + 16 * i == c0 + 16 * j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (fr == 4 * fh + v) {
+                            m.e[r0 + 16 * i + fr] =
+                                kb * dr[i] + kc * (dr[i] * dr[i] + acc[i][j][v] * (1.0f / (S_SCALE * S_SCALE)));
+                            h[v] = 0.0f;
+                        }
+                image_put<PARTS, IM>(m.pi, PART, r0 + 16 * i + fr, c0 + 16 * j + 4 * fh, h);
+            }
+        __syncthreads();
     }
 };
 struct SmallArgs {
@@ -451,11 +606,10 @@ struct SmallArgs {
 template <typename G, int IM>
 __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallArgs a)
 {
-    using V8 = El<half_t>::v8;
     using S = Small<IM>;
     constexpr int TM = S::TM, TN = S::TN, PARTS = S::PARTS;
-    __shared__ __attribute__((aligned(1024))) half_t xi[PARTS * IM * IM], oi[PARTS * IM * IM], pi[PARTS * IM * IM];
-    __shared__ __attribute__((aligned(16))) float d[IM], e[IM];
+    __shared__ __attribute__((aligned(1024))) half_t xi[PARTS * IM * IM];
+    __shared__ __attribute__((aligned(1024))) typename S::Core m;
     __shared__ double sums[S::WAVES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -510,75 +664,8 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallAr
             for (int v = 0; v < 4; ++v)
                 x[i][j][v] = (float)((double)x[i][j][v] * inv);
 
-    auto kmajor = [&](const half_t *img, int row, int kk) {
-        return *reinterpret_cast<const V8 *>(img + S::off(row + fr, kk * 32 + 8 * fh));
-    };
-    auto trans = [&](const half_t *img, int col, int kk) {
-        const int k = kk * 32 + 8 * fh + (fr >> 2), c = col + 4 * (fr & 3);
-        union {
-            s16x4 h[2];
-            V8 v;
-        } u;
-        u.h[0] = lds_read_tr(img + S::off(k, c));
-        u.h[1] = lds_read_tr(img + S::off(k + 4, c));
-        return u.v;
-    };
-    // acc = the wave's block of A·Bᵀ (B K-major) or A·B (transposed reads)
-    auto product = [&](const half_t *ai, const half_t *bi, auto transposed, f32x4(&acc)[TM][TN]) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kk = 0; kk < IM / 32; ++kk) {
-            V8 fa[PARTS][TM], fb[PARTS][TN];
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    fa[p][i] = kmajor(ai + p * IM * IM, r0 + 16 * i, kk);
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    fb[p][j] = decltype(transposed)::value ? trans(bi + p * IM * IM, c0 + 16 * j, kk)
-                                                           : kmajor(bi + p * IM * IM, c0 + 16 * j, kk);
-            }
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    acc[i][j] = El<half_t>::mfma(fb[0][j], fa[0][i], acc[i][j]);
-                    if constexpr (PARTS == 2) {
-                        acc[i][j] = El<half_t>::mfma(fb[1][j], fa[0][i], acc[i][j]);
-                        acc[i][j] = El<half_t>::mfma(fb[0][j], fa[1][i], acc[i][j]);
-                    }
-                }
-        }
-    };
-    // v as the operand's image holds it; returns the value held
-    auto put = [&](half_t *img, int i, int j, const f32x4 &v) {
-        half4 h;
-        f32x4 held;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = (half_t)v[k];
-            held[k] = (float)h[k];
-        }
-        const int at = S::off(r0 + 16 * i + fr, c0 + 16 * j + 4 * fh);
-        *reinterpret_cast<half4 *>(img + at) = h;
-        if constexpr (PARTS == 2) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h[k] = (half_t)(v[k] - held[k]);
-                held[k] += (float)h[k];
-            }
-            *reinterpret_cast<half4 *>(img + IM * IM + at) = h;
-        }
-        return held;
-    };
 #pragma unroll 1
     for (int t = 0; t < a.steps; ++t) {
-        const float ka = a.k[3 * t], kb = a.k[3 * t + 1], kc = a.k[3 * t + 2];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -587,62 +674,18 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallAr
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     v[k] = x[i][j][k] * X_SCALE;
-                put(xi, i, j, v);
+                image_put<PARTS, IM>(xi, S::PART, r0 + 16 * i + fr, c0 + 16 * j + 4 * fh, v);
             }
         __syncthreads();
-        f32x4 acc[TM][TN], o[TM][TN];
-        product(xi, xi, std::false_type{}, acc);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    o[i][j][v] = acc[i][j][v] * (S_SCALE / (X_SCALE * X_SCALE));
-                if (r0 + 16 * i == c0 + 16 * j)  // a block of the diagonal
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (fr == 4 * fh + v) {
-                            d[r0 + 16 * i + fr] = acc[i][j][v] * (1.0f / (X_SCALE * X_SCALE));
-                            o[i][j][v] = 0.0f;
-                        }
-                o[i][j] = put(oi, i, j, o[i][j]);
-            }
-        __syncthreads();
-        product(oi, oi, std::false_type{}, acc);
-        float dr[TM];
-        f32x4 dc[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            dr[i] = d[r0 + 16 * i + fr];
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            dc[j] = *reinterpret_cast<const f32x4 *>(d + c0 + 16 * j + 4 * fh);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                f32x4 h;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float f = o[i][j][v], y = acc[i][j][v] * (1.0f / S_SCALE);
-                    h[v] = kb * f + kc * ((dr[i] + dc[j][v]) * f + y);
-                }
-                if (r0 + 16 * i == c0 + 16 * j)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (fr == 4 * fh + v) {
-                            e[r0 + 16 * i + fr] =
-                                kb * dr[i] + kc * (dr[i] * dr[i] + acc[i][j][v] * (1.0f / (S_SCALE * S_SCALE)));
-                            h[v] = 0.0f;
-                        }
-                put(pi, i, j, h);
-            }
-        __syncthreads();
-        product(pi, xi, std::true_type{}, acc);
+        f32x4 acc[TM][TN];
+        zero_blocks(acc);
+        image_product<PARTS, IM, IM, false, IM / 32>(xi, S::PART, xi, S::PART, r0, c0, fr, fh, acc);
+        S::square(m, acc, a.k[3 * t + 1], a.k[3 * t + 2], r0, c0, fr, fh);
+        zero_blocks(acc);
+        image_product<PARTS, IM, IM, true, IM / 32>(m.pi, S::PART, xi, S::PART, r0, c0, fr, fh, acc);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const float f = ka + e[r0 + 16 * i + fr];
+            const float f = a.k[3 * t] + m.e[r0 + 16 * i + fr];
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -673,6 +716,249 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallAr
         }
 }
 
+// ------------------------------------------------- a short and a long side
+constexpr int STRIP = 64;  // columns
+struct ThinArgs {
+    const void *g;
+    int64_t ld, g_stride;
+    __bf16 *out;
+    int64_t ldo, o_stride;
+    int s, l;
+    bool flip;
+    const double *part;      // sums of squares
+    int norm_blocks;
+    float eps;
+    float *x;                // [matrix][s][lp], lp = l rounded up to whole strips
+    int64_t lp;
+    int strips, per, groups; // strips per matrix, per workgroup, workgroups per matrix
+    float *gram;             // [matrix][group][IM·IM], the accumulators' order
+    float *sum;              // [matrix][IM·IM]
+    half_t *p;               // [matrix][PARTS·IM·IM], the image's order
+    float *e;                // [matrix][IM]
+    unsigned *arrived;       // [matrix]
+    int reducers;            // core workgroups per matrix
+    float ka, kb, kc;
+};
+// FIRST: X from G.  LAST: the result, and no Gram matrix.  (Both: no steps.)
+template <typename G, int IM, bool FIRST, bool LAST>
+__global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_strip_kernel(ThinArgs a)
+{
+    using S = Small<IM>;
+    constexpr int PARTS = S::PARTS, THREADS = S::WAVES * 64;
+    constexpr int TM = S::TM, TN = STRIP / S::WN / 16;  // a wave's blocks of a strip
+    __shared__ __attribute__((aligned(1024))) half_t xi[PARTS * IM * STRIP];
+    __shared__ __attribute__((aligned(1024))) half_t pi[FIRST ? 8 : PARTS * IM * IM];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, fh = lane >> 4;
+    const int m = blockIdx.x / a.groups, group = blockIdx.x % a.groups;
+    const int r0 = wave / S::WN * (IM / S::WM), c0 = wave % S::WN * (STRIP / S::WN);
+    const int g0 = wave % S::WN * (IM / S::WN);  // the wave's columns of the Gram matrix
+    if (threadIdx.x == 0 && group == 0)
+        a.arrived[m] = 0;
+    double inv = 0.0;
+    if constexpr (FIRST) {
+        double s2 = 0.0;
+        for (int i = lane; i < a.norm_blocks; i += 64)
+            s2 += a.part[m * a.norm_blocks + i];
+        for (int o = 32; o; o >>= 1)
+            s2 += __shfl_xor(s2, o);
+        inv = inverse(sqrt(s2) + (double)a.eps);
+    } else {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.p + (int64_t)m * PARTS * IM * IM);
+#pragma unroll
+        for (int i = 0; i < PARTS * IM * IM / 8 / THREADS; ++i)
+            reinterpret_cast<uint4 *>(pi)[i * THREADS + threadIdx.x] = src[i * THREADS + threadIdx.x];
+    }
+    float er[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+        er[i] = FIRST ? 0.0f : a.ka + a.e[m * IM + r0 + 16 * i + fr];
+    const G *g = reinterpret_cast<const G *>(a.g) + (int64_t)m * a.g_stride;
+    float *xm = a.x + (int64_t)m * a.s * a.lp;
+    __bf16 *out = a.out + (int64_t)m * a.o_stride;
+    typedef G four __attribute__((ext_vector_type(4)));
+    const bool g4 = !a.flip && a.ld % 4 == 0 && (uintptr_t)g % sizeof(four) == 0;
+    const bool out4 = !a.flip && a.ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
+    f32x4 gram[S::TM][S::TN];
+    zero_blocks(gram);
+#pragma unroll 1
+    for (int q = group * a.per; q < imin((group + 1) * a.per, a.strips); ++q) {
+        f32x4 x[TM][TN];
+        zero_blocks(x);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int r = r0 + 16 * i + fr;
+                const int64_t c = (int64_t)q * STRIP + c0 + 16 * j + 4 * fh;
+                if (r >= a.s)
+                    continue;
+                if constexpr (!FIRST) {
+                    x[i][j] = *reinterpret_cast<const f32x4 *>(xm + r * a.lp + c);
+                } else if (g4 && c + 4 <= a.l) {
+                    const four v = *reinterpret_cast<const four *>(g + r * a.ld + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[i][j][k] = (float)((double)(float)v[k] * inv);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c + k < a.l)
+                            x[i][j][k] = (float)((double)(float)g[a.flip ? (c + k) * a.ld + r : r * a.ld + c + k] * inv);
+                }
+            }
+        auto put = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    f32x4 v;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = x[i][j][k] * X_SCALE;
+                    image_put<PARTS, STRIP>(xi, IM * STRIP, r0 + 16 * i + fr, c0 + 16 * j + 4 * fh, v);
+                }
+        };
+        if constexpr (!FIRST) {
+            put();
+            __syncthreads();
+            f32x4 acc[TM][TN];
+            zero_blocks(acc);
+            image_product<PARTS, IM, STRIP, true, IM / 32>(pi, IM * IM, xi, IM * STRIP, r0, c0, fr, fh, acc);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[i][j][k] = er[i] * x[i][j][k] + acc[i][j][k] * (1.0f / (S_SCALE * X_SCALE));
+            __syncthreads();  // every wave has read the image
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int r = r0 + 16 * i + fr;
+                const int64_t c = (int64_t)q * STRIP + c0 + 16 * j + 4 * fh;
+                if (r >= a.s)
+                    continue;
+                if constexpr (!LAST) {
+                    *reinterpret_cast<f32x4 *>(xm + r * a.lp + c) = x[i][j];
+                } else {
+                    El<__bf16>::v4 h;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = (__bf16)x[i][j][k];
+                    if (out4 && c + 4 <= a.l) {
+                        *reinterpret_cast<El<__bf16>::v4 *>(out + r * a.ldo + c) = h;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (c + k < a.l)
+                                out[a.flip ? (c + k) * a.ldo + r : r * a.ldo + c + k] = h[k];
+                    }
+                }
+            }
+        if constexpr (!LAST) {
+            put();
+            __syncthreads();
+            image_product<PARTS, STRIP, STRIP, false, STRIP / 32>(xi, IM * STRIP, xi, IM * STRIP, r0, g0, fr, fh, gram);
+            __syncthreads();
+        }
+    }
+    if constexpr (!LAST) {
+        f32x4 *dst = reinterpret_cast<f32x4 *>(a.gram + ((int64_t)m * a.groups + group) * IM * IM) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+                dst[(i * S::TN + j) * THREADS] = gram[i][j];
+    }
+}
+// Adds the groups' Gram matrices (each workgroup a range of elements, in the
+// groups' order), and in the workgroup that arrives last squares the sum.
+template <int IM>
+__global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_core_kernel(ThinArgs a)
+{
+    using S = Small<IM>;
+    constexpr int THREADS = S::WAVES * 64, PARTS = S::PARTS;
+    __shared__ __attribute__((aligned(1024))) typename S::Core core;
+    __shared__ bool last;
+    const int m = blockIdx.x / a.reducers, part = blockIdx.x % a.reducers;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, fh = lane >> 4;
+    const int r0 = wave / S::WN * (IM / S::WM), c0 = wave % S::WN * (IM / S::WN);
+    const f32x4 *in = reinterpret_cast<const f32x4 *>(a.gram + (int64_t)m * a.groups * IM * IM);
+    constexpr int n = IM * IM / 4;
+    f32x4 acc[S::TM][S::TN];
+    if (a.reducers == 1) {
+        zero_blocks(acc);
+        for (int z = 0; z < a.groups; ++z)
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int j = 0; j < S::TN; ++j)
+                    acc[i][j] += in[(int64_t)z * n + (i * S::TN + j) * THREADS + threadIdx.x];
+    } else {
+        // this workgroup's elements, the groups in `slices` parts side by side
+        unsigned long long *sum = reinterpret_cast<unsigned long long *>(a.sum) + (int64_t)m * n * 2;
+        const int each = n / a.reducers, width = imin(each, THREADS), slices = THREADS / width;
+        const int slice = threadIdx.x / width, z0 = slice * a.groups / slices, z1 = (slice + 1) * a.groups / slices;
+        f32x4 *joined = reinterpret_cast<f32x4 *>(core.oi);
+        for (int i = part * each + threadIdx.x % width; i < (part + 1) * each; i += width) {
+            f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (int z = z0; z < z1; ++z)
+                v += in[(int64_t)z * n + i];
+            if (slices > 1) {  // then each thread has one element
+                joined[threadIdx.x] = v;
+                __syncthreads();
+                if (slice)
+                    break;
+                for (int q = 1; q < slices; ++q)
+                    v += joined[q * width + threadIdx.x];
+            }
+            // past the caches: another workgroup reads it
+            union {
+                f32x4 f;
+                unsigned long long u[2];
+            } w = {v};
+            for (int h = 0; h < 2; ++h)
+                __hip_atomic_store(sum + 2 * i + h, w.u[h], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        wait_vmem<0>();  // each wave's sums are out before the arrival is
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(a.arrived + m, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                   (unsigned)a.reducers - 1;
+        __syncthreads();
+        if (!last)
+            return;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j) {
+                union {
+                    unsigned long long u[2];
+                    f32x4 f;
+                } w;
+                for (int h = 0; h < 2; ++h)
+                    w.u[h] = __hip_atomic_load(sum + 2 * ((i * S::TN + j) * THREADS + threadIdx.x) + h, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+                acc[i][j] = w.f;
+            }
+    }
+    S::square(core, acc, a.kb, a.kc, r0, c0, fr, fh);
+    uint4 *dst = reinterpret_cast<uint4 *>(a.p + (int64_t)m * PARTS * IM * IM);
+#pragma unroll
+    for (int i = 0; i < PARTS * IM * IM / 8 / THREADS; ++i)
+        dst[i * THREADS + threadIdx.x] = reinterpret_cast<const uint4 *>(core.pi)[i * THREADS + threadIdx.x];
+    if (threadIdx.x < IM)
+        a.e[m * IM + threadIdx.x] = core.e[threadIdx.x];
+}
+
 // -------------------------------------------------------------------- plans
 // Tile classes, chosen by tile_time for the whole batch.  One 256×256 or
 // 192×192 workgroup per CU, two of the smaller ones.  192×192 is there for the
@@ -701,7 +987,9 @@ using T64 = Tile<half_t, 64, 64, 2, 2, 3, TA, TB>;
 
 struct Plan {
     int64_t s, l, ldx, lds;
-    bool tall, small;
+    bool tall, small, thin;
+    int image;        // rows of the short side's image (small, thin)
+    int strips, per, groups, reducers;  // thin
     Class gram, square, upd;
     int splits;       // of the gram product's contraction
     int64_t per_split;
@@ -719,6 +1007,29 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
     p.small = std::max(rows, cols) <= 128;
     p.s = std::min(rows, cols), p.l = std::max(rows, cols);
     p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
+    p.image = (p.small ? p.l : p.s) <= 64 ? 64 : 128;
+    // Up to 64 rows always take the strips: the operands in two parts are right
+    // where one is not, and nothing was slower (1x64x200 66 -> 53 us, 1x16x14336
+    // 133 -> 79, 1x64x131072 705 -> 160, 32x64x14336 500 -> 305, 300x64x300
+    // 166 -> 137).  Up to 128 rows a workgroup's Gram matrix is twice a strip's
+    // bytes, which pays for one matrix (1x100x200 76 -> 73, 1x128x14336
+    // 174 -> 133) and for long ones (8x128x4096 163 -> 145, 32x128x14336
+    // 1023 -> 732), and not for several short ones (16x128x1024 104 with the
+    // chain, 136 with strips; 32x100x1000 128 and 143).
+    p.thin = !p.small && (p.s <= 64 || (p.s <= 128 && (batch == 1 || p.l >= 2048)));
+    // Workgroups: with 512 and 256 in all, 32x64x14336 takes 305 and 520 us and
+    // 1x64x131072 160 and 185; for 128 rows 8x128x4096 157 and 145, 1x128x131072
+    // 281 and 261 (128x128x2048 378 and 384; 128 in all: 613).
+    p.strips = (int)cdiv(p.l, STRIP);
+    const int64_t most = std::max((int64_t)1, std::min((int64_t)p.strips, (p.image == 64 ? 512 : 256) / batch));
+    p.per = (int)cdiv(p.strips, most);
+    p.groups = (int)cdiv(p.strips, p.per);
+    // Workgroups that add up one matrix's parts: each costs a write past the
+    // caches and an arrival, so few where the matrices are many (8x64x4096 with
+    // 32 each 113 us, with 8 each 99; 1x64x131072 with 16 175, with 32 160).
+    p.reducers = 1;
+    while (p.groups > 4 && p.reducers < (p.groups <= 16 ? 8 : 32) && 2 * p.reducers * batch <= 64)
+        p.reducers *= 2;
     const auto best = [&](const TileClass *cls, auto count, int64_t k) {
         int c = 0;
         for (int i = 1; i < CLASSES; ++i)
@@ -752,8 +1063,9 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
 }
 struct Buffers {
     double *part;
-    float *x, *d, *e, *gram;
+    float *x, *d, *e, *gram, *sum;
     half_t *xh[2], *o, *p;
+    unsigned *arrived;
     int64_t used = 0;
 };
 Buffers lay_out(char *base, const Plan &p, int64_t batch, int64_t rows)
@@ -767,6 +1079,16 @@ Buffers lay_out(char *base, const Plan &p, int64_t batch, int64_t rows)
         b.used += round_up(n * (int64_t)sizeof(X), 256);
     };
     take(b.part, batch * p.norm_blocks);
+    if (p.thin) {
+        const int64_t im2 = (int64_t)p.image * p.image;
+        take(b.x, batch * p.s * p.strips * STRIP);
+        take(b.gram, batch * p.groups * im2);
+        take(b.sum, batch * im2);
+        take(b.p, batch * im2 * 2);
+        take(b.e, batch * p.image);
+        take(b.arrived, batch);
+        return b;
+    }
     take(b.x, batch * rows * p.ldx);
     take(b.xh[0], batch * rows * p.ldx);
     take(b.xh[1], batch * rows * p.ldx);
@@ -787,7 +1109,7 @@ int validate_sizes(int64_t batch, int64_t rows, int64_t cols)
     const int64_t lim = (int64_t)1 << 31;
     if (rows >= MAX_DMA_LD - BK || cols >= MAX_DMA_LD - BK || batch >= lim)
         return TG_ERR_TOO_LARGE;
-    if (batch * cdiv(rows, 64) >= lim || batch * cdiv(rows, 64) * cdiv(cols, 64) >= lim)
+    if (batch * cdiv(rows, 64) >= lim || batch * cdiv(rows, 64) * cdiv(cols, 64) >= MAX_GRID)
         return TG_ERR_TOO_LARGE;
     return TG_OK;
 }
@@ -842,6 +1164,23 @@ bool launch_sym_class(Class c, const SymArgs &a, int64_t batch, void *stream)
                        : launch_sym<T64, SQUARE, TRANS>(a, batch, stream);
 }
 
+template <typename G, int IM>
+bool thin_steps(const Plan &p, ThinArgs a, int64_t batch, int steps, const float *coefficients, void *stream)
+{
+    constexpr int THREADS = Small<IM>::WAVES * 64;
+    const int64_t grid = batch * p.groups;
+    if (steps == 0)
+        return launch(ns_strip_kernel<G, IM, true, true>, grid, THREADS, stream, a);
+    bool ok = launch(ns_strip_kernel<G, IM, true, false>, grid, THREADS, stream, a);
+    for (int t = 0; ok && t < steps; ++t) {
+        a.ka = coefficients[3 * t], a.kb = coefficients[3 * t + 1], a.kc = coefficients[3 * t + 2];
+        ok = launch(ns_core_kernel<IM>, batch * p.reducers, THREADS, stream, a) &&
+             (t == steps - 1 ? launch(ns_strip_kernel<G, IM, false, true>, grid, THREADS, stream, a)
+                             : launch(ns_strip_kernel<G, IM, false, false>, grid, THREADS, stream, a));
+    }
+    return ok;
+}
+
 template <typename G>
 int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t g_stride,
                   int64_t ldo, int64_t o_stride, int steps, const float *coefficients, float eps, void *ws,
@@ -864,24 +1203,37 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         return TG_ERR_DEVICE;
     const G *src = reinterpret_cast<const G *>(g);
     __bf16 *out = reinterpret_cast<__bf16 *>(o);
-    static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
+    float k[3 * TG_NS_MAX_STEPS] = {};
+    for (int i = 0; i < 3 * steps; ++i) {
+        static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
+        k[i] = coefficients ? coefficients[i] : standard[i % 3];
+    }
     if (p.small) {
         SmallArgs a = {g, ldg, g_stride, out, ldo, o_stride, (int)p.s, (int)p.l, p.tall, steps, eps, {}};
-        for (int i = 0; i < 3 * steps; ++i)
-            a.k[i] = coefficients ? coefficients[i] : standard[i % 3];
-        const bool ok = p.l <= 64 ? launch(ns_small_kernel<G, 64>, batch, Small<64>::WAVES * 64, stream, a)
+        memcpy(a.k, k, sizeof k);
+        const bool ok = p.image == 64 ? launch(ns_small_kernel<G, 64>, batch, Small<64>::WAVES * 64, stream, a)
                                   : launch(ns_small_kernel<G, 128>, batch, Small<128>::WAVES * 64, stream, a);
         return ok ? TG_OK : TG_ERR_LAUNCH;
     }
     bool ok = launch(ns_norm_kernel<G>, batch * p.norm_blocks, 256, stream, src, rows, cols, ldg, g_stride,
                      p.norm_blocks, b.part);
+    if (p.thin) {
+        ThinArgs a = {};
+        a.g = g, a.ld = ldg, a.g_stride = g_stride, a.out = out, a.ldo = ldo, a.o_stride = o_stride;
+        a.s = (int)p.s, a.l = (int)p.l, a.flip = p.tall;
+        a.part = b.part, a.norm_blocks = p.norm_blocks, a.eps = eps;
+        a.x = b.x, a.lp = (int64_t)p.strips * STRIP, a.strips = p.strips, a.per = p.per, a.groups = p.groups;
+        a.gram = b.gram, a.sum = b.sum, a.p = b.p, a.e = b.e, a.arrived = b.arrived, a.reducers = p.reducers;
+        ok = ok && (p.image == 64 ? thin_steps<G, 64>(p, a, batch, steps, k, stream)
+                                  : thin_steps<G, 128>(p, a, batch, steps, k, stream));
+        return ok ? TG_OK : TG_ERR_LAUNCH;
+    }
     const int64_t chunks = cdiv(rows * p.ldx / 4, 256);
     const int scale_blocks = (int)std::max((int64_t)1, std::min(chunks, std::max((int64_t)1, 8 * NUM_CU / batch)));
     ok = ok && launch(ns_scale_kernel<G>, batch * scale_blocks, 256, stream, src, rows, cols, ldg, g_stride,
                       p.norm_blocks, (const double *)b.part, eps, scale_blocks, b.x, b.xh[0], p.ldx,
                       steps == 0 ? out : nullptr, ldo, o_stride);
     for (int t = 0; ok && t < steps; ++t) {
-        const float *k = coefficients ? coefficients + 3 * t : standard;
         const half_t *xh = b.xh[t & 1];
         SymArgs a = {};
         a.x = {xh, p.ldx, (int)p.s};
@@ -901,7 +1253,7 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         q.x_stride = p.s * p.lds;
         q.K = (int)round_up(p.s, 8);
         q.s = (int)p.s, q.out = b.p, q.lds = p.lds, q.diag = b.e, q.o = b.o, q.d = b.d;
-        q.b = k[1], q.c = k[2];
+        q.b = k[3 * t + 1], q.c = k[3 * t + 2];
         ok = ok && launch_sym_class<true, false>(p.square, q, batch, stream);
         UpdateArgs u = {};
         const Operand x = {xh, p.ldx, (int)(p.tall ? rows : cols)}, pm = {b.p, p.lds, (int)p.s};
@@ -909,7 +1261,7 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
         u.l_stride = p.tall ? rows * p.ldx : p.s * p.lds, u.r_stride = p.tall ? p.s * p.lds : rows * p.ldx;
         u.K = (int)(p.tall ? round_up(p.s, 8) : p.s);
         u.rows = (int)rows, u.cols = (int)cols, u.x = b.x, u.xh = b.xh[(t + 1) & 1], u.ldx = p.ldx;
-        u.e = b.e, u.lds = p.lds, u.a = k[0];
+        u.e = b.e, u.lds = p.lds, u.a = k[3 * t];
         u.out = out, u.ldo = ldo, u.o_stride = o_stride;
         u.vec = ldo % 8 == 0 && o_stride % 8 == 0 && (uintptr_t)out % 16 == 0;
         const bool last = t == steps - 1;
@@ -966,7 +1318,9 @@ extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, 
         return st;
     const Plan p = make_plan(batch, rows, cols);
     if (name && name_len > 0 && p.small)
-        snprintf(name, (size_t)name_len, "small_%d", p.l <= 64 ? 64 : 128);
+        snprintf(name, (size_t)name_len, "small_%d", p.image);
+    else if (name && name_len > 0 && p.thin)
+        snprintf(name, (size_t)name_len, "thin_%d", p.image);
     else if (name && name_len > 0)
         snprintf(name, (size_t)name_len, "%s gram_%s%s square_%s update_%s", p.tall ? "tall" : "wide",
                  CLASS_NAME[p.gram], p.splits > 1 ? "_split" : "", CLASS_NAME[p.square], CLASS_NAME[p.upd]);

@@ -327,9 +327,9 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 }
 
 // Joins each row's pairs: 16 rows per workgroup, 64 threads to a row, which take
-// every 64th tile.  Reads 8·M bytes per column of tiles, 128 at a time.  For SUM and MEAN each workgroup
-// leaves its own sum, and the one that arrives last adds them all, in their
-// order: which one that is changes nothing in the result.
+// every 64th tile.  Reads 8·M bytes per column of tiles, 128 at a time.  For SUM
+// and MEAN each workgroup leaves its own sum, and the one that arrives last adds
+// them all, in their order: which one that is changes nothing in the result.
 constexpr int JOIN_ROWS = 16;
 struct JoinArgs {
     const float2 *part;
@@ -713,6 +713,7 @@ Class logits_class(int64_t M, int64_t V, int64_t K)
     return M <= 64 && tiles(C64X128, M, V) >= NUM_CU / 4 ? C64X128 : best_class(M, V, K);
 }
 constexpr int64_t G_BYTES = (int64_t)512 << 20;  // of G at a time
+constexpr int64_t G_COLS = 768 * 1365;           // and so many columns (a row is walked with 32-bit offsets)
 constexpr int64_t COMPACT_FLOP = (int64_t)1 << 38;
 
 struct Plan {
@@ -737,7 +738,7 @@ Plan make_plan(const void *H, const void *W, int64_t M, int64_t V, int64_t K, in
     p.compact = bwd || !rows_ok(H, ldh, K) || 2.0 * (double)M * (double)V * (double)K >= (double)COMPACT_FLOP;
     int64_t most = V;
     if (bwd)
-        most = std::min(V, std::max(G_BYTES / 2 / M, (int64_t)8192));
+        most = std::min(std::min(V, G_COLS), std::max(G_BYTES / 2 / M, (int64_t)8192));
     if (p.pack_w)
         most = std::min(most, std::max(G_BYTES / 2 / p.K8, (int64_t)1024));
     p.piece = most >= V ? V : round_up(most, 768);  // whole tiles of 256 and of 192
@@ -800,28 +801,32 @@ Buffers lay_out(Space &s, const Plan &p, int64_t M, int64_t V, bool bwd)
     return b;
 }
 
-int validate(const void *H, const void *W, int64_t M, int64_t V, int64_t K, int64_t ldh, int64_t ldw)
+// The kernels' own limits beside the interface's: a row of a packed or gathered
+// operand is K8 elements (a descriptor's offsets are 32-bit), and a launch holds
+// fewer than 2^32 threads.
+int validate(const void *H, const void *W, int64_t M, int64_t V, int64_t K, int64_t ldh, int64_t ldw, bool bwd)
 {
     if (M < 0 || V < 0 || K < 0 || ldh < K || ldw < K)
         return TG_ERR_INVALID_ARG;
     const int64_t lim = (int64_t)1 << 31;
-    if (M >= lim || V >= lim || K >= lim || ldh >= lim || ldw >= lim)
+    if (M >= lim / 32 || V >= lim / 2 || K > MAX_DMA_LD || ldh >= lim || ldw >= lim)
         return TG_ERR_TOO_LARGE;
     if (M == 0)
         return TG_OK;
     if (V == 0 || K == 0 || !H || !W)
         return TG_ERR_INVALID_ARG;
-    if (cdiv(M, 64) * cdiv(V, 64) >= lim || cdiv(M, 64) * cdiv(K, 64) * 64 >= lim ||
-        cdiv(V, 64) * cdiv(K, 64) >= lim || M > lim - 1024 || V > lim - 1024 || K > lim - 1024)
-        return TG_ERR_TOO_LARGE;
-    return TG_OK;
+    const Plan p = make_plan(H, W, M, V, K, ldh, ldw, bwd);
+    int64_t most = tiles(p.logits, M, p.piece);
+    if (bwd)
+        most = std::max(most, std::max(tiles(p.dh, M, K), tiles(p.dw, p.piece, K)));
+    return most >= MAX_GRID ? TG_ERR_TOO_LARGE : TG_OK;
 }
 bool reduction_ok(int r) { return r == TG_XENT_NONE || r == TG_XENT_SUM || r == TG_XENT_MEAN; }
 
 int64_t workspace_bytes(const void *H, const void *W, int64_t M, int64_t V, int64_t K, int64_t ldh, int64_t ldw,
                         bool bwd)
 {
-    if (validate(H, W, M, V, K, ldh, ldw) != TG_OK)
+    if (validate(H, W, M, V, K, ldh, ldw, bwd) != TG_OK)
         return -1;
     if (M == 0)
         return 0;
@@ -859,7 +864,7 @@ int forward(const void *H, const void *W, const int64_t *target, float *loss, fl
             int64_t K, int64_t ldh, int64_t ldw, int64_t ignore, int reduction, void *ws, int64_t ws_bytes,
             void *stream)
 {
-    int st = validate(H, W, M, V, K, ldh, ldw);
+    int st = validate(H, W, M, V, K, ldh, ldw, false);
     if (st != TG_OK)
         return st;
     if (!reduction_ok(reduction) || (M > 0 && !target) || (!loss && (M > 0 || reduction != TG_XENT_NONE)))
@@ -930,7 +935,7 @@ int backward(const void *H, const void *W, const int64_t *target, const float *l
              const float *dlse, void *dH, void *dW, int64_t M, int64_t V, int64_t K, int64_t ldh, int64_t ldw,
              int64_t lddh, int64_t lddw, int64_t ignore, int reduction, void *ws, int64_t ws_bytes, void *stream)
 {
-    int st = validate(H, W, M, V, K, ldh, ldw);
+    int st = validate(H, W, M, V, K, ldh, ldw, true);
     if (st != TG_OK)
         return st;
     if (!reduction_ok(reduction) || (dH && lddh < K) || (dW && lddw < K) ||
@@ -1068,7 +1073,7 @@ extern "C" int tg_xent_plan(const void *H, const void *W, int64_t M, int64_t V, 
         name[0] = 0;
     if (pieces)
         *pieces = 0;
-    const int st = validate(H, W, M, V, K, ldh, ldw);
+    const int st = validate(H, W, M, V, K, ldh, ldw, true);
     if (st != TG_OK || M == 0)
         return st;
     const Plan p = make_plan(H, W, M, V, K, ldh, ldw, backward_pass != 0);

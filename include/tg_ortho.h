@@ -19,9 +19,15 @@
  * bits at any magnitude met; the diagonals of A and B, which hold most of
  * their weight, stay in fp32 outside the products.  The result is bfloat16,
  * rounded once; its distance from the 64-bit result is that of the rounding to
- * within some 15%.  The scales bound the iterates: the singular values of X
- * have to stay below 4 and those of B below 16 (the default coefficients keep
- * them below 1.3 and 3); beyond, elements overflow to infinity.
+ * within some 15% where the small singular values are those of many
+ * directions.  A direction with less than some 1e-2 of the norm is amplified by
+ * up to 485, and with it the part of the operands' rounding that falls there;
+ * the fewer rows the shorter side has, the larger that part.  Up to 64 of them
+ * every operand is therefore the sum of two binary16 values (22 bits), and the
+ * result within 2^-8 of the 64-bit one at any spectrum.  The scales bound the
+ * iterates: the singular values of X have to stay below 4 and those of B below
+ * 16 (the default coefficients keep them below 1.3 and 3); beyond, elements
+ * overflow to infinity.
  */
 #ifndef TG_ORTHO_H
 #define TG_ORTHO_H
@@ -64,8 +70,8 @@ int64_t tg_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * TG_ERR_INVALID_ARG (negative sizes, a leading dimension below cols, batches
  * whose o_stride lets results overlap, steps or eps out of range, NULL pointers, a
  * workspace that is NULL, misaligned or too small), TG_ERR_TOO_LARGE (rows or
- * cols >= 2^21, batch >= 2^31, or more than 2^31 tiles), TG_ERR_DEVICE or
- * TG_ERR_LAUNCH.
+ * cols >= 2^21 - 64, or 2^23 or more 64×64 blocks in all matrices),
+ * TG_ERR_DEVICE or TG_ERR_LAUNCH.
  */
 int tg_newton_schulz_f32(const void *G, void *O, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
                          int64_t g_stride, int64_t ldo, int64_t o_stride, int steps, const float *coefficients,

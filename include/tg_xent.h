@@ -72,8 +72,9 @@ int64_t tg_xent_bwd_workspace_bytes(const void *H, const void *W, int64_t M, int
  * M == 0: loss (SUM, MEAN) is set to 0.  V and K must be at least 1 where M is
  * not 0.  Returns TG_OK, TG_ERR_INVALID_ARG (negative sizes, a leading
  * dimension below K, V or K 0, a NULL pointer, an unknown reduction, a
- * workspace that is NULL, misaligned or too small), TG_ERR_TOO_LARGE (M, V,
- * K, ldh or ldw >= 2^31, or more than 2^31 tiles), TG_ERR_DEVICE or
+ * workspace that is NULL, misaligned or too small), TG_ERR_TOO_LARGE
+ * (M >= 2^26, V >= 2^30, K > 2^21, ldh or ldw >= 2^31, or a product of
+ * 2^23 or more tiles, which are of 64×64 to 256×256), TG_ERR_DEVICE or
  * TG_ERR_LAUNCH.
  */
 int tg_xent_f16(const void *H, const void *W, const int64_t *target, float *loss, float *lse, int64_t M, int64_t V,

@@ -205,6 +205,80 @@ def test_captured_and_replayed(b, m, n):
         assert torch.equal(got, tg.newton_schulz(new))  # eager work between the replays
 
 
+# a short side of up to 128 and a long one: strips of 64 columns, one and several
+# to a workgroup, one and several workgroups to add a matrix's parts
+THIN = [(1, 1, 129), (1, 2, 4000), (1, 64, 65 * 64 - 3), (1, 5, 70000), (1, 70000, 5), (7, 63, 190), (70, 64, 257),
+        (5, 64, 1500), (2, 1500, 64), (600, 3, 130), (1, 65, 200), (1, 128, 2048), (1, 129, 100), (1, 127, 33000),
+        (3, 128, 2100), (9, 2051, 100), (33, 72, 2048)]
+
+
+@pytest.mark.parametrize("b,m,n", THIN)
+def test_short_sides(b, m, n):
+    for dt in (F32, BF16):
+        G = matrix(b, m, n, dt, seed=20)
+        say(b, m, n, dt, tg.tg_newton_schulz_plan(b, m, n))
+        O = tg.newton_schulz(G)
+        norm_check(O, G)
+        assert torch.equal(O, tg.newton_schulz(G))
+    if b > 1:  # a broadcast matrix
+        O = tg.newton_schulz(G[:1].expand(b, m, n))
+        assert all(torch.equal(O[0], x) for x in O)
+
+
+@pytest.mark.parametrize("m,n", [(2, 1000), (2, 40), (1000, 3), (16, 5000), (64, 700)])
+def test_few_rows_of_which_some_are_nearly_parallel(m, n):
+    """A direction with 1e-2 of the norm is amplified some hundred times more than
+    the first ones, and what an operand's rounding puts there with it: 2^-12 would
+    show as 2^-5, the two parts' 2^-23 as 2^-16."""
+    s = min(m, n)
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    U, _ = torch.linalg.qr(torch.randn(m, s, generator=gen, device="cuda", dtype=torch.float64))
+    V, _ = torch.linalg.qr(torch.randn(n, s, generator=gen, device="cuda", dtype=torch.float64))
+    sv = torch.full((s,), 1e-2, device="cuda", dtype=torch.float64)
+    sv[: (s + 1) // 2] = 1.0
+    G = ((U * sv) @ V.t().contiguous()).float()[None]
+    norm_check(tg.newton_schulz(G), G)
+
+
+@pytest.mark.parametrize("b,m,n", [(2, 40, 3001), (1, 3001, 100), (1, 60, 20000)])
+def test_short_sides_in_place_strided_captured_and_overlapping(b, m, n):
+    G = matrix(b, m, n, BF16, seed=21)
+    want = tg.newton_schulz(G)
+    big = torch.full((b, m + 1, n + 7), float("nan"), dtype=BF16, device="cuda")
+    view = big[:, 1:, 3:3 + n]
+    view.copy_(G)
+    out = torch.zeros(b, m + 2, n + 9, dtype=BF16, device="cuda")
+    tg.newton_schulz(view, out=out[:, 1:1 + m, 1:1 + n])
+    assert torch.equal(out[:, 1:1 + m, 1:1 + n], want)
+    out[:, 1:1 + m, 1:1 + n] = 0
+    assert not out.any()
+    same = G.clone()
+    tg.newton_schulz(same, out=same)
+    assert torch.equal(same, want)
+    bad = G.clone()
+    bad[b - 1, 0, n // 2] = float("inf")
+    O = tg.newton_schulz(bad)
+    assert torch.isnan(O[b - 1]).all() and torch.equal(O[: b - 1], want[: b - 1])
+    assert not tg.newton_schulz(torch.zeros_like(G)).any()
+    res = torch.zeros_like(G)
+    tg.newton_schulz(same, out=res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tg.newton_schulz(same, out=res)
+    side = torch.cuda.Stream()
+    for seed in (22, 23, 24):
+        new = matrix(b, m, n, BF16, seed=seed)
+        same.copy_(new)
+        res.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):  # an eager call beside the replay
+            other = tg.newton_schulz(new)
+        torch.cuda.synchronize()
+        assert torch.equal(res, other)
+
+
 def test_python_refusals():
     G = matrix(2, 20, 30, BF16)
     with pytest.raises(ValueError, match="contiguous"):

@@ -59,6 +59,32 @@ def test_too_large_refused(kw):
     assert bwd(lddh=LIM) == tg.TG_ERR_TOO_LARGE
 
 
+@pytest.mark.parametrize("kw", [
+    dict(M=1 << 26), dict(V=1 << 30), dict(K=(1 << 21) + 1, ldh=1 << 22, ldw=1 << 22),
+    dict(M=(1 << 26) - 1, V=1 << 29),  # launches of 2^32 threads and more
+])
+def test_sizes_beyond_the_kernels_offsets_are_refused(kw):
+    assert fwd(**kw) == tg.TG_ERR_TOO_LARGE
+    sizes = {**dict(M=5, V=100, K=16, ldh=4096, ldw=4096), **kw}
+    args = (A, A, sizes["M"], sizes["V"], sizes["K"], sizes["ldh"], sizes["ldw"])
+    assert tg.tg_xent_workspace_bytes(*args) == -1
+    if kw.get("M") != (1 << 26) - 1:  # the backward pass takes the vocabulary in pieces
+        assert bwd(**kw) == tg.TG_ERR_TOO_LARGE and tg.tg_xent_bwd_workspace_bytes(*args) == -1
+
+
+def test_largest_sizes_are_planned():
+    for args in ((A, A, 1, (1 << 30) - 128, 64, 64, 64), (A, A, 4, 1000, 1 << 21, 1 << 21, 1 << 21),
+                 (A + 2, A + 2, 1 << 20, 131072, 4096, 4097, 4097)):
+        for fn in (tg.tg_xent_workspace_bytes, tg.tg_xent_bwd_workspace_bytes):
+            assert fn(*args) > 0
+    # a piece's columns stay few enough for 32-bit offsets inside a tile, however few the tokens
+    status, name, pieces = tg.tg_xent_plan(A, A, 1, (1 << 30) - 128, 64, 64, 64, 1)
+    assert status == tg.TG_OK and pieces >= ((1 << 30) - 128) / 2 ** 20
+    assert tg.tg_newton_schulz_workspace_bytes(1, 64, (1 << 21) - 65) > 0
+    assert tg.tg_newton_schulz_workspace_bytes((1 << 23) - 1, 8, 8) == 0  # one workgroup each
+    assert tg.tg_newton_schulz_workspace_bytes(1 << 23, 8, 8) == -1
+
+
 def test_workspace_one_byte_short_is_refused():
     n = tg.tg_xent_workspace_bytes(A, A, 100, 1000, 64, 64, 64)
     b = tg.tg_xent_bwd_workspace_bytes(A, A, 100, 1000, 64, 64, 64)
@@ -118,7 +144,7 @@ def test_every_tile_class_is_reached():
         for c in classes:
             assert f"{what}_{c}" in seen, (what, c)
     seen = set()
-    for b, m, n in itertools.product((1, 2, 8, 64), (64, 129, 700, 1000, 2048, 4096, 9000), (64, 200, 1000, 4096, 9000)):
+    for b, m, n in itertools.product((1, 2, 8, 64), (64, 128, 129, 700, 1000, 2048, 4096, 9000), (64, 200, 1000, 4096, 9000)):
         st, name = tg.tg_newton_schulz_plan(b, m, n)
         assert st == tg.TG_OK
         seen.update(name.split())
@@ -127,6 +153,7 @@ def test_every_tile_class_is_reached():
             assert f"{what}_{c}" in seen, (what, c)
     assert {"gram_64x64_split", "gram_128x128_split"} <= seen
     assert {"small_64", "tall", "wide"} <= seen and tg.tg_newton_schulz_plan(1, 65, 3)[1] == "small_128"
+    assert {"thin_64", "thin_128"} <= seen
 
 
 @pytest.mark.parametrize("kw", [
