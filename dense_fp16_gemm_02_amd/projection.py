@@ -282,8 +282,11 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
     For a penalty on the normaliser add e.g. ``1e-4 * (lse * lse).sum()``.
 
     Runs on torch's current stream and takes its workspace from torch's
-    allocator.  Raises TypeError / ValueError on tensors it cannot take and
-    TgError on a non-zero status.
+    allocator; it may be captured into a graph, its backward pass with
+    torch.autograd.grad, or with .backward() where no eager graph of the same
+    leaves is alive (autograd would accumulate on that graph's stream, which
+    ends the capture).  Raises TypeError / ValueError on tensors it cannot take
+    and TgError on a non-zero status.
     """
     import torch
 
@@ -309,6 +312,13 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
     return (loss, lse) if return_lse else loss
 
 
+def _meet(a, b):
+    """Whether the memory from first to last element of two tensors overlaps."""
+    (a0, a1), (b0, b1) = ((t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum(
+        (n - 1) * s for n, s in zip(t.shape, t.stride())))) for t in (a, b))
+    return a0 < b1 and b0 < a1
+
+
 @functools.lru_cache(maxsize=1024)
 def _ns_size(batch, rows, cols):
     return _lib().tg_newton_schulz_workspace_bytes(batch, rows, cols)
@@ -331,7 +341,9 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     shape (see include/tg_ortho.h for the precision held inside).
     ``coefficients`` is one triple (a, b, c) for all steps, or one per step;
     the default is (3.4445, -4.7750, 2.0315).  ``out``, where given, is a bf16
-    tensor of G's shape with non-overlapping rows and matrices.
+    tensor of G's shape whose rows and matrices follow each other without
+    overlapping; it may be G itself where that is fp16 or bf16, and share no
+    memory with G otherwise.
 
     Runs on torch's current stream and takes its workspace from torch's
     allocator; not differentiable.  Raises TypeError / ValueError on tensors it
@@ -351,7 +363,8 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     if coefficients is not None:
         per_step = steps > 0 and hasattr(coefficients[0], "__len__")
         c = _coefficients(tuple(map(tuple, coefficients)) if per_step else (tuple(coefficients),) * steps, steps)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
     elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
         raise ValueError("out must be a bfloat16 tensor of G's shape on G's device")
@@ -361,7 +374,9 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
         return out
     ldg, ldo = _row_stride(g[0], "G", cols), _row_stride(o[0], "out", cols)
     if batch > 1 and o.stride(0) < (rows - 1) * ldo + cols:
-        raise ValueError("out has overlapping matrices")
+        raise ValueError("out has overlapping or interleaved matrices")
+    if given and out is not G and _meet(g, o) and (g.data_ptr(), g.stride(), g.element_size()) != (o.data_ptr(), o.stride(), 2):
+        raise ValueError("out overlaps G")
     lib = _lib()
     size = _ns_size(batch, rows, cols)
     ws = torch.empty(size, dtype=torch.uint8, device=G.device) if size > 0 else None

@@ -289,5 +289,14 @@ def test_python_refusals():
         tg.newton_schulz(G, out=torch.empty_like(G, dtype=F32))
     with pytest.raises(ValueError, match="overlapping"):
         tg.newton_schulz(G, out=G[:1].expand(2, 20, 30))
+    room = torch.zeros(2, 60, 30, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="overlaps G"):
+        tg.newton_schulz(room[:, :20], out=room[:, 10:30])
+    with pytest.raises(ValueError, match="interleaved"):
+        tg.newton_schulz(G, out=room.view(60, 2, 30)[:20].transpose(0, 1))
+    tg.newton_schulz(room[:, :20], out=room[:, :20])
+    F = torch.ones(20, 30, device="cuda")
+    with pytest.raises(ValueError, match="overlaps G"):
+        tg.newton_schulz(F, out=F.view(BF16)[:, :30])
     assert tg.newton_schulz(G[:0]).shape == (0, 20, 30)
     assert tg.newton_schulz(G[:, :0]).shape == (2, 0, 30)

@@ -40,3 +40,41 @@ def test_a_training_step_and_its_scores():
         # the GEMM's logits are rounded to bfloat16: half a step of the largest, twice
         assert float((per - direct)[live].abs().max()) <= 2 * 2.0 ** -8 * float(z.abs().max()) + 1e-4
         assert abs(float(per.sum() / live.sum()) - float(loss)) <= 1e-5 * abs(float(loss))
+
+
+def test_a_training_step_captured_and_replayed():
+    """Loss, gradients through autograd and the update in one graph, with eager work
+    on other tensors and an eager graph of the same ones between the replays."""
+    M, V, K = 300, 700, 136
+    gen = torch.Generator(device="cuda").manual_seed(4)
+
+    def draw():
+        H = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+        W = (torch.randn(V, K, generator=gen, device="cuda") / K ** 0.5).bfloat16()
+        t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+        t[::7] = -100
+        return H, W, t
+
+    def step(H, W, t):
+        loss, lse = tg.linear_cross_entropy(H, W, t, return_lse=True)
+        dH, dW = torch.autograd.grad(loss + 1e-4 * lse.square().sum() / M, (H, W))
+        return loss.detach(), dH, dW, tg.newton_schulz(dW)
+
+    H, W, t = draw()
+    H.requires_grad_(), W.requires_grad_()
+    step(H, W, t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(H, W, t)
+    for _ in range(3):
+        H2, W2, t2 = draw()
+        with torch.no_grad():
+            H.copy_(H2), W.copy_(W2), t.copy_(t2)
+        for x in held:
+            x.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in held]
+        want = step(H2.requires_grad_(), W2.requires_grad_(), t2)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
