@@ -225,6 +225,26 @@ def test_short_sides(b, m, n):
         assert all(torch.equal(O[0], x) for x in O)
 
 
+@pytest.mark.parametrize("b,m,n", [(1, 40, 3000), (3, 500, 17), (1, 100, 2500)])
+def test_short_sides_by_steps_and_coefficients(b, m, n):
+    co = [(3.4445, -4.7750, 2.0315), (3.0, -3.0, 1.0), (1.875, -1.25, 0.375)]
+    G = matrix(b, m, n, F16, seed=30)
+    X0 = po.newton_schulz(G, steps=0)
+    O = tg.newton_schulz(G, steps=0)
+    assert bool(((O.double() - X0).abs() <= (2.0 ** -8 + 2.0 ** -20) * X0.abs()).all())
+    same = G.clone()
+    tg.newton_schulz(same, steps=0, out=same.view(BF16))  # in place, under its own type's width
+    assert torch.equal(same.view(BF16), O)
+    for g in (G, matrix(b, m, n, BF16, seed=31, kind="spikes")):
+        O = tg.newton_schulz(g, steps=1)
+        want, tol = po.newton_schulz_one_step_bound(g)
+        assert bool(((O.double() - want).abs() <= tol).all())
+    norm_check(tg.newton_schulz(G, steps=3, coefficients=co, eps=0.25), G, steps=3, coefficients=co, eps=0.25)
+    F = matrix(b, m, n, F32, seed=32, scale=1e25)  # beyond fp32's squares
+    norm_check(tg.newton_schulz(F, eps=0.0), F, eps=0.0)
+    assert not tg.newton_schulz(torch.zeros_like(G), eps=0.0).any()
+
+
 @pytest.mark.parametrize("m,n", [(2, 1000), (2, 40), (1000, 3), (16, 5000), (64, 700)])
 def test_few_rows_of_which_some_are_nearly_parallel(m, n):
     """A direction with 1e-2 of the norm is amplified some hundred times more than
