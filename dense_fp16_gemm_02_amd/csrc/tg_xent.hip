@@ -52,9 +52,10 @@ __device__ inline float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * LO
 // ------------------------------------------------------------------ gather
 // Numbers the live tokens and copies their rows of H to consecutive rows, K
 // columns padded with zeros to K8; for the backward pass also each live token's
-// coefficients, and zeros for the ignored tokens' rows of dH.  A workgroup has
-// PREP_ROWS tokens at most and counts the live ones before them itself (8·M
-// bytes from the caches): one launch, no pass over the targets in between.
+// coefficients, and zeros for the ignored tokens' rows of dH.  A workgroup counts
+// the live tokens before its own itself (8·M bytes from the caches): one launch,
+// no pass over the targets in between.  So there are at most two workgroups to a
+// compute unit, which take their tokens PREP_ROWS at a time.
 constexpr int PREP_THREADS = 256, PREP_ROWS = 256;
 struct PrepArgs {
     const int64_t *target;
@@ -127,15 +128,16 @@ __global__ __launch_bounds__(PREP_THREADS) void xent_prep_kernel(PrepArgs a)
     if constexpr (BWD) {
         if (a.reduction == TG_XENT_MEAN)
             scale = 1.0f / (float)imax(all, 1);
-        // the largest coefficient (a NaN among them reaches its own row through
-        // its coefficient, not through the maximum)
+        // the largest coefficient (a NaN or an infinity among them reaches its own
+        // row through its coefficient, not the others through the maximum)
+        const auto size = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.0f; };
         if (a.reduction != TG_XENT_NONE && !a.dlse) {
-            top = fabsf(a.dloss[0] * scale);
+            top = size(a.dloss[0] * scale);
         } else {
             for (int64_t i = tid; i < a.M; i += PREP_THREADS)
                 if (a.target[i] != a.ignore) {
                     const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
-                    top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[i]) : 0.0f));
+                    top = fmaxf(top, fmaxf(size(g), a.dlse ? size(g + a.dlse[i]) : 0.0f));
                 }
             for (int o = 32; o; o >>= 1)
                 top = fmaxf(top, __shfl_xor(top, o));
@@ -152,50 +154,54 @@ __global__ __launch_bounds__(PREP_THREADS) void xent_prep_kernel(PrepArgs a)
         a.head->live = all;
         a.head->alpha = top;
     }
-    // this workgroup's tokens, 64 at a time by the first wave
-    if (wave == 0)
-        for (int c = 0; c < rows; c += 64) {
-            const int64_t i = r0 + c + lane;
-            const int64_t t = c + lane < rows ? a.target[i] : a.ignore;
-            const bool live = c + lane < rows && t != a.ignore;
-            const unsigned long long votes = __ballot(live);
-            const int at = before + __popcll(votes & ((1ull << lane) - 1));
-            before += __popcll(votes);
-            if (c + lane >= rows)
-                continue;
-            place[c + lane] = live ? at : -1;
-            if (live) {
-                const bool in = t >= 0 && t < a.V;
-                a.map[at] = (int)i;
-                a.col[at] = in ? (int)t : -1;
-                if constexpr (BWD) {
-                    const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
-                    a.lse_c[at] = a.lse[i];
-                    a.cp[at] = in ? (g + (a.dlse ? a.dlse[i] : 0.0f)) / top : NAN;
-                    a.ct[at] = g / top;
+    const int per = (int)(a.K8 / 8);
+    for (int64_t first = r0; first < r0 + rows; first += PREP_ROWS) {
+        const int n = (int)(r0 + rows - first < PREP_ROWS ? r0 + rows - first : PREP_ROWS);
+        // numbered 64 at a time by the first wave
+        if (wave == 0)
+            for (int c = 0; c < n; c += 64) {
+                const int64_t i = first + c + lane;
+                const int64_t t = c + lane < n ? a.target[i] : a.ignore;
+                const bool live = c + lane < n && t != a.ignore;
+                const unsigned long long votes = __ballot(live);
+                const int at = before + __popcll(votes & ((1ull << lane) - 1));
+                before += __popcll(votes);
+                if (c + lane >= n)
+                    continue;
+                place[c + lane] = live ? at : -1;
+                if (live) {
+                    const bool in = t >= 0 && t < a.V;
+                    a.map[at] = (int)i;
+                    a.col[at] = in ? (int)t : -1;
+                    if constexpr (BWD) {
+                        const float g = (a.reduction == TG_XENT_NONE ? a.dloss[i] : a.dloss[0]) * scale;
+                        a.lse_c[at] = a.lse[i];
+                        a.cp[at] = in ? (g + (a.dlse ? a.dlse[i] : 0.0f)) / top : NAN;
+                        a.ct[at] = g / top;
+                    }
+                } else if constexpr (!BWD) {
+                    if (a.loss)
+                        a.loss[i] = 0.0f;
+                    if (a.lse_out)
+                        a.lse_out[i] = 0.0f;
                 }
-            } else if constexpr (!BWD) {
-                if (a.loss)
-                    a.loss[i] = 0.0f;
-                if (a.lse_out)
-                    a.lse_out[i] = 0.0f;
+            }
+        __syncthreads();
+        for (int r = wave; r < n; r += WAVES) {
+            const int at = place[r];
+            if (at >= 0) {
+                const uint16_t *src = a.H + (first + r) * a.ldh;
+                uint4 *dst = reinterpret_cast<uint4 *>(a.hc + at * a.K8);
+#pragma unroll 4
+                for (int c = lane; c < per; c += 64)
+                    dst[c] = load8(src, 8 * (int64_t)c, a.K, a.vec);
+            } else if (BWD && a.dH) {
+                uint16_t *dst = a.dH + (first + r) * a.lddh;
+                for (int64_t c = lane; c < a.K; c += 64)
+                    dst[c] = 0;
             }
         }
-    __syncthreads();
-    const int per = (int)(a.K8 / 8);
-    for (int r = wave; r < rows; r += WAVES) {
-        const int at = place[r];
-        if (at >= 0) {
-            const uint16_t *src = a.H + (r0 + r) * a.ldh;
-            uint4 *dst = reinterpret_cast<uint4 *>(a.hc + at * a.K8);
-#pragma unroll 4
-            for (int c = lane; c < per; c += 64)
-                dst[c] = load8(src, 8 * (int64_t)c, a.K, a.vec);
-        } else if (BWD && a.dH) {
-            uint16_t *dst = a.dH + (r0 + r) * a.lddh;
-            for (int64_t c = lane; c < a.K; c += 64)
-                dst[c] = 0;
-        }
+        __syncthreads();  // every wave has read `place`
     }
 }
 
@@ -809,7 +815,7 @@ int validate(const void *H, const void *W, int64_t M, int64_t V, int64_t K, int6
     if (M < 0 || V < 0 || K < 0 || ldh < K || ldw < K)
         return TG_ERR_INVALID_ARG;
     const int64_t lim = (int64_t)1 << 31;
-    if (M >= lim / 32 || V >= lim / 2 || K > MAX_DMA_LD || ldh >= lim || ldw >= lim)
+    if (M >= lim / 64 || V >= lim / 2 || K > MAX_DMA_LD || ldh >= lim || ldw >= lim)
         return TG_ERR_TOO_LARGE;
     if (M == 0)
         return TG_OK;
@@ -852,10 +858,10 @@ bool w_piece(const Plan &p, const Buffers &b, const void *W, int64_t ldw, int64_
     w = {b.wp, p.K8, (int)n};
     return launch(xent_pack_kernel, copy_grid(n * p.K8 / 8), 256, stream, src, ldw, (uint16_t *)b.wp, n, K, p.K8);
 }
-// the workgroups' share of the tokens: all CUs busy, PREP_ROWS at most
+// the workgroups' share of the tokens
 void split_rows(PrepArgs &a, int64_t &grid)
 {
-    a.rows = (int)std::min((int64_t)PREP_ROWS, std::max((int64_t)4, cdiv(a.M, 2 * NUM_CU)));
+    a.rows = (int)std::max((int64_t)4, cdiv(a.M, 2 * NUM_CU));
     grid = cdiv(a.M, a.rows);
 }
 

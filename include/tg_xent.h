@@ -73,7 +73,7 @@ int64_t tg_xent_bwd_workspace_bytes(const void *H, const void *W, int64_t M, int
  * not 0.  Returns TG_OK, TG_ERR_INVALID_ARG (negative sizes, a leading
  * dimension below K, V or K 0, a NULL pointer, an unknown reduction, a
  * workspace that is NULL, misaligned or too small), TG_ERR_TOO_LARGE
- * (M >= 2^26, V >= 2^30, K > 2^21, ldh or ldw >= 2^31, or a product of
+ * (M >= 2^25, V >= 2^30, K > 2^21, ldh or ldw >= 2^31, or a product of
  * 2^23 or more tiles, which are of 64×64 to 256×256), TG_ERR_DEVICE or
  * TG_ERR_LAUNCH.
  */

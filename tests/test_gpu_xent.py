@@ -106,6 +106,28 @@ def check_raw(H, W, t, reduction="mean", dloss=None):
     return (loss.detach(), lse.detach()) + torch.autograd.grad(loss, (h, w), up)
 
 
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("value", ["inf", "-inf", "nan"])
+def test_one_tokens_infinite_upstream_leaves_the_others_gradients(value, dt):
+    M, V, K = 150, 400, 72
+    H, W, t = inputs(M, V, K, dt, seed=30, ignored=0.2)
+    t[7], t[9] = 3, IGNORE
+    dloss = torch.randn(M, device="cuda")
+    dloss[7] = 0.0
+    clean = check_raw(H, W, t, "none", dloss)[2]
+    dloss[7] = dloss[9] = float(value)  # the second one's token is ignored
+    dH, dW = check_raw(H, W, t, "none", dloss)[2:]
+    rest = torch.arange(M, device="cuda") != 7
+    assert torch.equal(dH[rest], clean[rest])
+    assert not torch.isfinite(dH[7]).all() and not torch.isfinite(dW).all()
+
+
+@pytest.mark.parametrize("M", [131072, 131073, 140000, 300001])
+def test_more_tokens_than_the_gather_takes_at_once(M):
+    H, W, t = inputs(M, 50, 16, BF16, seed=31, ignored=0.3)
+    check(H, W, t, "none", torch.randn(M, device="cuda"))
+
+
 def test_in_range_ignore_index():
     H, W, t = inputs(100, 50, 64, F16, seed=3)
     t[::3] = 7

@@ -60,15 +60,15 @@ def test_too_large_refused(kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(M=1 << 26), dict(V=1 << 30), dict(K=(1 << 21) + 1, ldh=1 << 22, ldw=1 << 22),
-    dict(M=(1 << 26) - 1, V=1 << 29),  # launches of 2^32 threads and more
+    dict(M=1 << 25), dict(V=1 << 30), dict(K=(1 << 21) + 1, ldh=1 << 22, ldw=1 << 22),
+    dict(M=(1 << 25) - 1, V=1 << 29),  # launches of 2^32 threads and more
 ])
 def test_sizes_beyond_the_kernels_offsets_are_refused(kw):
     assert fwd(**kw) == tg.TG_ERR_TOO_LARGE
     sizes = {**dict(M=5, V=100, K=16, ldh=4096, ldw=4096), **kw}
     args = (A, A, sizes["M"], sizes["V"], sizes["K"], sizes["ldh"], sizes["ldw"])
     assert tg.tg_xent_workspace_bytes(*args) == -1
-    if kw.get("M") != (1 << 26) - 1:  # the backward pass takes the vocabulary in pieces
+    if kw.get("M") != (1 << 25) - 1:  # the backward pass takes the vocabulary in pieces
         assert bwd(**kw) == tg.TG_ERR_TOO_LARGE and tg.tg_xent_bwd_workspace_bytes(*args) == -1
 
 
