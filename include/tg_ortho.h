@@ -24,7 +24,10 @@
  * up to 485, and with it the part of the operands' rounding that falls there;
  * the fewer rows the shorter side has, the larger that part.  Up to 64 of them
  * every operand is therefore the sum of two binary16 values (22 bits), and the
- * result within 2^-8 of the 64-bit one at any spectrum.  The scales bound the
+ * result within 2^-8 of the 64-bit one at any spectrum.  Above 64 one value is
+ * held: where all of a matrix is in a few of its rows and these are nearly
+ * parallel, the result was measured up to 1.7e-2 off (two rows), 1.0e-2 (four),
+ * 4e-3 (64); for a single row, or equal rows, up to 7.4e-3.  The scales bound the
  * iterates: the singular values of X have to stay below 4 and those of B below
  * 16 (the default coefficients keep them below 1.3 and 3); beyond, elements
  * overflow to infinity.
