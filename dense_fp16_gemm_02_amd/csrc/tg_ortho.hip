@@ -52,7 +52,7 @@ constexpr float X_SCALE = 16384.0f, S_SCALE = 4096.0f;  // of X, and of O and P
 constexpr int NORM_BLOCKS = 1024;  // most partial sums per matrix
 // Sums of squares in 64 bits: fp32 squares would overflow or vanish for
 // elements beyond 1e19 or below 1e-23.  Reads G once, 16 bytes per lane where
-// rows follow each other without gaps and are aligned.
+// rows follow each other without gaps.
 template <typename G>
 __global__ __launch_bounds__(256) void ns_norm_kernel(const G *g, int64_t rows, int64_t cols, int64_t ld,
                                                       int64_t stride, int blocks, double *part)
@@ -69,10 +69,11 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const G *g, int64_t rows, 
     if (ld == cols) {
         constexpr int N = 16 / sizeof(G);
         typedef G vec __attribute__((ext_vector_type(N)));
-        const int64_t chunks = (uintptr_t)p % 16 == 0 ? total / N : 0;
+        const int64_t chunks = total / N;
 #pragma unroll 4
         for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < chunks; i += (int64_t)blocks * 256) {
-            const vec v = *reinterpret_cast<const vec *>(p + i * N);
+            vec v;
+            __builtin_memcpy(&v, p + i * N, 16);  // at an element's alignment
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 add(v[e]);
@@ -114,11 +115,12 @@ __global__ __launch_bounds__(256) void ns_scale_kernel(const G *g, int64_t rows,
     const G *p = g + (int64_t)m * stride;
     const int64_t per = ldx / 4, total = rows * per, step = (int64_t)blocks * 256;
     typedef G four __attribute__((ext_vector_type(4)));
-    const bool vec = ld % 4 == 0 && (uintptr_t)p % sizeof(four) == 0;
     const auto load = [&](int64_t r, int64_t c) {
         four v = {(G)0.0f, (G)0.0f, (G)0.0f, (G)0.0f};
-        if (vec && c + 4 <= cols)
-            return *reinterpret_cast<const four *>(p + r * ld + c);
+        if (c + 4 <= cols) {
+            __builtin_memcpy(&v, p + r * ld + c, sizeof v);  // at an element's alignment
+            return v;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (c + e < cols)
@@ -801,7 +803,6 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_strip_kernel(ThinArg
     float *xm = a.x + (int64_t)m * a.s * a.lp;
     __bf16 *out = a.out + (int64_t)m * a.o_stride;
     typedef G four __attribute__((ext_vector_type(4)));
-    const bool g4 = !a.flip && a.ld % 4 == 0 && (uintptr_t)g % sizeof(four) == 0;
     const bool out4 = !a.flip && a.ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
     f32x4 gram[S::TM][S::TN];
     zero_blocks(gram);
@@ -819,8 +820,9 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_strip_kernel(ThinArg
                     continue;
                 if constexpr (!FIRST) {
                     x[i][j] = *reinterpret_cast<const f32x4 *>(xm + r * a.lp + c);
-                } else if (g4 && c + 4 <= a.l) {
-                    const four v = *reinterpret_cast<const four *>(g + r * a.ld + c);
+                } else if (!a.flip && c + 4 <= a.l) {
+                    four v;
+                    __builtin_memcpy(&v, g + r * a.ld + c, sizeof v);  // at an element's alignment
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         x[i][j][k] = (float)((double)(float)v[k] * inv);
