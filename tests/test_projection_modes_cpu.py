@@ -1,0 +1,90 @@
+"""Modes of autograd and tracing that the projection operators do not follow: each
+is refused, or raises where it would be used, instead of giving a number without its
+derivative.  On the CPU: the wrappers run as they are, with the library's two passes
+replaced by the same formulas in torch and tensors that say they are on a GPU."""
+import pytest
+
+torch = pytest.importorskip("torch")
+tg = pytest.importorskip("dense_fp16_gemm_02_amd")
+
+import torch.autograd.forward_ad as fwad  # noqa: E402
+
+from dense_fp16_gemm_02_amd import projection as pr  # noqa: E402
+
+
+class OnCard(torch.Tensor):
+    is_cuda = True
+
+
+def forward(H, W, target, ignore_index, reduction, want_lse):
+    with torch.no_grad():
+        z = H.float() @ W.float().t()
+        lse = torch.logsumexp(z, 1)
+        loss = (lse - z.gather(1, target[:, None])[:, 0]).mean()
+    return loss, lse if want_lse else None
+
+
+def backward(H, W, target, lse, dloss, dlse, need_h, need_w, ignore_index, reduction):
+    with torch.no_grad():
+        G = torch.exp(H.float() @ W.float().t() - lse[:, None])
+        G = (G - torch.nn.functional.one_hot(target, W.shape[0])) * dloss / H.shape[0]
+        if dlse is not None:
+            G = G + dlse[:, None] * torch.exp(H.float() @ W.float().t() - lse[:, None])
+        return (G @ W.float()).to(H.dtype) if need_h else None, (G.t() @ H.float()).to(W.dtype) if need_w else None
+
+
+@pytest.fixture
+def card(monkeypatch):
+    monkeypatch.setattr(pr, "_forward", forward)
+    monkeypatch.setattr(pr, "_backward", backward)
+    gen = torch.Generator().manual_seed(0)
+    H = torch.randn(6, 16, generator=gen).half().as_subclass(OnCard)
+    W = torch.randn(9, 16, generator=gen).half().as_subclass(OnCard)
+    return H, W, torch.arange(6).as_subclass(OnCard)
+
+
+def test_the_stubs_stand_for_the_library(card):
+    """Otherwise the other tests would say nothing."""
+    H, W, t = card
+    h, w = H.clone().requires_grad_(), W.clone().requires_grad_()
+    loss = tg.linear_cross_entropy(h, w, t)
+    dH, dW = torch.autograd.grad(loss, (h, w))
+    h32, w32 = H.detach().float().requires_grad_(), W.detach().float().requires_grad_()
+    want = torch.nn.functional.cross_entropy(h32 @ w32.t(), t)
+    eH, eW = torch.autograd.grad(want, (h32, w32))
+    assert torch.allclose(loss, want, rtol=1e-6)
+    assert torch.allclose(dH.float(), eH, rtol=2e-3, atol=1e-6) and torch.allclose(dW.float(), eW, rtol=2e-3, atol=1e-6)
+
+
+@pytest.mark.parametrize("which", ["H", "W"])
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_forward_mode_is_refused(card, which, requires_grad):
+    H, W, t = card
+    with fwad.dual_level():
+        h = fwad.make_dual(H, torch.ones_like(H)) if which == "H" else H
+        w = fwad.make_dual(W, torch.ones_like(W)) if which == "W" else W
+        if requires_grad:
+            h = h.requires_grad_() if which == "W" else h
+            w = w.requires_grad_() if which == "H" else w
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            tg.linear_cross_entropy(h, w, t)
+        tg.linear_cross_entropy(H, W, t)  # a dual level without dual tensors is nothing to object to
+
+
+def test_forward_mode_through_the_upstream_gradient_is_refused(card):
+    H, W, t = card
+    h = H.clone().requires_grad_()
+    loss = tg.linear_cross_entropy(h, W, t)
+    with fwad.dual_level():
+        up = fwad.make_dual(torch.ones(()), torch.ones(()))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            torch.autograd.grad(loss, h, up)
+
+
+def test_forward_mode_of_the_update_is_refused():
+    G = torch.ones(3, 4).as_subclass(OnCard)
+    with fwad.dual_level():
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            tg.newton_schulz(fwad.make_dual(G, G))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            tg.newton_schulz(G, out=fwad.make_dual(G.bfloat16(), G.bfloat16()))
