@@ -247,7 +247,18 @@ def _backward(H, W, target, lse, dloss, dlse, need_h, need_w, ignore_index, redu
 @functools.lru_cache(maxsize=None)
 def _xent_function():
     import torch
-    from torch.autograd.function import once_differentiable
+
+    class Gradients(torch.autograd.Function):
+        """dH and dW as values with a graph, for create_graph: what depends on them
+        would need second derivatives, which there are none of, and raises."""
+
+        @staticmethod
+        def forward(ctx, H, W, target, lse, dloss, dlse, *how):
+            return _backward(H, W, target, lse, dloss, dlse, *how)
+
+        @staticmethod
+        def backward(ctx, *_):
+            raise RuntimeError("linear_cross_entropy can be differentiated once")
 
     class LinearCrossEntropy(torch.autograd.Function):
         @staticmethod
@@ -259,7 +270,6 @@ def _xent_function():
             return loss, lse
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, dloss, dlse):
             H, W, target, lse = ctx.saved_tensors
             if dloss is None and dlse is None:
@@ -269,7 +279,8 @@ def _xent_function():
                 dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, device=H.device)
             dloss = dloss.contiguous()
             dlse = None if dlse is None else dlse.contiguous()
-            dH, dW = _backward(H, W, target, lse, dloss, dlse, ctx.needs_input_grad[0], ctx.needs_input_grad[1],
+            gradients = Gradients.apply if torch.is_grad_enabled() else _backward
+            dH, dW = gradients(H, W, target, lse, dloss, dlse, ctx.needs_input_grad[0], ctx.needs_input_grad[1],
                                ctx.ignore_index, ctx.reduction)
             return dH, dW, None, None, None
 
@@ -288,7 +299,8 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
     ``reduction`` is "mean" (over the tokens that count; 0 if there are none),
     "sum" or "none" (one loss per token).  Returns the fp32 loss, or (loss, lse)
     with ``return_lse``, lse the log of each token's sum of exponentials (0 for
-    ignored tokens); both can be differentiated with respect to H and W, once.
+    ignored tokens); both can be differentiated with respect to H and W, once
+    (under create_graph, what depends on the gradients raises RuntimeError).
     For a penalty on the normaliser add e.g. ``1e-4 * (lse * lse).sum()``.
 
     Runs on torch's current stream and takes its workspace from torch's

@@ -88,3 +88,48 @@ def test_forward_mode_of_the_update_is_refused():
             tg.newton_schulz(fwad.make_dual(G, G))
         with pytest.raises(NotImplementedError, match="forward-mode"):
             tg.newton_schulz(G, out=fwad.make_dual(G.bfloat16(), G.bfloat16()))
+
+
+def test_a_second_derivative_raises_where_it_is_taken(card):
+    H, W, t = card
+    h, w = H.clone().requires_grad_(), W.clone().requires_grad_()
+    plain = torch.autograd.grad(tg.linear_cross_entropy(h, w, t), (h, w))
+    loss = tg.linear_cross_entropy(h, w, t)
+    dH, dW = torch.autograd.grad(loss, (h, w), create_graph=True)
+    # the first derivatives are there and are the same
+    assert torch.equal(dH, plain[0]) and torch.equal(dW, plain[1])
+    for term in (dH, dW):
+        with pytest.raises(RuntimeError, match="once"):
+            (loss + term.float().square().sum()).backward(retain_graph=True)
+        assert h.grad is None and w.grad is None
+    # what does not go through them is not held up
+    (loss + dH.detach().float().square().sum()).backward()
+    assert torch.equal(h.grad, plain[0]) and torch.equal(w.grad, plain[1])
+
+
+def test_a_second_derivative_of_one_operand_raises(card):
+    H, W, t = card
+    h = H.clone().requires_grad_()
+    dH, = torch.autograd.grad(tg.linear_cross_entropy(h, W, t), h, create_graph=True)
+    with pytest.raises(RuntimeError, match="once"):
+        dH.float().sum().backward()
+    w = W.clone().requires_grad_()
+    loss, lse = tg.linear_cross_entropy(H, w, t, return_lse=True)
+    dW, = torch.autograd.grad(loss + lse.square().sum(), w, create_graph=True)
+    with pytest.raises(RuntimeError, match="once"):
+        dW.float().sum().backward()
+
+
+def test_a_derivative_along_the_upstream_gradient_raises(card):
+    H, W, t = card
+    h = H.clone().requires_grad_()
+    up = torch.ones((), requires_grad=True)
+    dH, = torch.autograd.grad(tg.linear_cross_entropy(h, W, t) * up, h, create_graph=True)
+    with pytest.raises(RuntimeError, match="once"):
+        torch.autograd.grad(dH.float().sum(), up)
+
+
+def test_hessian_products_raise(card):
+    H, W, t = card
+    with pytest.raises(RuntimeError, match="once"):
+        torch.autograd.functional.hvp(lambda h: tg.linear_cross_entropy(h, W, t), H, torch.ones_like(H))
