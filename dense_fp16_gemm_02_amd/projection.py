@@ -184,11 +184,22 @@ def _row_stride(t, name, width):
     return t.stride(0)
 
 
-def _refuse_tangents(what, *tensors):
-    """The library takes addresses, which carry no tangents: the result would come
-    back without one."""
+@functools.lru_cache(maxsize=None)
+def _mode_queries():
+    import torch
     from torch.autograd.forward_ad import unpack_dual
+    from torch.fx.experimental.proxy_tensor import get_proxy_mode
 
+    return torch.jit.is_tracing, get_proxy_mode, unpack_dual
+
+
+def _refuse_modes(what, *tensors):
+    """The library takes addresses.  They carry no tangents: the result would come
+    back without one.  And a trace does not see the call: it would hold the result's
+    torch.empty alone."""
+    is_tracing, get_proxy_mode, unpack_dual = _mode_queries()
+    if is_tracing() or get_proxy_mode() is not None:
+        raise NotImplementedError(f"{what} cannot be traced")
     if any(t is not None and unpack_dual(t).tangent is not None for t in tensors):
         raise NotImplementedError(f"{what} has no forward-mode derivative")
 
@@ -274,7 +285,7 @@ def _xent_function():
             H, W, target, lse = ctx.saved_tensors
             if dloss is None and dlse is None:
                 return None, None, None, None, None
-            _refuse_tangents("linear_cross_entropy (backward)", dloss, dlse)
+            _refuse_modes("linear_cross_entropy (backward)", dloss, dlse)
             if dloss is None:
                 dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, device=H.device)
             dloss = dloss.contiguous()
@@ -309,6 +320,7 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
     leaves is alive (autograd would accumulate on that graph's stream, which
     ends the capture).  Raises TypeError / ValueError on tensors it cannot take,
     NotImplementedError on dual tensors (there is no forward-mode derivative) and
+    while torch.jit.trace or make_fx records (they would not see the call), and
     TgError on a non-zero status.
     """
     import torch
@@ -327,7 +339,7 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
         raise ValueError(f"{target.shape[0]} targets for {H.shape[0]} rows of H")
     if reduction not in _REDUCTIONS:
         raise ValueError("reduction is 'none', 'sum' or 'mean'")
-    _refuse_tangents("linear_cross_entropy", H, W)
+    _refuse_modes("linear_cross_entropy", H, W)
     target = target.contiguous()
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         loss, lse = _xent_function().apply(H, W, target, ignore_index, _REDUCTIONS[reduction])
@@ -371,8 +383,8 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
 
     Runs on torch's current stream and takes its workspace from torch's
     allocator; not differentiable.  Raises TypeError / ValueError on tensors it
-    cannot take, NotImplementedError on dual tensors and TgError on a non-zero
-    status.
+    cannot take, NotImplementedError on dual tensors and while torch.jit.trace or
+    make_fx records, and TgError on a non-zero status.
     """
     import torch
 
@@ -393,7 +405,7 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
         out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
     elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
         raise ValueError("out must be a bfloat16 tensor of G's shape on G's device")
-    _refuse_tangents("newton_schulz", G, out)
+    _refuse_modes("newton_schulz", G, out)
     g, o = (G, out) if G.dim() == 3 else (G.unsqueeze(0), out.unsqueeze(0))
     batch, rows, cols = g.shape
     if batch == 0 or rows == 0 or cols == 0:

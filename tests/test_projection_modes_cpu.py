@@ -133,3 +133,37 @@ def test_hessian_products_raise(card):
     H, W, t = card
     with pytest.raises(RuntimeError, match="once"):
         torch.autograd.functional.hvp(lambda h: tg.linear_cross_entropy(h, W, t), H, torch.ones_like(H))
+
+
+def traced(fn, *args):
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    yield "make_fx", lambda: make_fx(fn)(*args)
+    yield "jit.trace", lambda: torch.jit.trace(fn, args, check_trace=False)
+    yield "symbolic_trace", lambda: torch.fx.symbolic_trace(fn)
+
+
+def test_tracing_is_refused(card):
+    """A trace would hold the torch.empty of the result and not the call that fills it."""
+    H, W, t = (x.as_subclass(torch.Tensor) for x in card)
+    as_is = lambda x: x if isinstance(x, torch.fx.Proxy) else x.as_subclass(OnCard)  # noqa: E731
+    cases = {
+        "cross entropy": (lambda h, w: tg.linear_cross_entropy(as_is(h), as_is(w), as_is(t)), (H, W)),
+        "update": (lambda g: tg.newton_schulz(as_is(g)), (H,)),
+    }
+    for what, (fn, args) in cases.items():
+        for how, call in traced(fn, *args):
+            with pytest.raises((NotImplementedError, TypeError, torch.fx.proxy.TraceError)) as e:
+                call()
+            if how != "symbolic_trace":  # its proxies stop at the first check of a type
+                assert e.type is NotImplementedError and "traced" in str(e.value), (what, how, e.value)
+
+
+def test_tracing_a_backward_pass_is_refused(card):
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    H, W, t = card
+    h = H.clone().requires_grad_()
+    loss = tg.linear_cross_entropy(h, W, t)
+    with pytest.raises(NotImplementedError, match="traced"):
+        make_fx(lambda up: torch.autograd.grad(loss, h, up)[0])(torch.ones(()))
