@@ -379,7 +379,8 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     the default is (3.4445, -4.7750, 2.0315).  ``out``, where given, is a bf16
     tensor of G's shape whose rows and matrices follow each other without
     overlapping; it may be G itself where that is fp16 or bf16, and share no
-    memory with G otherwise.
+    memory with G otherwise.  It is modified in place as torch counts it, and may
+    require grad only under torch.no_grad().
 
     Runs on torch's current stream and takes its workspace from torch's
     allocator; not differentiable.  Raises TypeError / ValueError on tensors it
@@ -405,6 +406,8 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
         out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
     elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
         raise ValueError("out must be a bfloat16 tensor of G's shape on G's device")
+    elif out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out requires grad, which the update does not propagate; write it under torch.no_grad()")
     _refuse_modes("newton_schulz", G, out)
     g, o = (G, out) if G.dim() == 3 else (G.unsqueeze(0), out.unsqueeze(0))
     batch, rows, cols = g.shape
@@ -430,4 +433,6 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
             st = fn(*args)
     if st:
         raise _pkg().TgError(st, "newton_schulz")
+    if given and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
     return out

@@ -167,3 +167,51 @@ def test_tracing_a_backward_pass_is_refused(card):
     loss = tg.linear_cross_entropy(h, W, t)
     with pytest.raises(NotImplementedError, match="traced"):
         make_fx(lambda up: torch.autograd.grad(loss, h, up)[0])(torch.ones(()))
+
+
+@pytest.fixture
+def update(monkeypatch):
+    """newton_schulz as far as the library's entry point, which accepts the call."""
+    from types import SimpleNamespace
+
+    entry = SimpleNamespace(tg_newton_schulz_workspace_bytes=lambda *a: 0, tg_newton_schulz_bf16=lambda *a: 0,
+                            tg_newton_schulz_f16=lambda *a: 0, tg_newton_schulz_f32=lambda *a: 0)
+    monkeypatch.setattr(pr, "_lib", lambda: entry)
+    monkeypatch.setattr(pr, "_ns_size", lambda *a: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    return lambda *shape: torch.ones(*shape, dtype=torch.bfloat16).as_subclass(OnCard)
+
+
+def test_out_is_written_as_torch_sees_it(update):
+    """A tensor saved for a backward pass must not be overwritten unnoticed."""
+    out = update(3, 4)
+    w = torch.ones(3, 4, dtype=torch.bfloat16, requires_grad=True)
+    loss = (w * out).sum()
+    before = out._version
+    assert tg.newton_schulz(update(3, 4), out=out) is out and out._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    base = update(2, 3, 4)
+    before = base._version
+    tg.newton_schulz(update(3, 4), out=base[1])
+    assert base._version > before  # through a view too
+    same = update(3, 4)
+    before = same._version
+    tg.newton_schulz(same, out=same)
+    assert same._version > before
+    before = same._version
+    tg.newton_schulz(same)
+    assert same._version == before
+    with torch.inference_mode():
+        tg.newton_schulz(update(3, 4), out=update(3, 4))
+
+
+def test_out_that_requires_grad_is_refused(update):
+    leaf = update(3, 4).requires_grad_()
+    for out in (leaf, leaf.view(3, 4), (leaf * 1.0)):
+        with pytest.raises(ValueError, match="requires grad"):
+            tg.newton_schulz(update(3, 4), out=out)
+    with torch.no_grad():  # as an optimizer writes its parameters
+        before = leaf._version
+        assert tg.newton_schulz(update(3, 4), out=leaf) is leaf and leaf._version > before
