@@ -1086,7 +1086,7 @@ extern "C" int tg_xent_plan(const void *H, const void *W, int64_t M, int64_t V, 
         name[0] = 0;
     if (pieces)
         *pieces = 0;
-    const int st = validate(H, W, M, V, K, ldh, ldw, true);
+    const int st = validate(H, W, M, V, K, ldh, ldw, backward_pass != 0);
     if (st != TG_OK || M == 0)
         return st;
     const Plan p = make_plan(H, W, M, V, K, ldh, ldw, backward_pass != 0);
