@@ -437,8 +437,8 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 // under one of work).  Two forms:
 //
 //   both sides at most 128   one workgroup runs the whole iteration, X (fp32)
-//                            in registers, the operands in LDS: 128x128 27 us
-//                            with the chain 65, 64x64 18 us;
+//                            in registers, the operands in LDS: 128x128 25 us
+//                            with the chain 65, 64x128 19, 64x64 14;
 //   a long side              two launches per step, and X read and written once
 //                            in it.  The strip kernel takes X in strips of 64
 //                            columns: update, store, and the strip's part of the
@@ -457,7 +457,8 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 // short side, and a direction whose singular value is small beside the norm is
 // amplified by up to 485 afterwards: with 64 and more of them that stays below
 // the result's own rounding, with a few it does not (a 2×2 matrix of condition
-// 100 came out 6e-3 off).  The forms for 64 rows therefore hold each operand as
+// 100 came out 6e-3 off, one of 2×100 and rank one 3e-2).  The forms for 64 rows
+// of the short side, however long the other, therefore hold each operand as
 // the sum of two binary16 values and take three products for each (the fourth,
 // of the two low parts, is below fp32).
 //
@@ -628,18 +629,23 @@ struct SmallArgs {
     float eps;
     float k[3 * TG_NS_MAX_STEPS];
 };
-template <typename G, int IM>
+// X is IM rows of L columns: 64×64 and 64×128 in two parts, 128×128 in one.  Two
+// parts of 64 rows are no more work than one of 128: 1x64x128 takes 19 us, as
+// 128×128 in one part 23, 512x64x128 33 and 50.
+template <typename G, int IM, int L>
 __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallArgs a)
 {
     using S = Small<IM>;
-    constexpr int TM = S::TM, TN = S::TN, PARTS = S::PARTS;
-    __shared__ __attribute__((aligned(1024))) half_t xi[PARTS * IM * IM];
+    constexpr int TM = S::TM, TN = L / S::WN / 16, PARTS = S::PARTS;  // a wave's blocks of X
+    constexpr int XPART = IM * L;
+    __shared__ __attribute__((aligned(1024))) half_t xi[PARTS * XPART];
     __shared__ __attribute__((aligned(1024))) typename S::Core m;
     __shared__ double sums[S::WAVES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fh = lane >> 4;
-    const int r0 = wave / S::WN * (IM / S::WM), c0 = wave % S::WN * (IM / S::WN);
+    const int r0 = wave / S::WN * (IM / S::WM), c0 = wave % S::WN * (L / S::WN);
+    const int g0 = wave % S::WN * (IM / S::WN);  // the wave's columns of the Gram matrix
     const G *g = reinterpret_cast<const G *>(a.g) + (int64_t)blockIdx.x * a.stride;
 
     // X in the accumulators' layout: block (i, j), row fr, columns 4·fh .. +3
@@ -699,15 +705,16 @@ __global__ __launch_bounds__(Small<IM>::WAVES * 64) void ns_small_kernel(SmallAr
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     v[k] = x[i][j][k] * X_SCALE;
-                image_put<PARTS, IM>(xi, S::PART, r0 + 16 * i + fr, c0 + 16 * j + 4 * fh, v);
+                image_put<PARTS, L>(xi, XPART, r0 + 16 * i + fr, c0 + 16 * j + 4 * fh, v);
             }
         __syncthreads();
+        f32x4 gram[TM][S::TN];
+        zero_blocks(gram);
+        image_product<PARTS, L, L, false, L / 32>(xi, XPART, xi, XPART, r0, g0, fr, fh, gram);
+        S::square(m, gram, a.k[3 * t + 1], a.k[3 * t + 2], r0, g0, fr, fh);
         f32x4 acc[TM][TN];
         zero_blocks(acc);
-        image_product<PARTS, IM, IM, false, IM / 32>(xi, S::PART, xi, S::PART, r0, c0, fr, fh, acc);
-        S::square(m, acc, a.k[3 * t + 1], a.k[3 * t + 2], r0, c0, fr, fh);
-        zero_blocks(acc);
-        image_product<PARTS, IM, IM, true, IM / 32>(m.pi, S::PART, xi, S::PART, r0, c0, fr, fh, acc);
+        image_product<PARTS, IM, L, true, IM / 32>(m.pi, S::PART, xi, XPART, r0, c0, fr, fh, acc);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const float f = a.k[3 * t] + m.e[r0 + 16 * i + fr];
@@ -1014,6 +1021,7 @@ struct Plan {
     int64_t s, l, ldx, lds;
     bool tall, small, thin;
     int image;        // rows of the short side's image (small, thin)
+    int columns;      // of X's image (small)
     int strips, per, groups, reducers;  // thin
     Class gram, square, upd;
     int splits;       // of the gram product's contraction
@@ -1032,7 +1040,7 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
     p.small = std::max(rows, cols) <= 128;
     p.s = std::min(rows, cols), p.l = std::max(rows, cols);
     p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
-    p.image = (p.small ? p.l : p.s) <= 64 ? 64 : 128;
+    p.image = p.s <= 64 ? 64 : 128, p.columns = p.l <= 64 ? 64 : 128;
     // Up to 64 rows always take the strips: the operands in two parts are right
     // where one is not, and nothing was slower (1x64x200 66 -> 53 us, 1x16x14336
     // 133 -> 79, 1x64x131072 705 -> 160, 32x64x14336 500 -> 305, 300x64x300
@@ -1236,8 +1244,9 @@ int newton_schulz(const void *g, void *o, int64_t batch, int64_t rows, int64_t c
     if (p.small) {
         SmallArgs a = {g, ldg, g_stride, out, ldo, o_stride, (int)p.s, (int)p.l, p.tall, steps, eps, {}};
         memcpy(a.k, k, sizeof k);
-        const bool ok = p.image == 64 ? launch(ns_small_kernel<G, 64>, batch, Small<64>::WAVES * 64, stream, a)
-                                  : launch(ns_small_kernel<G, 128>, batch, Small<128>::WAVES * 64, stream, a);
+        const bool ok = p.columns == 64 ? launch(ns_small_kernel<G, 64, 64>, batch, Small<64>::WAVES * 64, stream, a)
+                        : p.image == 64 ? launch(ns_small_kernel<G, 64, 128>, batch, Small<64>::WAVES * 64, stream, a)
+                                        : launch(ns_small_kernel<G, 128, 128>, batch, Small<128>::WAVES * 64, stream, a);
         return ok ? TG_OK : TG_ERR_LAUNCH;
     }
     bool ok = launch(ns_norm_kernel<G>, batch * p.norm_blocks, 256, stream, src, rows, cols, ldg, g_stride,
@@ -1343,7 +1352,7 @@ extern "C" int tg_newton_schulz_plan(int64_t batch, int64_t rows, int64_t cols, 
         return st;
     const Plan p = make_plan(batch, rows, cols);
     if (name && name_len > 0 && p.small)
-        snprintf(name, (size_t)name_len, "small_%d", p.image);
+        snprintf(name, (size_t)name_len, "small_%d", p.columns);
     else if (name && name_len > 0 && p.thin)
         snprintf(name, (size_t)name_len, "thin_%d", p.image);
     else if (name && name_len > 0)
