@@ -318,13 +318,16 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
     allocator; it may be captured into a graph, its backward pass with
     torch.autograd.grad, or with .backward() where no eager graph of the same
     leaves is alive (autograd would accumulate on that graph's stream, which
-    ends the capture).  Raises TypeError / ValueError on tensors it cannot take,
+    ends the capture).  Under torch.compile it runs between the compiled parts.
+    Raises TypeError / ValueError on tensors it cannot take,
     NotImplementedError on dual tensors (there is no forward-mode derivative) and
     while torch.jit.trace or make_fx records (they would not see the call), and
     TgError on a non-zero status.
     """
     import torch
 
+    if torch.compiler.is_dynamo_compiling():  # the call stays between the compiled parts
+        return torch.compiler.disable(linear_cross_entropy)(H, W, target, ignore_index, reduction, return_lse)
     if H.dtype != W.dtype or H.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("H and W must both be float16 or both bfloat16")
     if target.dtype != torch.int64:
@@ -383,12 +386,15 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     require grad only under torch.no_grad().
 
     Runs on torch's current stream and takes its workspace from torch's
-    allocator; not differentiable.  Raises TypeError / ValueError on tensors it
+    allocator; not differentiable.  Under torch.compile it runs between the
+    compiled parts.  Raises TypeError / ValueError on tensors it
     cannot take, NotImplementedError on dual tensors and while torch.jit.trace or
     make_fx records, and TgError on a non-zero status.
     """
     import torch
 
+    if torch.compiler.is_dynamo_compiling():  # the call stays between the compiled parts
+        return torch.compiler.disable(newton_schulz)(G, steps, coefficients, eps, out)
     if G.dtype not in (torch.float32, torch.float16, torch.bfloat16):
         raise TypeError("G must be float32, float16 or bfloat16")
     if not G.is_cuda:

@@ -1,0 +1,51 @@
+"""The projection operators under torch.compile: the call runs as it is, between the
+compiled parts, and gives what it gives without.  (The modes that are refused are in
+test_projection_modes_cpu.py.)"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+tg = pytest.importorskip("dense_fp16_gemm_02_amd")
+
+
+def operands():
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    H = torch.randn(60, 136, generator=gen, device="cuda").half()
+    W = torch.randn(300, 136, generator=gen, device="cuda").half()
+    return H, W, torch.randint(0, 300, (60,), generator=gen, device="cuda")
+
+
+@pytest.mark.parametrize("backend", ["eager", "aot_eager"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_compiled_cross_entropy(backend, grad):
+    torch._dynamo.reset()
+    H, W, t = operands()
+
+    def f(h, w):
+        loss, lse = tg.linear_cross_entropy(h * 0.5, w, t, return_lse=True)
+        return 2.0 * loss + 1e-4 * lse.square().sum()
+
+    compiled = torch.compile(f, backend=backend)
+    for scale in (1.0, 2.0):
+        h, w = (H * scale).requires_grad_(grad), W.clone().requires_grad_(grad)
+        want, got = f(h, w), compiled(h, w)
+        assert torch.equal(got, want)
+        if grad:
+            for a, b in zip(torch.autograd.grad(got, (h, w)), torch.autograd.grad(want, (h, w))):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("backend", ["eager", "aot_eager"])
+def test_compiled_update(backend):
+    torch._dynamo.reset()
+    H, W, _ = operands()
+
+    def f(g, out):
+        tg.newton_schulz(g * 2.0, steps=3, out=out)
+        return out.float() + tg.newton_schulz(g, coefficients=(1.5, -0.5, 0.0)).float()
+
+    compiled = torch.compile(f, backend=backend)
+    for scale in (1.0, 3.0):
+        g = W * scale
+        a, b = (torch.empty_like(g, dtype=torch.bfloat16) for _ in range(2))
+        assert torch.equal(compiled(g, a), f(g, b)) and torch.equal(a, b)
