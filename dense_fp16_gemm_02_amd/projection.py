@@ -352,10 +352,23 @@ def linear_cross_entropy(H, W, target, ignore_index: int = -100, reduction: str 
 
 
 def _meet(a, b):
-    """Whether the memory from first to last element of two tensors overlaps."""
+    """Whether two batches of matrices of one shape share memory."""
+    import torch
+
     (a0, a1), (b0, b1) = ((t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum(
         (n - 1) * s for n, s in zip(t.shape, t.stride())))) for t in (a, b))
-    return a0 < b1 and b0 < a1
+    if a1 <= b0 or b1 <= a0:
+        return False
+
+    # windows of one buffer: row by row
+    def rows(t):
+        at = [torch.arange(n, device="cpu") * s for n, s in zip(t.shape[:2], t.stride())]
+        start = (at[0][:, None] + at[1]).flatten() * t.element_size() + t.data_ptr()
+        return start.sort().values, t.shape[2] * t.element_size()
+
+    (ra, wa), (rb, wb) = rows(a), rows(b)
+    # rows of b from the first that ends behind a row's start to the last that begins before its end
+    return bool((torch.searchsorted(rb, ra + wa) > torch.searchsorted(rb, ra - wb, right=True)).any())
 
 
 @functools.lru_cache(maxsize=1024)

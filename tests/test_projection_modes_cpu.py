@@ -215,3 +215,47 @@ def test_out_that_requires_grad_is_refused(update):
     with torch.no_grad():  # as an optimizer writes its parameters
         before = leaf._version
         assert tg.newton_schulz(update(3, 4), out=leaf) is leaf and leaf._version > before
+
+
+def elements(t):
+    """Byte addresses of every element of a 3-D tensor."""
+    b, m, n = t.shape
+    return {t.data_ptr() + t.element_size() * (i * t.stride(0) + j * t.stride(1) + k * t.stride(2)) + byte
+            for i in range(b) for j in range(m) for k in range(n) for byte in range(t.element_size())}
+
+
+def test_out_beside_g_in_one_buffer_is_taken(update):
+    """Windows that share no element, whatever lies between their first and last."""
+    room = update(6, 40)
+    tg.newton_schulz(room[:, :12], out=room[:, 12:24])
+    tg.newton_schulz(room[0::2, :12], out=room[1::2, :12])
+    batch = update(3, 6, 40)
+    tg.newton_schulz(batch[:, :, :7], out=batch[:, :, 7:14])
+    tg.newton_schulz(batch[:, :3], out=batch[:, 3:])
+    wide = torch.ones(4, 20).as_subclass(OnCard)  # fp32 on the left, the result on the right half of each row
+    tg.newton_schulz(wide[:, :10], out=wide.view(torch.bfloat16)[:, 20:30])
+    with pytest.raises(ValueError, match="overlaps G"):
+        tg.newton_schulz(wide[:, :10], out=wide.view(torch.bfloat16)[:, 19:29])
+    with pytest.raises(ValueError, match="overlaps G"):
+        tg.newton_schulz(room[:, :12], out=room[:, 11:23])
+    with pytest.raises(ValueError, match="overlaps G"):
+        tg.newton_schulz(batch[:, :4], out=batch[:, 2:])
+
+
+def test_overlap_is_found_as_by_listing_every_byte():
+    import random
+
+    rng = random.Random(0)
+    room = torch.zeros(4096, dtype=torch.uint8)
+    seen = {True: 0, False: 0}
+    for _ in range(3000):
+        b, m, n = rng.randint(1, 3), rng.randint(1, 4), rng.randint(1, 6)
+        pair = []
+        for dt in (rng.choice((torch.float32, torch.bfloat16)), torch.bfloat16):
+            row = rng.randint(n, 14)
+            stride = rng.choice((0, rng.randint(1, 3), rng.randint(n, 60)))
+            pair.append(torch.as_strided(room.view(dt), (b, m, n), (stride, row, 1), rng.randint(0, 40)))
+        want = bool(elements(pair[0]) & elements(pair[1]))
+        assert pr._meet(*pair) == want, [(t.shape, t.stride(), t.dtype, t.storage_offset()) for t in pair]
+        seen[want] += 1
+    assert min(seen.values()) > 300
