@@ -1,10 +1,14 @@
 """The host-only queries of the projection operators agree with the calls they
-speak for."""
+speak for; and every kernel they choose is run by a GPU test."""
 import itertools
+import math
+import random
 
 import pytest
 
 tg = pytest.importorskip("dense_fp16_gemm_02_amd")
+
+import projection_cases as cases  # noqa: E402
 
 A = 1 << 20  # 16-byte aligned, never dereferenced
 
@@ -25,3 +29,28 @@ def test_a_plans_status_is_that_of_its_direction():
         if (sizes[0] < 0) != (sizes[1] < 0):
             differ.add(sizes[0] < 0)
     assert differ == {True, False}  # each direction is refused somewhere the other is not
+
+
+def sizes(seed, count, *ranges):
+    """Sizes spread over the logarithms of their ranges, the same in every run."""
+    rng = random.Random(seed)
+    for _ in range(count):
+        yield tuple(int(round(math.exp(rng.uniform(math.log(lo), math.log(hi))))) for lo, hi in ranges)
+
+
+def test_listed_plans_hold():
+    for b, m, n, plan in cases.NEWTON_SCHULZ:
+        assert tg.tg_newton_schulz_plan(b, m, n) == (tg.TG_OK, plan)
+
+
+def test_gpu_tests_reach_every_newton_schulz_kernel():
+    import test_gpu_newton_schulz as gpu
+
+    run = set()
+    for size in gpu.SIZES + gpu.THIN + [c[:3] for c in cases.NEWTON_SCHULZ]:
+        run |= cases.newton_schulz_kernels(*size)
+    reachable = set()
+    for b, m, n in sizes(1, 40000, (1, 64), (1, 14336), (1, 14336)):
+        if b * m * n * min(m, n) <= 14336 * 4096 * 4096:
+            reachable |= cases.newton_schulz_kernels(b, m, n)
+    assert len(reachable) >= 26 and reachable <= run, reachable - run
