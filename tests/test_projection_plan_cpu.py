@@ -41,6 +41,9 @@ def sizes(seed, count, *ranges):
 def test_listed_plans_hold():
     for b, m, n, plan in cases.NEWTON_SCHULZ:
         assert tg.tg_newton_schulz_plan(b, m, n) == (tg.TG_OK, plan)
+    for M, V, K, fwd, fwd_pieces, bwd, bwd_pieces in cases.XENT:
+        assert tg.tg_xent_plan(A, A, M, V, K, K, K, 0) == (tg.TG_OK, fwd, fwd_pieces)
+        assert tg.tg_xent_plan(A, A, M, V, K, K, K, 1) == (tg.TG_OK, bwd, bwd_pieces)
 
 
 def test_gpu_tests_reach_every_newton_schulz_kernel():
@@ -54,3 +57,16 @@ def test_gpu_tests_reach_every_newton_schulz_kernel():
         if b * m * n * min(m, n) <= 14336 * 4096 * 4096:
             reachable |= cases.newton_schulz_kernels(b, m, n)
     assert len(reachable) >= 26 and reachable <= run, reachable - run
+
+
+def test_gpu_tests_reach_every_cross_entropy_kernel():
+    import test_gpu_xent as gpu
+
+    run = set()
+    for size in gpu.SHAPES + [(4096, 8000, 4160)] + [c[:3] for c in cases.XENT]:
+        run |= cases.xent_kernels(*size)
+    reachable = set()
+    for M, V, K in sizes(2, 60000, (1, 20000), (64, 300000), (8, 8192)):
+        if M * V * K <= 2 ** 42:
+            reachable |= cases.xent_kernels(M, V, K) | cases.xent_kernels(M, V, (K + 7) // 8 * 8)
+    assert len(reachable) >= 30 and reachable <= run, reachable - run
