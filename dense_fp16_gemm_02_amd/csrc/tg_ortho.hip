@@ -27,6 +27,9 @@
 // 1.66e-3 to 1.85e-3 (relative, 2-norm) for the bfloat16 result, 1.66e-3 being
 // the rounding of the result itself; with B rounded whole 2.1e-3 to 2.7e-3,
 // with X carried in 16 bits up to 4.4e-3, with bfloat16 operands 1e-2 to 3e-2.
+// Where many directions are far below the norm, or the rank is low, the rounding of
+// the operands shows more (include/tg_ortho.h has the figures): up to 64 rows they
+// are held in two parts, above in one, as two would take three times the products.
 //
 // Operands are binary16 times 2^14 (X) and 2^12 (O, P): entries of X start near
 // (rows·cols)^-1/2 and of O near 1/s·l^-1/2, far below binary16's 2^-14, and the

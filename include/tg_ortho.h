@@ -18,16 +18,27 @@
  * times 2^14, A and B times 2^12), so that every operand keeps 11 significant
  * bits at any magnitude met; the diagonals of A and B, which hold most of
  * their weight, stay in fp32 outside the products.  The result is bfloat16,
- * rounded once; its distance from the 64-bit result is that of the rounding to
- * within some 15% where the small singular values are those of many
- * directions.  A direction with less than some 1e-2 of the norm is amplified by
- * up to 485, and with it the part of the operands' rounding that falls there;
- * the fewer rows the shorter side has, the larger that part.  Up to 64 of them
- * every operand is therefore the sum of two binary16 values (22 bits), and the
- * result within 2^-8 of the 64-bit one at any spectrum.  Above 64 one value is
- * held: where all of a matrix is in a few of its rows and these are nearly
- * parallel, the result was measured up to 1.7e-2 off (two rows), 1.0e-2 (four),
- * 4e-3 (64); for a single row, or equal rows, up to 7.4e-3.  The scales bound the
+ * rounded once, which by itself is 1.66e-3 of the 64-bit result (2-norm, root
+ * mean square; at most 2^-8).
+ *
+ * A direction with a small part of the norm is amplified by up to 485 in five
+ * steps, and with it the part of the operands' rounding that falls there.  Up to 64
+ * rows of the shorter side every operand is therefore the sum of two binary16
+ * values (22 bits), and the result within 2^-8 of the 64-bit one at any spectrum.
+ * Above 64 one value is held, and the error depends on the spectrum:
+ *
+ *     noise, 1/k, singular values from 1 to 1e-2          up to 1.9e-3
+ *     rows parallel to 1e-2; to 1e-3                      up to 1.8e-3; 2.6e-3
+ *     half of the singular values at 1, half at 1e-2      2.1e-3 to 3.5e-3
+ *     an eighth at 1, the others at 1e-3                  2.0e-3 to 3.6e-3
+ *     equal rows; equal elements                          up to 5.3e-3; 8.9e-3
+ *     rank four; one   65 rows up to 4.6e-3; 9.2e-3, 128 2.8e-3; 4.1e-3, 1000 1.7e-3
+ *     all of it in a few rows of the shorter side, of rank one or parallel to
+ *     1e-3             2 to 4 rows up to 4.5e-2, 8 3.7e-2, 16 3e-2, 64 9e-3
+ *                      parallel to 1e-2: 2 rows up to 1.3e-2, 4 5e-3, 64 1.8e-3
+ *
+ * (up to: the largest that matrices of 65 to 1500 rows gave, a few of each kind
+ * and size).  The scales bound the
  * iterates: the singular values of X have to stay below 4 and those of B below
  * 16 (the default coefficients keep them below 1.3 and 3); beyond, elements
  * overflow to infinity.
