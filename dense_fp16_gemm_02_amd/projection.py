@@ -189,19 +189,21 @@ def _mode_queries():
     import torch
     from torch.autograd.forward_ad import unpack_dual
     from torch.fx.experimental.proxy_tensor import get_proxy_mode
+    from torch.utils._python_dispatch import is_in_torch_dispatch_mode
 
-    return torch.jit.is_tracing, get_proxy_mode, unpack_dual
+    return torch.jit.is_tracing, is_in_torch_dispatch_mode, get_proxy_mode, unpack_dual
 
 
 def _refuse_modes(what, *tensors):
     """The library takes addresses.  They carry no tangents: the result would come
     back without one.  And a trace does not see the call: it would hold the result's
     torch.empty alone."""
-    is_tracing, get_proxy_mode, unpack_dual = _mode_queries()
-    if is_tracing() or get_proxy_mode() is not None:
+    is_tracing, in_any_mode, get_proxy_mode, unpack_dual = _mode_queries()
+    if is_tracing() or (in_any_mode() and get_proxy_mode() is not None):
         raise NotImplementedError(f"{what} cannot be traced")
-    if any(t is not None and unpack_dual(t).tangent is not None for t in tensors):
-        raise NotImplementedError(f"{what} has no forward-mode derivative")
+    for t in tensors:
+        if t is not None and unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward-mode derivative")
 
 
 @functools.lru_cache(maxsize=1024)
