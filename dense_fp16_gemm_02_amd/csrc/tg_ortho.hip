@@ -447,10 +447,10 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 //                            columns: update, store, and the strip's part of the
 //                            next Gram matrix, from the image it already holds.
 //                            The core kernel adds the parts and, in the workgroup
-//                            that finishes last, does the square: 1x64x4096 66 us
-//                            with the chain 95, of which the core's wait for
+//                            that finishes last, does the square: 1x64x4096 60 us
+//                            with the chain 87, of which the core's wait for
 //                            memory, three trips there one after the other, is
-//                            the longest part (8 us of each step's 13).
+//                            the longest part (6 us of each step's 11).
 //
 // X is held with the shorter side as rows (`flip`: G and the result are
 // transposed on the way), so that no other form is needed.  Images are IM rows,
@@ -1045,24 +1045,24 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
     p.ldx = round_up(cols, BK), p.lds = round_up(p.s, BK);
     p.image = p.s <= 64 ? 64 : 128, p.columns = p.l <= 64 ? 64 : 128;
     // Up to 64 rows always take the strips: the operands in two parts are right
-    // where one is not, and nothing was slower (1x64x200 66 -> 53 us, 1x16x14336
-    // 133 -> 79, 1x64x131072 705 -> 160, 32x64x14336 500 -> 305, 300x64x300
-    // 166 -> 137).  Up to 128 rows a workgroup's Gram matrix is twice a strip's
-    // bytes, which pays for one matrix (1x100x200 76 -> 73, 1x128x14336
-    // 174 -> 133) and for long ones (8x128x4096 163 -> 145, 32x128x14336
-    // 1023 -> 732), and not for several short ones (16x128x1024 104 with the
-    // chain, 136 with strips; 32x100x1000 128 and 143).
+    // where one is not, and nothing was slower (1x64x200 59 -> 48 us, 1x16x14336
+    // 124 -> 73, 1x64x131072 676 -> 162, 32x64x14336 502 -> 316, 300x64x300
+    // 164 -> 136).  Up to 128 rows a workgroup's Gram matrix is twice a strip's
+    // bytes, which pays for one matrix (1x100x200 69 -> 63, 1x128x14336
+    // 171 -> 132) and for long ones (8x128x4096 160 -> 140, 32x128x14336
+    // 1013 -> 730), and not for several short ones (16x128x1024 99 with the
+    // chain, 135 with strips; 32x100x1000 126 and 143).
     p.thin = !p.small && (p.s <= 64 || (p.s <= 128 && (batch == 1 || p.l >= 2048)));
-    // Workgroups: with 512 and 256 in all, 32x64x14336 takes 305 and 520 us and
-    // 1x64x131072 160 and 185; for 128 rows 8x128x4096 157 and 145, 1x128x131072
-    // 281 and 261 (128x128x2048 378 and 384; 128 in all: 613).
+    // Workgroups: with 512 and 256 in all, 32x64x14336 takes 313 and 432 us and
+    // 1x64x131072 158 and 178; for 128 rows 8x128x4096 154 and 139, 1x128x131072
+    // 281 and 259, 128x128x2048 402 and 390.
     p.strips = (int)cdiv(p.l, STRIP);
     const int64_t most = std::max((int64_t)1, std::min((int64_t)p.strips, (p.image == 64 ? 512 : 256) / batch));
     p.per = (int)cdiv(p.strips, most);
     p.groups = (int)cdiv(p.strips, p.per);
     // Workgroups that add up one matrix's parts: each costs a write past the
     // caches and an arrival, so few where the matrices are many (8x64x4096 with
-    // 32 each 113 us, with 8 each 99; 1x64x131072 with 16 175, with 32 160).
+    // 32 each 109 us, with 8 each 95; 1x64x131072 with 16 171, with 32 157).
     p.reducers = 1;
     while (p.groups > 4 && p.reducers < (p.groups <= 16 ? 8 : 32) && 2 * p.reducers * batch <= 64)
         p.reducers *= 2;
@@ -1078,7 +1078,9 @@ Plan make_plan(int64_t batch, int64_t rows, int64_t cols)
     p.square = best(SYM_CLASS, sym, p.s);
     // splits that fill the slots of a small class, at least 4 K-tiles each, where
     // with the second kernel (some 5 us and the partial tiles twice through the
-    // caches) they are faster than the best class without
+    // caches) they are faster than the best class without.  (The larger classes and
+    // the square product are not split: their split forms are not built, and what
+    // they would take is not measured.)
     p.splits = 1, p.per_split = p.l;
     const int64_t kt = cdiv(p.l, BK);
     double t = tile_time(SYM_CLASS[p.gram], sym(SYM_CLASS[p.gram].bm), kt);

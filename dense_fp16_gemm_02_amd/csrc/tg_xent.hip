@@ -211,8 +211,8 @@ __global__ __launch_bounds__(PREP_THREADS) void xent_prep_kernel(PrepArgs a)
 }
 
 // Rows of W padded with zeros to K8 columns (W whose rows are not aligned).  Bound
-// by memory: 60000×2047 in 101 us (492 MB, 4.9 TB/s; 143 with loads of one element
-// each), 20000×1001 in 14 (23).
+// by memory: with nothing of W in the caches 60000×2047 in 138 us (492 MB, 3.6 TB/s;
+// 164 with loads of one element each), 20000×1001 in 23 (31).
 __global__ __launch_bounds__(256) void xent_pack_kernel(const uint16_t *src, int64_t ld, uint16_t *dst, int64_t rows,
                                                         int64_t K, int64_t K8)
 {
@@ -683,9 +683,9 @@ constexpr TileClass CLASS[] = {{256, 256, 1, 1.50, 1.50, 16.0},
                                {64, 64, 2, 0.50, 0.27, 4.0},
                                {64, 128, 2, 0.80, 0.45, 5.0}};
 // `stream`: one row of tiles and a W larger than the 256 MB last-level cache, so
-// that each element of W comes from memory, once (100×50001×4096 92 -> 80 us,
-// 250×131072×2048 149 -> 126; a W that the cache still holds is read faster
-// without: 200×50001×1000 38 against 43).
+// that each element of W comes from memory, once (a forward call of 100×50001×4096
+// 106 -> 91 us, 250×131072×2048 165 -> 132; a W that the cache still holds is read
+// faster without: 200×50001×1000 42 against 50).
 template <typename E, bool TA, bool TB, typename F>
 bool with_tile(Class c, bool stream, F f)
 {
