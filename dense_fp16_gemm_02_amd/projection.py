@@ -437,7 +437,8 @@ def newton_schulz(G, steps: int = 5, coefficients=None, eps: float = 1e-7, out=N
     ldg, ldo = _row_stride(g[0], "G", cols), _row_stride(o[0], "out", cols)
     if batch > 1 and o.stride(0) < (rows - 1) * ldo + cols:
         raise ValueError("out has overlapping or interleaved matrices")
-    if given and out is not G and _meet(g, o) and (g.data_ptr(), g.stride(), g.element_size()) != (o.data_ptr(), o.stride(), 2):
+    in_place = (g.data_ptr(), g.stride(), g.element_size()) == (o.data_ptr(), o.stride(), 2)
+    if given and not in_place and _meet(g, o):
         raise ValueError("out overlaps G")
     lib = _lib()
     size = _ns_size(batch, rows, cols)

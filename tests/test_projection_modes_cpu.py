@@ -259,3 +259,13 @@ def test_overlap_is_found_as_by_listing_every_byte():
         assert pr._meet(*pair) == want, [(t.shape, t.stride(), t.dtype, t.storage_offset()) for t in pair]
         seen[want] += 1
     assert min(seen.values()) > 300
+
+
+def test_in_place_is_not_compared_row_by_row(update, monkeypatch):
+    monkeypatch.setattr(pr, "_meet", lambda *a: pytest.fail("compared"))
+    G = update(2, 3, 4)
+    tg.newton_schulz(G, out=G)
+    tg.newton_schulz(G[1], out=G[1])
+    tg.newton_schulz(G.half(), out=None)
+    half = G.half()
+    tg.newton_schulz(half, out=half.view(torch.bfloat16))
