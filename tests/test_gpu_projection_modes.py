@@ -1,5 +1,5 @@
-"""The projection operators under torch.compile: the call runs as it is, between the
-compiled parts, and gives what it gives without.  (The modes that are refused are in
+"""The projection operators under torch.compile (the call runs as it is, between the
+compiled parts, and gives what it gives without) and create_graph.  (What is refused is in
 test_projection_modes_cpu.py.)"""
 import pytest
 
@@ -49,3 +49,21 @@ def test_compiled_update(backend):
         g = W * scale
         a, b = (torch.empty_like(g, dtype=torch.bfloat16) for _ in range(2))
         assert torch.equal(compiled(g, a), f(g, b)) and torch.equal(a, b)
+
+
+def test_first_derivatives_under_create_graph_and_no_second_ones():
+    H, W, t = operands()
+    h, w = H.requires_grad_(), W.requires_grad_()
+    plain = torch.autograd.grad(tg.linear_cross_entropy(h, w, t), (h, w))
+    loss, lse = tg.linear_cross_entropy(h, w, t, return_lse=True)
+    dH, dW = torch.autograd.grad(loss, (h, w), create_graph=True)
+    assert torch.equal(dH, plain[0]) and torch.equal(dW, plain[1])
+    for term in (dH, dW):
+        with pytest.raises(RuntimeError, match="once"):
+            torch.autograd.grad(term.float().square().sum(), (h, w), retain_graph=True)
+    # the update written over a tensor that a graph holds
+    out = torch.zeros_like(W, dtype=torch.bfloat16)
+    held = (torch.ones_like(out, requires_grad=True) * out).sum()
+    assert torch.equal(tg.newton_schulz(W.detach(), out=out), tg.newton_schulz(W.detach()))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        held.backward()
