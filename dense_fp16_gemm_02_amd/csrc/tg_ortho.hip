@@ -458,8 +458,8 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 //
 // The rounding of X's operand spreads evenly over the s directions of the
 // short side, and a direction whose singular value is small beside the norm is
-// amplified by up to 485 afterwards: with 64 and more of them that stays below
-// the result's own rounding, with a few it does not (a 2×2 matrix of condition
+// amplified by up to 485 afterwards: with many directions that stays below the
+// result's own rounding for most spectra, with a few it does not (a 2×2 matrix of condition
 // 100 came out 6e-3 off, one of 2×100 and rank one 3e-2).  The forms for 64 rows
 // of the short side, however long the other, therefore hold each operand as
 // the sum of two binary16 values and take three products for each (the fourth,
