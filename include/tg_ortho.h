@@ -28,6 +28,7 @@
  * Above 64 one value is held, and the error depends on the spectrum:
  *
  *     noise, 1/k, singular values from 1 to 1e-2          up to 1.9e-3
+ *     noise of 5e-2; of 1e-2 beside eight directions      up to 1.9e-3; 2.5e-3
  *     rows parallel to 1e-2; to 1e-3                      up to 1.8e-3; 2.6e-3
  *     half of the singular values at 1, half at 1e-2      2.1e-3 to 3.5e-3
  *     an eighth at 1, the others at 1e-3                  2.0e-3 to 3.6e-3

@@ -16,16 +16,18 @@
  *
  * The logits are products of the 16-bit operands summed in fp32; maxima,
  * sums, lse and losses are fp32.  For the gradients the logits are computed
- * again, a piece of the vocabulary at a time; G, scaled by its largest |g| so
- * that it lies in [-1, 1] (times 2^14 for binary16, whose exponent range would
- * flush small probabilities), is rounded once to the operands' type, as the
- * matrix cores take it; dH and dW are summed in fp32 and rounded once.  (Against
+ * again, a piece of the vocabulary at a time; G, scaled so that the largest of
+ * its coefficients (g_i and g_i + l_i) is 1 (2^14 for binary16, whose exponent range
+ * would flush small probabilities), is rounded once to the operands' type, as the
+ * matrix cores take it; dH and dW are summed in fp32 and rounded once.  Against
  * gradients of an unrounded G that is 1.9e-3 for bfloat16 instead of 1.66e-3, the
- * result's own rounding, and 2.5e-4 instead of 2.1e-4 for binary16.)  One scale
- * serves all tokens: in binary16 an element of G below 2^-28 of the largest |g|
- * errs by up to 2^-39 of that, so the row of dH of a token whose weight is far
- * below another's is inexact (50001 words: 4e-4 off at 1e-6 of the largest weight,
- * 5e-3 at 1e-7, 4e-2 at 1e-8).
+ * result's own rounding, and 2.5e-4 instead of 2.1e-4 for binary16; where few
+ * tokens or words make up an element the two roundings come to 2.4e-3 and 3e-4.
+ * One scale serves all tokens: in binary16 an element of G below 2^-28 of the
+ * largest coefficient errs by up to 2^-39 of it, so the row of dH of a token whose
+ * weight is far below another's is inexact (50001 words: 4e-4 off at 1e-6 of the
+ * largest weight, 5e-3 at 1e-7, 4e-2 at 1e-8).
+ *
  * Results do not depend on the order in which workgroups run: repeated calls
  * give the same bits.
  */
