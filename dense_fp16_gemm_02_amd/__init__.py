@@ -13,7 +13,10 @@ not built, importing the functions below raises.
 
 and, from ``projection.py``, the operators around a trained projection: the
 softmax cross entropy of H·Wᵀ with its gradients (``linear_cross_entropy``) and
-the Newton–Schulz update (``newton_schulz``), with their C entry points.
+the Newton–Schulz update (``newton_schulz``), with their C entry points; from
+``training.py`` those of a training step around them: products of rows grouped by
+expert (``grouped_linear``), the embedding lookup (``embedding``), both with their
+gradients, and the AdamW step (``adamw``, ``adamw_8bit``).
 
 Pointers may be given as torch tensors (their ``data_ptr()``) or integers;
 ``stream`` may be a ``torch.cuda.Stream``, an integer hipStream_t or None
@@ -30,6 +33,13 @@ from .projection import (TG_NS_MAX_STEPS, TG_XENT_MEAN, TG_XENT_NONE, TG_XENT_SU
                          tg_xent_bwd_f16, tg_xent_bwd_workspace_bytes, tg_xent_f16, tg_xent_plan,
                          tg_xent_workspace_bytes)
 from .projection import declare as _declare_projection
+from .training import (TG_ADAMW_BF16, TG_ADAMW_BLOCK, TG_ADAMW_F16, TG_ADAMW_F32, TG_GROUPED_DW, TG_GROUPED_DX,
+                       TG_GROUPED_Y, adamw, adamw_8bit, adamw_8bit_state, embedding, grouped_linear, tg_adamw,
+                       tg_adamw_config, tg_adamw_tensor, tg_embedding_bf16, tg_embedding_bwd_bf16,
+                       tg_embedding_bwd_f16, tg_embedding_bwd_f32, tg_embedding_bwd_workspace_bytes, tg_embedding_f16,
+                       tg_embedding_f32, tg_grouped_bf16, tg_grouped_dw_bf16, tg_grouped_dw_f16, tg_grouped_dx_bf16,
+                       tg_grouped_dx_f16, tg_grouped_f16, tg_grouped_plan, tg_grouped_workspace_bytes)
+from .training import declare as _declare_training
 
 __all__ = ["TG_OK", "TG_ERR_INVALID_ARG", "TG_ERR_LAUNCH", "TG_ERR_DEVICE", "TG_ERR_TOO_LARGE",
            "TG_ERR_LAYOUT", "TG_MFMA_F16_16X16X32", "TG_MFMA_F16_32X32X16", "TG_MFMA_BF16_16X16X32",
@@ -43,7 +53,13 @@ __all__ = ["TG_OK", "TG_ERR_INVALID_ARG", "TG_ERR_LAUNCH", "TG_ERR_DEVICE", "TG_
            "TG_XENT_NONE", "TG_XENT_SUM", "TG_XENT_MEAN", "TG_NS_MAX_STEPS", "tg_xent_f16", "tg_xent_bf16",
            "tg_xent_bwd_f16", "tg_xent_bwd_bf16", "tg_xent_workspace_bytes", "tg_xent_bwd_workspace_bytes",
            "tg_xent_plan", "tg_newton_schulz_f32", "tg_newton_schulz_f16", "tg_newton_schulz_bf16",
-           "tg_newton_schulz_workspace_bytes", "tg_newton_schulz_plan", "linear_cross_entropy", "newton_schulz"]
+           "tg_newton_schulz_workspace_bytes", "tg_newton_schulz_plan", "linear_cross_entropy", "newton_schulz",
+           "TG_GROUPED_Y", "TG_GROUPED_DX", "TG_GROUPED_DW", "tg_grouped_f16", "tg_grouped_bf16", "tg_grouped_dx_f16",
+           "tg_grouped_dx_bf16", "tg_grouped_dw_f16", "tg_grouped_dw_bf16", "tg_grouped_workspace_bytes",
+           "tg_grouped_plan", "tg_embedding_f32", "tg_embedding_f16", "tg_embedding_bf16", "tg_embedding_bwd_f32",
+           "tg_embedding_bwd_f16", "tg_embedding_bwd_bf16", "tg_embedding_bwd_workspace_bytes", "TG_ADAMW_BLOCK",
+           "TG_ADAMW_F32", "TG_ADAMW_F16", "TG_ADAMW_BF16", "tg_adamw", "tg_adamw_tensor", "tg_adamw_config",
+           "grouped_linear", "embedding", "adamw", "adamw_8bit", "adamw_8bit_state"]
 
 TG_MX_E4M3 = 0  # block-scaled element encodings (include/tg_gemm.h)
 TG_MX_E5M2 = 1
@@ -129,6 +145,7 @@ def load():
     lib.tg_device_info.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
                                    ctypes.c_char_p, i64]
     _declare_projection(lib)
+    _declare_training(lib)
     _lib = lib
     return lib
 

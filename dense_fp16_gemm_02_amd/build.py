@@ -4,10 +4,12 @@ Usage: python -m dense_fp16_gemm_02_amd.build  (or call ``build()``).
 """
 from __future__ import annotations
 
+from concurrent.futures import ThreadPoolExecutor
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +20,8 @@ ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "tg_gemm.hip"), os.path.join(CSRC, "tg_ceiling.hip"),
            os.path.join(CSRC, "tg_xent.hip"), os.path.join(CSRC, "tg_ortho.hip"),
-           os.path.join(CSRC, "tile_layout_abi.cpp")]
+           os.path.join(CSRC, "tg_grouped.hip"), os.path.join(CSRC, "tg_embed.hip"),
+           os.path.join(CSRC, "tg_adamw.hip"), os.path.join(CSRC, "tile_layout_abi.cpp")]
 
 FLAGS = [
     f"--offload-arch={ARCH}",
@@ -43,11 +46,21 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
+    """Compile every source, a few at a time, and link them."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}", *SOURCES, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def run(*args):
+        cmd = [hipcc(), *args]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as at, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(at, f"{i}.o") for i in range(len(SOURCES))]
+        flags = [f for f in FLAGS if f != "-shared"]
+        list(pool.map(lambda so: run(*flags, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}", "-c", so[0], "-o", so[1]),
+                      zip(SOURCES, objects)))
+        run(*FLAGS, *extra_flags, *objects, "-o", tmp)
     os.replace(tmp, LIB)
     return LIB
 

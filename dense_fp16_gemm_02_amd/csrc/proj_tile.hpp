@@ -1,5 +1,5 @@
 // proj_tile.hpp — the tile product behind the projection operators
-// (tg_xent.hip, tg_ortho.hip): a BM×BN block of op(A)·op(B) accumulated in
+// (tg_xent.hip, tg_ortho.hip, tg_grouped.hip): a BM×BN block of op(A)·op(B) accumulated in
 // fp32 registers, with each operand either K-major (a row of K consecutive
 // elements per output row, as tg_gemm takes them) or transposed (a row of
 // consecutive output rows per K, as the gradient products need them), so that
@@ -40,9 +40,9 @@
 // K tails: the K-major × K-major product takes the partial K-tile first (its
 // columns below 0 read as zero); a transposed operand takes it last (rows past
 // K are past the end of the buffer range and read as zero), and a K-major
-// operand beside it has to hold zeros up to a multiple of 64.  Rows (columns)
-// past an operand's extent are clamped to its last one: they feed only outputs
-// that are never stored.
+// operand beside it has to hold zeros up to a multiple of 64 or is masked (MASK).
+// Rows (columns) past an operand's extent are clamped to its last one: they feed
+// only outputs that are never stored.
 #ifndef TG_PROJ_TILE_HPP
 #define TG_PROJ_TILE_HPP
 
@@ -277,10 +277,14 @@ struct Operand {
 // STREAM: for a product bound by reading B (one tile row): B is loaded past the
 // caches, and the workgroups of the eight XCDs start at K-tiles spread over K and
 // wrap around, so that they read from different address ranges at any moment.
-template <typename E, int BM_, int BN_, int WM_, int WN_, int S_, bool TA_, bool TB_, bool STREAM_ = false>
+// MASK: for a K-major A beside a transposed B, whose rows do not hold zeros up to
+// a multiple of 64: A's chunks past K, a multiple of 8, read as zero.
+template <typename E, int BM_, int BN_, int WM_, int WN_, int S_, bool TA_, bool TB_, bool STREAM_ = false,
+          bool MASK_ = false>
 struct Tile {
-    static constexpr bool STREAM = STREAM_;
+    static constexpr bool STREAM = STREAM_, MASK = MASK_;
     static_assert(!STREAM_ || (!TA_ && !TB_), "rotation is for the K-major product");
+    static_assert(!MASK_ || (!TA_ && TB_), "the other products need no mask");
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
     static constexpr bool TA = TA_, TB = TB_;
     using V8 = typename El<E>::v8;
@@ -368,6 +372,7 @@ struct Tile {
             const int pt = STREAM ? (t + rot >= KT ? t + rot - KT : t + rot) : t;
             return FIRST && pt == 0 && k0 + kc < 0;
         };
+        auto past = [&](int t) { return MASK && kc >= K - t * BK; };
         auto dma_a = [&](__amdgpu_buffer_rsrc_t r, int stage, int p, bool zero) {
             dma16(r, a_ring + stage * STAGE_A + (p * NW + wave) * 512, zero ? DMA_OOB : a_off[p]);
         };
@@ -458,7 +463,7 @@ struct Tile {
             const bool zero = (STREAM || t == 0) && below(t);
 #pragma unroll
             for (int p = 0; p < PA; ++p)
-                dma_a(ra, t, p, zero);
+                dma_a(ra, t, p, zero || past(t));
 #pragma unroll
             for (int p = 0; p < PB; ++p)
                 dma_b(rb, t, p, zero);
@@ -480,7 +485,7 @@ struct Tile {
         int da = S % (S + 1);     // stage A(t+S) goes into
         for (int t = 0; t < (PEEL ? KT - 1 : KT); ++t) {
             step(fa[0], fb[0], true, sa, sb, 1, fa[1], fb[1], 1, rsrc_a(t + S), da,
-                 STREAM && below(t + S));
+                 (STREAM && below(t + S)) || past(t + S));
             wait_vmem<(S - 2) * (PA + PB) + PA>();  // K-tile t+1 has landed (this wave's part)
             barrier_lds();                          // ... for every wave; K-tile t's stages are drained
             const int sa1 = sa == S ? 0 : sa + 1, sb1 = sb == S - 1 ? 0 : sb + 1;
@@ -521,6 +526,29 @@ struct Tile {
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 };
+
+// Elements c .. c + 7 of a row of K 16-bit elements, zeros behind its end; vec:
+// the row is 16-byte aligned and K a multiple of 8.
+__device__ inline uint4 load8(const uint16_t *s, int64_t c, int64_t K, bool vec)
+{
+    if (vec)
+        return *reinterpret_cast<const uint4 *>(s + c);
+    union {
+        uint4 u;
+        uint16_t h[8];
+    } w;
+    if (c + 8 <= K) {
+        // one load of 16 bytes at the alignment of an element
+        __builtin_memcpy(&w, s + c, 16);
+        return w.u;
+    }
+    w.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e < K)
+            w.h[e] = s[c + e];
+    return w.u;
+}
 
 // ------------------------------------------------------- staged block stores
 // A wave's R×C block of 16-bit values in LDS, row-major with the 16-byte

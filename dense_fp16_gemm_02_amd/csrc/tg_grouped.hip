@@ -1,0 +1,503 @@
+// tg_grouped.hip — products of rows grouped by expert.  See include/tg_grouped.h
+// for the contract.
+//
+// One launch covers all experts: the output is cut into tiles expert by expert,
+// and a workgroup finds its tile from `ends` itself (a scan over the experts, 64
+// at a time), so that nothing of the routing passes through the host.  The grid is
+// an upper bound: experts' last tile rows are partly empty, so that E of them
+// may be added to M rows' tiles; workgroups past the last tile leave at once.
+//
+// The tile product is that of proj_tile.hpp; with few rows an expert it is bound by
+// streaming W, with many by the matrix cores.
+#include "proj_tile.hpp"
+
+#include <algorithm>
+#include <stdio.h>
+
+#include "tg_gemm.h"
+#include "tg_grouped.h"
+
+namespace {
+using namespace pt;
+
+// ------------------------------------------------------------------- groups
+// Where group idx's rows end: expert idx, or the rows behind all of them (idx >= E).
+__device__ inline int group_end(const int64_t *ends, int E, int M, int idx)
+{
+    if (idx >= E)
+        return M;
+    const int64_t x = ends[idx];
+    return (int)(x < 0 ? 0 : x > M ? M : x);
+}
+// 64 groups from `base` on, one to a lane: first row, end, and the tile rows up to
+// and with it.  `row` and `tiles`: the end and the count of the groups before.
+template <int BM>
+__device__ inline void scan_groups(const int64_t *ends, int E, int M, int base, int lane, int row, int tiles,
+                                   int &lo, int &hi, int &upto)
+{
+    hi = imax(group_end(ends, E, M, base + lane), row);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(hi, o);
+        hi = lane >= o ? imax(hi, x) : hi;
+    }
+    lo = __shfl_up(hi, 1);
+    lo = lane == 0 ? row : lo;
+    upto = (hi - lo + BM - 1) / BM;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(upto, o);
+        upto += lane >= o ? x : 0;
+    }
+    upto += tiles;
+}
+struct Tile2d {
+    int e, lo, rows;  // group (E: the rows behind), its first row and their number
+    int tm, tn;
+};
+template <int BM>
+__device__ inline bool find_tile(const int64_t *ends, int E, int M, int tiles_n, Tile2d &t)
+{
+    const int lane = lane_id();
+    int lo, hi, upto, row = 0, tiles = 0;
+    for (int base = 0; base <= E; base += 64) {
+        scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
+        row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
+    }
+    if ((int64_t)blockIdx.x >= (int64_t)tiles * tiles_n)
+        return false;
+    const int logical = xcd_contiguous(blockIdx.x, tiles * tiles_n), tile_row = logical / tiles_n;
+    int base = 0;
+    if (E >= 64) {  // otherwise the registers still hold the only scan
+        row = tiles = 0;
+        for (;; base += 64) {
+            scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
+            if (__builtin_amdgcn_readlane(upto, 63) > tile_row)
+                break;
+            row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
+    const int at = uniform(__builtin_ctzll(__ballot(upto > tile_row)));
+    t.e = base + at;
+    t.lo = __builtin_amdgcn_readlane(lo, at);
+    t.rows = __builtin_amdgcn_readlane(hi, at) - t.lo;
+    const int rows_tiles = (t.rows + BM - 1) / BM;
+    const int first = __builtin_amdgcn_readlane(upto, at) - rows_tiles;
+    grouped_tile<4>(logical - first * tiles_n, rows_tiles, tiles_n, t.tm, t.tn);
+    return true;
+}
+// Expert e's rows.
+__device__ inline void find_rows(const int64_t *ends, int M, int e, int &lo, int &rows)
+{
+    const int lane = lane_id();
+    int before = 0;
+    for (int i = lane; i < e; i += 64)
+        before = imax(before, group_end(ends, e, M, i));
+#pragma unroll
+    for (int o = 32; o; o >>= 1)
+        before = imax(before, __shfl_xor(before, o));
+    lo = uniform(before);
+    rows = uniform(imax(group_end(ends, e + 1, M, e) - before, 0));
+}
+
+// ------------------------------------------------------------------ products
+template <typename E, typename T>
+__device__ inline void store_tile(E *smem, const f32x4 (&acc)[T::TM][T::TN], E *D, int64_t ld, int m0, int n0, int rows,
+                                  int cols, bool vec)
+{
+    using V4 = typename El<E>::v4;
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int fr = lane & 15, fc = 4 * (lane >> 4);
+    barrier_lds();
+    E *stg = smem + wave * T::WTM * T::WTN;
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) {
+            V4 d;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                d[v] = (E)acc[i][j][v];
+            *reinterpret_cast<V4 *>(stg + stage_off<T::WTN>(16 * i + fr, 16 * j + fc)) = d;
+        }
+    store_block<E, T::WTM, T::WTN>(stg, D, ld, m0 + wm * T::WTM, n0 + wn * T::WTN, rows, cols, vec, nullptr, lane);
+}
+// Zeros where a tile's product is over nothing.
+template <typename E, int BM, int BN, int THREADS>
+__device__ inline void zero_tile(E *D, int64_t ld, int m0, int n0, int rows, int cols)
+{
+    const int r1 = imin(rows, m0 + BM), c1 = imin(cols, n0 + BN);
+    for (int r = m0 + (int)threadIdx.x / 64; r < r1; r += THREADS / 64)
+        for (int c = n0 + lane_id(); c < c1; c += 64)
+            D[r * ld + c] = (E)0.0f;
+}
+
+// Y (K-major W) and dX (transposed W): tiles of rows of one expert.
+struct RowsArgs {
+    const void *a, *w;
+    const int64_t *ends;
+    void *d;
+    int64_t lda, ldw, w_stride, ldd;
+    int M, E;
+    int inner;     // K (Y) or N (dX): what is summed over
+    int w_extent;  // rows (Y) or columns (dX) of a weight
+    int cols;      // of d
+    bool vec;      // d's rows are 16-byte aligned
+    int tiles_n;
+};
+template <typename E, typename T>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_rows_kernel(
+    RowsArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
+    Tile2d t;
+    if (!find_tile<T::BM>(a.ends, a.E, a.M, a.tiles_n, t))
+        return;
+    const int m0 = t.tm * T::BM, n0 = t.tn * T::BN;
+    E *d = reinterpret_cast<E *>(a.d) + (int64_t)t.lo * a.ldd;
+    if (t.e >= a.E) {
+        zero_tile<E, T::BM, T::BN, T::THREADS>(d, a.ldd, m0, n0, t.rows, a.cols);
+        return;
+    }
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    const Operand x = {reinterpret_cast<const E *>(a.a) + (int64_t)t.lo * a.lda, a.lda, t.rows};
+    const Operand w = {reinterpret_cast<const E *>(a.w) + (int64_t)t.e * a.w_stride, a.ldw, a.w_extent};
+    T::run(smem, x, w, m0, n0, a.inner, acc);
+    store_tile<E, T>(smem, acc, d, a.ldd, m0, n0, t.rows, a.cols, a.vec);
+}
+
+// dW: tiles of one expert's weight, summed over its rows.
+struct WeightArgs {
+    const void *dy, *x;
+    const int64_t *ends;
+    void *dw;
+    int64_t lddy, ldx, lddw, dw_stride;
+    int M, E, N, K;
+    bool vec;
+    int tiles_m, tiles_n;
+};
+template <typename E, typename T>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_weight_kernel(
+    WeightArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
+    const int per = a.tiles_m * a.tiles_n;
+    const int logical = xcd_contiguous(blockIdx.x, a.E * per), e = logical / per;
+    int tm, tn, lo, rows;
+    grouped_tile<4>(logical - e * per, a.tiles_m, a.tiles_n, tm, tn);
+    find_rows(a.ends, a.M, e, lo, rows);
+    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    E *d = reinterpret_cast<E *>(a.dw) + (int64_t)e * a.dw_stride;
+    if (rows == 0) {
+        zero_tile<E, T::BM, T::BN, T::THREADS>(d, a.lddw, m0, n0, a.N, a.K);
+        return;
+    }
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    const Operand dy = {reinterpret_cast<const E *>(a.dy) + (int64_t)lo * a.lddy, a.lddy, a.N};
+    const Operand x = {reinterpret_cast<const E *>(a.x) + (int64_t)lo * a.ldx, a.ldx, a.K};
+    T::run(smem, dy, x, m0, n0, rows, acc);
+    store_tile<E, T>(smem, acc, d, a.lddw, m0, n0, a.N, a.K, a.vec);
+}
+
+// ------------------------------------------------------------------- packing
+// Rows of `cols` elements to 16-byte aligned rows of cols8, zeros behind (rows
+// that the tile product cannot load as they lie).  `ends`: the rows are those of
+// `per`-row weights, and weights of experts without rows are left out.
+struct PackArgs {
+    const uint16_t *src;
+    uint16_t *dst;
+    int64_t ld, stride, rows, per, cols, cols8;
+    const int64_t *ends;
+    int M;
+};
+__global__ __launch_bounds__(256) void grouped_pack_kernel(PackArgs a)
+{
+    const int64_t chunks = a.cols8 / 8;
+    // a workgroup takes whole runs of rows of one weight
+    const int64_t runs = cdiv(a.per, 64);
+    for (int64_t b = blockIdx.x; b < (a.rows / a.per) * runs; b += gridDim.x) {
+        const int64_t e = b / runs, r0 = (b - e * runs) * 64, r1 = r0 + 64 < a.per ? r0 + 64 : a.per;
+        if (a.ends) {
+            int lo, n;
+            find_rows(a.ends, a.M, (int)e, lo, n);
+            if (n == 0)
+                continue;
+        }
+        for (int64_t i = threadIdx.x; i < (r1 - r0) * chunks; i += 256) {
+            const int64_t r = r0 + i / chunks, c = i % chunks * 8;
+            *reinterpret_cast<uint4 *>(a.dst + (e * a.per + r) * a.cols8 + c) =
+                load8(a.src + e * a.stride + r * a.ld, c, a.cols, false);
+        }
+    }
+}
+__global__ __launch_bounds__(256) void grouped_zero_kernel(uint16_t *d, int64_t ld, int64_t stride, int64_t batch,
+                                                           int64_t rows, int64_t cols)
+{
+    for (int64_t b = blockIdx.x; b < batch * rows; b += gridDim.x) {
+        uint16_t *row = d + b / rows * stride + b % rows * ld;
+        for (int64_t c = threadIdx.x; c < cols; c += 256)
+            row[c] = 0;
+    }
+}
+
+// ------------------------------------------------------------------- plans
+enum Class { C256, C192, C128, C64, C64X128, C16X64, CLASSES };
+const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x128", "16x64"};
+constexpr TileClass CLASS[] = {{256, 256, 1, 1.50, 1.50, 16.0},
+                               {192, 192, 1, 1.15, 1.15, 9.0},
+                               {128, 128, 2, 1.10, 0.50, 6.0},
+                               {64, 64, 2, 0.50, 0.27, 4.0},
+                               {64, 128, 2, 0.80, 0.45, 5.0},
+                               {16, 64, 4, 0.50, 0.27, 4.0}};
+template <typename E, bool TA, bool TB, typename F>
+bool with_tile(Class c, F f)
+{
+    constexpr bool MASK = !TA && TB, STREAM = !TA && !TB;
+    switch (c) {
+    case C256:
+        return f(Tile<E, 256, 256, 2, 2, 2, TA, TB, false, MASK>{});
+    case C192:
+        if constexpr (TA == TB)
+            return f(Tile<E, 192, 192, 2, 2, 2, TA, TB>{});
+        [[fallthrough]];
+    case C128:
+        return f(Tile<E, 128, 128, 2, 2, 2, TA, TB, false, MASK>{});
+    case C64X128:
+        if constexpr (!TA)
+            return f(Tile<E, 64, 128, 1, 4, 3, TA, TB, STREAM, MASK>{});
+        [[fallthrough]];
+    case C16X64:
+        if constexpr (!TA)
+            return f(Tile<E, 16, 64, 1, 2, 3, TA, TB, STREAM, MASK>{});
+        [[fallthrough]];
+    default:
+        return f(Tile<E, 64, 64, 2, 2, 3, TA, TB, false, MASK>{});
+    }
+}
+
+struct Call {
+    int product;
+    const void *A, *B;
+    int64_t M, E, N, K, lda, ldb, w_stride;
+};
+struct Plan {
+    Class c;
+    int64_t grid;
+    bool pack_a, pack_b;
+    int64_t a_cols, b_cols;  // of the operands' rows
+    int64_t a_bytes, b_bytes;
+};
+bool rows_ok(const void *p, int64_t ld, int64_t cols)
+{
+    return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= MAX_DMA_LD;
+}
+// The experts that get a row, if M rows go to E experts evenly, and the tile rows
+// of their shares.
+double tile_rows(int64_t M, int64_t E, int bm)
+{
+    const double hit = (double)std::min(M, E), each = (double)M / hit;
+    return hit * std::max(1.0, each / bm + 0.45);
+}
+Plan make_plan(const Call &q)
+{
+    Plan p = {};
+    const bool dw = q.product == TG_GROUPED_DW, dx = q.product == TG_GROUPED_DX;
+    p.a_cols = q.product == TG_GROUPED_Y ? q.K : q.N;
+    p.b_cols = q.K;
+    p.pack_a = !rows_ok(q.A, q.M > 1 ? q.lda : round_up(q.lda, 8), p.a_cols);
+    p.pack_b = !rows_ok(q.B, (dw ? q.M : q.N) > 1 ? q.ldb : round_up(q.ldb, 8), p.b_cols) ||
+               (!dw && q.E > 1 && q.w_stride % 8 != 0);
+    p.a_bytes = p.pack_a ? round_up(2 * q.M * round_up(p.a_cols, 8), 256) : 0;
+    p.b_bytes = p.pack_b ? round_up(2 * (dw ? q.M : q.E * q.N) * round_up(p.b_cols, 8), 256) : 0;
+    const int64_t out = dx ? q.K : q.N, inner = dx ? q.N : q.K;
+    if (dw) {
+        int c = 0;
+        const auto time = [&](int i) {
+            return tile_time(CLASS[i], q.E * cdiv(q.N, CLASS[i].bm) * cdiv(q.K, CLASS[i].bn), cdiv(cdiv(q.M, q.E), BK));
+        };
+        for (int i = 1; i < C64X128; ++i)
+            if (time(i) < time(c))
+                c = i;
+        p.c = (Class)c;
+        p.grid = q.E * cdiv(q.N, CLASS[c].bm) * cdiv(q.K, CLASS[c].bn);
+        return p;
+    }
+    const double each = (double)q.M / (double)std::min(q.M, q.E);
+    if (each <= 16.0) {
+        p.c = C16X64;
+    } else if (each <= 48.0) {
+        p.c = C64X128;
+    } else {
+        int c = 0;
+        const auto time = [&](int i) {
+            return tile_time(CLASS[i], (int64_t)(tile_rows(q.M, q.E, CLASS[i].bm) * (double)cdiv(out, CLASS[i].bn)), cdiv(inner, BK));
+        };
+        for (int i = 1; i < C64X128; ++i)
+            if (!(dx && i == C192) && time(i) < time(c))
+                c = i;
+        p.c = (Class)c;
+    }
+    const int64_t bm = CLASS[p.c].bm;
+    // each group adds at most bm - 1 rows to whole tiles
+    p.grid = (q.M + std::min(q.E + 1, q.M) * (bm - 1)) / bm * cdiv(out, CLASS[p.c].bn);
+    return p;
+}
+
+constexpr int64_t LIM = (int64_t)1 << 31, LIM_STRIDE = (int64_t)1 << 42;
+// Whether anything is multiplied: otherwise the result is zeros, or nothing.
+bool multiplies(const Call &q) { return q.M > 0 && q.E > 0 && q.N > 0 && q.K > 0; }
+int validate(const Call &q)
+{
+    if (q.product < TG_GROUPED_Y || q.product > TG_GROUPED_DW || q.M < 0 || q.E < 0 || q.N < 0 || q.K < 0)
+        return TG_ERR_INVALID_ARG;
+    const bool dw = q.product == TG_GROUPED_DW;
+    if (q.lda < (q.product == TG_GROUPED_Y ? q.K : q.N) || q.ldb < q.K || (!dw && q.E > 1 && q.w_stride < 0))
+        return TG_ERR_INVALID_ARG;
+    if (q.M >= LIM || q.E >= 1 << 16 || q.N >= MAX_DMA_LD || q.K >= MAX_DMA_LD || q.lda >= LIM || q.ldb >= LIM ||
+        (!dw && q.E > 1 && q.w_stride >= LIM_STRIDE))
+        return TG_ERR_TOO_LARGE;
+    if (!multiplies(q))
+        return TG_OK;
+    if (!q.A || !q.B || (uintptr_t)q.A % 2 || (uintptr_t)q.B % 2)
+        return TG_ERR_INVALID_ARG;
+    return make_plan(q).grid >= MAX_GRID ? TG_ERR_TOO_LARGE : TG_OK;
+}
+int64_t copy_grid(int64_t n) { return std::max((int64_t)1, std::min(n, (int64_t)16 * NUM_CU)); }
+
+bool pack(const void *src, void *dst, int64_t ld, int64_t stride, int64_t batch, int64_t per, int64_t cols,
+          const int64_t *ends, int64_t M, void *stream)
+{
+    const PackArgs a = {reinterpret_cast<const uint16_t *>(src), reinterpret_cast<uint16_t *>(dst), ld, stride, batch * per,
+                        per, cols, round_up(cols, 8), ends, (int)M};
+    return launch(grouped_pack_kernel, copy_grid(batch * cdiv(per, 64)), 256, stream, a);
+}
+
+// `ldd`, `d_stride`: of the result
+template <typename E>
+int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_stride, void *ws, int64_t ws_bytes,
+            void *stream)
+{
+    const int st = validate(q);
+    const bool dw = q.product == TG_GROUPED_DW, y = q.product == TG_GROUPED_Y;
+    const int64_t batch = dw ? q.E : 1, rows = dw ? q.N : q.M, cols = y ? q.N : q.K;
+    if (st == TG_ERR_INVALID_ARG || ldd < cols || (dw && q.E > 1 && q.N > 0 && d_stride < (q.N - 1) * ldd + q.K))
+        return TG_ERR_INVALID_ARG;
+    if (st != TG_OK || ldd >= LIM || (dw && q.E > 1 && d_stride >= LIM_STRIDE))
+        return TG_ERR_TOO_LARGE;
+    if (batch == 0 || rows == 0 || cols == 0)
+        return TG_OK;
+    if (!D || (uintptr_t)D % 2)
+        return TG_ERR_INVALID_ARG;
+    if (!multiplies(q)) {
+        if (gfx950_status() != 1)
+            return TG_ERR_DEVICE;
+        return launch(grouped_zero_kernel, copy_grid(batch * rows), 256, stream, (uint16_t *)D, ldd, d_stride, batch, rows,
+                      cols)
+                   ? TG_OK
+                   : TG_ERR_LAUNCH;
+    }
+    const Plan p = make_plan(q);
+    const int64_t need = p.a_bytes + p.b_bytes;
+    if (!ends || (uintptr_t)ends % 8 || (need > 0 && (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < need)))
+        return TG_ERR_INVALID_ARG;
+    if (gfx950_status() != 1)
+        return TG_ERR_DEVICE;
+    const void *A = q.A, *B = q.B;
+    int64_t lda = q.M > 1 ? q.lda : round_up(q.lda, 8), ldb = (dw ? q.M : q.N) > 1 ? q.ldb : round_up(q.ldb, 8);
+    int64_t w_stride = q.E > 1 ? q.w_stride : 0;
+    bool ok = true;
+    if (p.pack_a) {
+        ok = pack(A, ws, q.lda, 0, 1, q.M, p.a_cols, nullptr, q.M, stream);
+        A = ws, lda = round_up(p.a_cols, 8);
+    }
+    if (p.pack_b) {
+        void *to = reinterpret_cast<char *>(ws) + p.a_bytes;
+        ok = ok && pack(B, to, q.ldb, w_stride, dw ? 1 : q.E, dw ? q.M : q.N, p.b_cols, dw ? nullptr : ends, q.M, stream);
+        B = to, ldb = round_up(p.b_cols, 8), w_stride = q.N * ldb;
+    }
+    const bool vec = ldd % 8 == 0 && (uintptr_t)D % 16 == 0 && (!dw || q.E == 1 || d_stride % 8 == 0);
+    if (dw) {
+        const WeightArgs a = {A, B, ends, D, lda, ldb, ldd, q.E > 1 ? d_stride : 0, (int)q.M, (int)q.E, (int)q.N, (int)q.K, vec,
+                              (int)cdiv(q.N, CLASS[p.c].bm), (int)cdiv(q.K, CLASS[p.c].bn)};
+        ok = ok && with_tile<E, true, true>(p.c, [&](auto t) {
+            return launch(grouped_weight_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
+        });
+    } else {
+        // behind a packed A the sum may run over its zeros: not over W's rows behind N
+        const RowsArgs a = {A, B, ends, D, lda, ldb, w_stride, ldd, (int)q.M, (int)q.E,
+                            (int)(y ? (p.pack_a || p.pack_b ? round_up(q.K, 8) : q.K) : q.N), (int)(y ? q.N : q.K), (int)cols, vec,
+                            (int)cdiv(cols, CLASS[p.c].bn)};
+        ok = ok && (y ? with_tile<E, false, false>(p.c, [&](auto t) {
+            return launch(grouped_rows_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
+        }) : with_tile<E, false, true>(p.c, [&](auto t) {
+            return launch(grouped_rows_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
+        }));
+    }
+    return ok ? TG_OK : TG_ERR_LAUNCH;
+}
+}  // namespace
+
+extern "C" int64_t tg_grouped_workspace_bytes(int product, const void *A, const void *B, int64_t M, int64_t E,
+                                              int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t w_stride)
+{
+    const Call q = {product, A, B, M, E, N, K, lda, ldb, w_stride};
+    if (validate(q) != TG_OK)
+        return -1;
+    if (!multiplies(q))
+        return 0;
+    const Plan p = make_plan(q);
+    return p.a_bytes + p.b_bytes;
+}
+
+#define TG_GROUPED_ENTRIES(suffix, E)                                                                                 \
+    extern "C" int tg_grouped_##suffix(const void *X, const void *W, const int64_t *ends, void *Y, int64_t M,         \
+                                       int64_t experts, int64_t N, int64_t K, int64_t ldx, int64_t ldw,               \
+                                       int64_t w_stride, int64_t ldy, void *workspace, int64_t workspace_bytes,       \
+                                       void *stream)                                                                  \
+    {                                                                                                                 \
+        return product<E>({TG_GROUPED_Y, X, W, M, experts, N, K, ldx, ldw, w_stride}, ends, Y, ldy, 0, workspace,     \
+                          workspace_bytes, stream);                                                                   \
+    }                                                                                                                 \
+    extern "C" int tg_grouped_dx_##suffix(const void *dY, const void *W, const int64_t *ends, void *dX, int64_t M,    \
+                                          int64_t experts, int64_t N, int64_t K, int64_t lddy, int64_t ldw,           \
+                                          int64_t w_stride, int64_t lddx, void *workspace, int64_t workspace_bytes,   \
+                                          void *stream)                                                               \
+    {                                                                                                                 \
+        return product<E>({TG_GROUPED_DX, dY, W, M, experts, N, K, lddy, ldw, w_stride}, ends, dX, lddx, 0,           \
+                          workspace, workspace_bytes, stream);                                                        \
+    }                                                                                                                 \
+    extern "C" int tg_grouped_dw_##suffix(const void *dY, const void *X, const int64_t *ends, void *dW, int64_t M,    \
+                                          int64_t experts, int64_t N, int64_t K, int64_t lddy, int64_t ldx,           \
+                                          int64_t lddw, int64_t dw_stride, void *workspace, int64_t workspace_bytes,  \
+                                          void *stream)                                                               \
+    {                                                                                                                 \
+        return product<E>({TG_GROUPED_DW, dY, X, M, experts, N, K, lddy, ldx, 0}, ends, dW, lddw, dw_stride,          \
+                          workspace, workspace_bytes, stream);                                                        \
+    }
+TG_GROUPED_ENTRIES(f16, _Float16)
+TG_GROUPED_ENTRIES(bf16, __bf16)
+
+extern "C" int tg_grouped_plan(int product, const void *A, const void *B, int64_t M, int64_t E, int64_t N, int64_t K,
+                               int64_t lda, int64_t ldb, int64_t w_stride, char *name, int64_t name_len)
+{
+    if (name && name_len > 0)
+        name[0] = 0;
+    const Call q = {product, A, B, M, E, N, K, lda, ldb, w_stride};
+    const int st = validate(q);
+    if (st != TG_OK || !name || name_len <= 0)
+        return st;
+    if (!multiplies(q)) {
+        const bool none = product == TG_GROUPED_DW ? E == 0 || N == 0 || K == 0 : M == 0 || (product == TG_GROUPED_Y ? N : K) == 0;
+        snprintf(name, (size_t)name_len, "%s", none ? "" : "zero");
+        return st;
+    }
+    const Plan p = make_plan(q);
+    static const char *const WHAT[] = {"y", "dx", "dw"};
+    snprintf(name, (size_t)name_len, "%s%s%s_%s", p.pack_a ? "pack_a " : "", p.pack_b ? "pack_b " : "", WHAT[product],
+             CLASS_NAME[p.c]);
+    return st;
+}

@@ -78,26 +78,6 @@ struct PrepArgs {
     uint16_t *dH;
     int64_t lddh;
 };
-__device__ inline uint4 load8(const uint16_t *s, int64_t c, int64_t K, bool vec)
-{
-    if (vec)
-        return *reinterpret_cast<const uint4 *>(s + c);
-    union {
-        uint4 u;
-        uint16_t h[8];
-    } w;
-    if (c + 8 <= K) {
-        // one load of 16 bytes at the alignment of an element
-        __builtin_memcpy(&w, s + c, 16);
-        return w.u;
-    }
-    w.u = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (c + e < K)
-            w.h[e] = s[c + e];
-    return w.u;
-}
 template <typename X>
 __device__ inline X wave_sum(X x)
 {

@@ -1,0 +1,626 @@
+"""The operators of a training step around the projections (include/tg_grouped.h,
+include/tg_embed.h, include/tg_adamw.h).
+
+    tg_grouped_f16 / _bf16(...), tg_grouped_dx_*(...), tg_grouped_dw_*(...)  -> status
+    tg_grouped_workspace_bytes(...), tg_grouped_plan(...)
+    tg_embedding_f32 / _f16 / _bf16(...), tg_embedding_bwd_*(...)            -> status
+    tg_embedding_bwd_workspace_bytes(...)
+    tg_adamw(tensors, config, stream)                                       -> status
+    grouped_linear(X, W, ends)               torch, differentiable
+    embedding(tokens, W, ...)                torch, differentiable
+    adamw(params, grads, ...), adamw_8bit(params, grads, ...), adamw_8bit_state(p)   torch
+
+Argument marshalling, checks and autograd glue only, as in the package.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+
+from .projection import _lib, _p, _pkg, _refuse_modes, _row_stride, _s
+
+TG_GROUPED_Y = 0  # include/tg_grouped.h
+TG_GROUPED_DX = 1
+TG_GROUPED_DW = 2
+TG_ADAMW_BLOCK = 256  # include/tg_adamw.h
+TG_ADAMW_F32 = 0
+TG_ADAMW_F16 = 1
+TG_ADAMW_BF16 = 2
+
+
+class tg_adamw_tensor(ctypes.Structure):
+    """One tensor of tg_adamw: addresses and the number of elements."""
+
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64)]
+
+
+class tg_adamw_config(ctypes.Structure):
+    """What all tensors of a tg_adamw call share."""
+
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("lr_at", ctypes.c_void_p), ("step_at", ctypes.c_void_p), ("g_scale", ctypes.c_void_p),
+                ("p_type", ctypes.c_int), ("g_type", ctypes.c_int), ("copy_type", ctypes.c_int),
+                ("bits", ctypes.c_int)]
+
+
+def declare(lib) -> None:
+    """Argument types of the entry points (called once by the package's load())."""
+    i64, vp, ci, cf = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    lib.tg_grouped_workspace_bytes.restype = i64
+    lib.tg_grouped_workspace_bytes.argtypes = [ci, vp, vp] + [i64] * 7
+    lib.tg_grouped_plan.restype = ci
+    lib.tg_grouped_plan.argtypes = [ci, vp, vp] + [i64] * 7 + [ctypes.c_char_p, i64]
+    for what in ("", "dx_", "dw_"):
+        for dtype in ("f16", "bf16"):
+            fn = getattr(lib, f"tg_grouped_{what}{dtype}")
+            fn.restype, fn.argtypes = ci, [vp] * 4 + [i64] * 8 + [vp, i64, vp]
+    for dtype in ("f32", "f16", "bf16"):
+        fn = getattr(lib, f"tg_embedding_{dtype}")
+        fn.restype, fn.argtypes = ci, [vp] * 3 + [i64] * 5 + [cf, vp]
+        fn = getattr(lib, f"tg_embedding_bwd_{dtype}")
+        fn.restype, fn.argtypes = ci, [vp] * 3 + [i64] * 5 + [cf, i64, vp, i64, vp]
+    lib.tg_embedding_bwd_workspace_bytes.restype = i64
+    lib.tg_embedding_bwd_workspace_bytes.argtypes = [i64] * 3
+    lib.tg_adamw.restype = ci
+    lib.tg_adamw.argtypes = [vp, i64, ctypes.POINTER(tg_adamw_config), vp]
+
+
+# ------------------------------------------------------------------ grouped
+def tg_grouped_workspace_bytes(product: int, A, B, M: int, E: int, N: int, K: int, lda: int, ldb: int,
+                               w_stride: int) -> int:
+    """Workspace bytes of a grouped product (TG_GROUPED_*) for these arguments (-1: refused)."""
+    return _lib().tg_grouped_workspace_bytes(product, _p(A), _p(B), M, E, N, K, lda, ldb, w_stride)
+
+
+def tg_grouped_plan(product: int, A, B, M: int, E: int, N: int, K: int, lda: int, ldb: int, w_stride: int):
+    """Host-only: (status, kernel names)."""
+    buf = ctypes.create_string_buffer(128)
+    st = _lib().tg_grouped_plan(product, _p(A), _p(B), M, E, N, K, lda, ldb, w_stride, buf, 128)
+    return st, buf.value.decode()
+
+
+def _grouped(name, A, B, ends, D, M, E, N, K, lda, ldb, stride, ldd, workspace, workspace_bytes, stream):
+    return getattr(_lib(), name)(_p(A), _p(B), _p(ends), _p(D), M, E, N, K, lda, ldb, stride, ldd, _p(workspace),
+                                 workspace_bytes, _s(stream))
+
+
+def tg_grouped_f16(X, W, ends, Y, M: int, E: int, N: int, K: int, ldx: int, ldw: int, w_stride: int, ldy: int,
+                   workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue Y[i] = X[i]·W[e]ᵀ (binary16); returns the C status code."""
+    return _grouped("tg_grouped_f16", X, W, ends, Y, M, E, N, K, ldx, ldw, w_stride, ldy, workspace, workspace_bytes,
+                    stream)
+
+
+def tg_grouped_bf16(X, W, ends, Y, M: int, E: int, N: int, K: int, ldx: int, ldw: int, w_stride: int, ldy: int,
+                    workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_grouped_f16 for bfloat16 operands."""
+    return _grouped("tg_grouped_bf16", X, W, ends, Y, M, E, N, K, ldx, ldw, w_stride, ldy, workspace,
+                    workspace_bytes, stream)
+
+
+def tg_grouped_dx_f16(dY, W, ends, dX, M: int, E: int, N: int, K: int, lddy: int, ldw: int, w_stride: int, lddx: int,
+                      workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue dX[i] = dY[i]·W[e] (binary16); returns the C status code."""
+    return _grouped("tg_grouped_dx_f16", dY, W, ends, dX, M, E, N, K, lddy, ldw, w_stride, lddx, workspace,
+                    workspace_bytes, stream)
+
+
+def tg_grouped_dx_bf16(dY, W, ends, dX, M: int, E: int, N: int, K: int, lddy: int, ldw: int, w_stride: int,
+                       lddx: int, workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_grouped_dx_f16 for bfloat16 operands."""
+    return _grouped("tg_grouped_dx_bf16", dY, W, ends, dX, M, E, N, K, lddy, ldw, w_stride, lddx, workspace,
+                    workspace_bytes, stream)
+
+
+def _grouped_dw(name, dY, X, ends, dW, M, E, N, K, lddy, ldx, lddw, dw_stride, workspace, workspace_bytes, stream):
+    return getattr(_lib(), name)(_p(dY), _p(X), _p(ends), _p(dW), M, E, N, K, lddy, ldx, lddw, dw_stride,
+                                 _p(workspace), workspace_bytes, _s(stream))
+
+
+def tg_grouped_dw_f16(dY, X, ends, dW, M: int, E: int, N: int, K: int, lddy: int, ldx: int, lddw: int,
+                      dw_stride: int, workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue dW[e] = Σ dY[i]ᵀ·X[i] (binary16); returns the C status code."""
+    return _grouped_dw("tg_grouped_dw_f16", dY, X, ends, dW, M, E, N, K, lddy, ldx, lddw, dw_stride, workspace,
+                       workspace_bytes, stream)
+
+
+def tg_grouped_dw_bf16(dY, X, ends, dW, M: int, E: int, N: int, K: int, lddy: int, ldx: int, lddw: int,
+                       dw_stride: int, workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_grouped_dw_f16 for bfloat16 operands."""
+    return _grouped_dw("tg_grouped_dw_bf16", dY, X, ends, dW, M, E, N, K, lddy, ldx, lddw, dw_stride, workspace,
+                       workspace_bytes, stream)
+
+
+# ---------------------------------------------------------------- embedding
+def _embedding(name, tokens, W, Y, M, V, K, ldw, ldy, scale, stream):
+    return getattr(_lib(), name)(_p(tokens), _p(W), _p(Y), M, V, K, ldw, ldy, scale, _s(stream))
+
+
+def tg_embedding_f32(tokens, W, Y, M: int, V: int, K: int, ldw: int, ldy: int, scale: float, stream=None) -> int:
+    """Enqueue Y[i] = scale·W[tokens[i]] (fp32); returns the C status code."""
+    return _embedding("tg_embedding_f32", tokens, W, Y, M, V, K, ldw, ldy, scale, stream)
+
+
+def tg_embedding_f16(tokens, W, Y, M: int, V: int, K: int, ldw: int, ldy: int, scale: float, stream=None) -> int:
+    """tg_embedding_f32 for binary16 rows."""
+    return _embedding("tg_embedding_f16", tokens, W, Y, M, V, K, ldw, ldy, scale, stream)
+
+
+def tg_embedding_bf16(tokens, W, Y, M: int, V: int, K: int, ldw: int, ldy: int, scale: float, stream=None) -> int:
+    """tg_embedding_f32 for bfloat16 rows."""
+    return _embedding("tg_embedding_bf16", tokens, W, Y, M, V, K, ldw, ldy, scale, stream)
+
+
+def tg_embedding_bwd_workspace_bytes(M: int, V: int, K: int) -> int:
+    """Workspace bytes of tg_embedding_bwd_* for these sizes (-1: refused)."""
+    return _lib().tg_embedding_bwd_workspace_bytes(M, V, K)
+
+
+def _embedding_bwd(name, tokens, dY, dW, M, V, K, lddy, lddw, scale, padding, workspace, workspace_bytes, stream):
+    return getattr(_lib(), name)(_p(tokens), _p(dY), _p(dW), M, V, K, lddy, lddw, scale, padding, _p(workspace),
+                                 workspace_bytes, _s(stream))
+
+
+def tg_embedding_bwd_f32(tokens, dY, dW, M: int, V: int, K: int, lddy: int, lddw: int, scale: float, padding: int,
+                         workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue dW[v] = scale·Σ dY[i] over the rows of token v (fp32); returns the C status code."""
+    return _embedding_bwd("tg_embedding_bwd_f32", tokens, dY, dW, M, V, K, lddy, lddw, scale, padding, workspace,
+                          workspace_bytes, stream)
+
+
+def tg_embedding_bwd_f16(tokens, dY, dW, M: int, V: int, K: int, lddy: int, lddw: int, scale: float, padding: int,
+                         workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_embedding_bwd_f32 for binary16 rows."""
+    return _embedding_bwd("tg_embedding_bwd_f16", tokens, dY, dW, M, V, K, lddy, lddw, scale, padding, workspace,
+                          workspace_bytes, stream)
+
+
+def tg_embedding_bwd_bf16(tokens, dY, dW, M: int, V: int, K: int, lddy: int, lddw: int, scale: float, padding: int,
+                          workspace, workspace_bytes: int, stream=None) -> int:
+    """tg_embedding_bwd_f32 for bfloat16 rows."""
+    return _embedding_bwd("tg_embedding_bwd_bf16", tokens, dY, dW, M, V, K, lddy, lddw, scale, padding, workspace,
+                          workspace_bytes, stream)
+
+
+# ------------------------------------------------------------------- adamw
+def tg_adamw(tensors, config: tg_adamw_config, stream=None) -> int:
+    """Enqueue one step over a sequence (or ctypes array) of tg_adamw_tensor; returns the C status code."""
+    if not isinstance(tensors, ctypes.Array):
+        tensors = (tg_adamw_tensor * len(tensors))(*tensors)
+    return _lib().tg_adamw(ctypes.addressof(tensors) if len(tensors) else None, len(tensors), ctypes.byref(config),
+                           _s(stream))
+
+
+# ------------------------------------------------------------------ torch
+def _on_device(dev, fn, args, what):
+    """fn(*args) with dev as the current device."""
+    import torch
+
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st:
+        raise _pkg().TgError(st, what)
+
+
+@functools.lru_cache(maxsize=1024)
+def _grouped_size(product, a_aligned, b_aligned, M, E, N, K, lda, ldb, w_stride):
+    """Workspace bytes; of the pointers only their alignment counts."""
+    return max(0, _lib().tg_grouped_workspace_bytes(product, 4096 if a_aligned else 4098, 4096 if b_aligned else 4098,
+                                                    M, E, N, K, lda, ldb, w_stride))
+
+
+def _grouped_call(product, A, B, ends, D, N, K, ldd, d_stride=0):
+    """Workspace, stream and device around one product of the library."""
+    import torch
+
+    M, E = A.shape[0], ends.shape[0]
+    dw = product == TG_GROUPED_DW
+    lda = _row_stride(A, "X" if product == TG_GROUPED_Y else "dY", A.shape[1])
+    if dw:
+        ldb, w_stride = _row_stride(B, "X", K), 0
+    else:
+        ldb, w_stride = _weight_strides(B)
+    a, b, dev = A.data_ptr(), B.data_ptr(), A.device
+    size = _grouped_size(product, a % 16 == 0, b % 16 == 0, M, E, N, K, lda, ldb, w_stride)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    name = ("tg_grouped_", "tg_grouped_dx_", "tg_grouped_dw_")[product] + ("f16" if A.dtype == torch.float16 else "bf16")
+    tail = (ldd, d_stride) if dw else (w_stride, ldd)
+    _on_device(dev, getattr(_lib(), name),
+               (a, b, ends.data_ptr(), D.data_ptr(), M, E, N, K, lda, ldb, *tail, _p(ws), size,
+                torch.cuda.current_stream(dev).cuda_stream),
+               "grouped_linear (backward)" if product else "grouped_linear")
+
+
+def _weight_strides(W):
+    """Row and expert strides of the weights; experts may share memory, rows may not."""
+    E, N, K = W.shape
+    if K > 1 and W.stride(2) != 1:
+        raise ValueError("W must have a contiguous last dimension")
+    ldw = W.stride(1) if N > 1 else max(K, 1)
+    if ldw < K:
+        raise ValueError(f"W has row stride {ldw} < row length {K}; pass a tensor with non-overlapping rows")
+    return ldw, W.stride(0) if E > 1 else N * ldw
+
+
+def _grouped_forward(X, W, ends):
+    import torch
+
+    N, K = W.shape[1:]
+    Y = torch.empty((X.shape[0], N), dtype=X.dtype, device=X.device)
+    _grouped_call(TG_GROUPED_Y, X, W, ends, Y, N, K, max(N, 1))
+    return Y
+
+
+def _grouped_backward(X, W, ends, dY, need_x, need_w):
+    import torch
+
+    N, K = W.shape[1:]
+    dX = dW = None
+    if need_x:
+        dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        _grouped_call(TG_GROUPED_DX, dY, W, ends, dX, N, K, max(K, 1))
+    if need_w:
+        dW = torch.empty(W.shape, dtype=W.dtype, device=W.device)
+        _grouped_call(TG_GROUPED_DW, dY, X, ends, dW, N, K, max(K, 1), N * max(K, 1))
+    return dX, dW
+
+
+def _rows(t):
+    """t with a contiguous last dimension and rows that do not overlap."""
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        return t.contiguous()
+    return t
+
+
+@functools.lru_cache(maxsize=None)
+def _grouped_function():
+    import torch
+
+    class Gradients(torch.autograd.Function):
+        """dX and dW as values with a graph, for create_graph: what depends on them
+        would need second derivatives, which there are none of, and raises."""
+
+        @staticmethod
+        def forward(ctx, X, W, ends, dY, *how):
+            return _grouped_backward(X, W, ends, dY, *how)
+
+        @staticmethod
+        def backward(ctx, *_):
+            raise RuntimeError("grouped_linear can be differentiated once")
+
+    class GroupedLinear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, W, ends):
+            ctx.save_for_backward(X, W, ends)
+            return _grouped_forward(X, W, ends)
+
+        @staticmethod
+        def backward(ctx, dY):
+            X, W, ends = ctx.saved_tensors
+            _refuse_modes("grouped_linear (backward)", dY)
+            gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
+            return (*gradients(X, W, ends, _rows(dY), ctx.needs_input_grad[0], ctx.needs_input_grad[1]), None)
+
+    return GroupedLinear
+
+
+def grouped_linear(X, W, ends):
+    """Rows grouped by expert times their expert's weight: Y[i] = X[i]·W[e]ᵀ for
+    ends[e-1] <= i < ends[e] (ends[-1] taken as 0); rows from the last end on are 0.
+
+    X (M×K, rows sorted by expert) and W (E×N×K, one weight as ``gemm`` takes its B
+    for each expert) are fp16 or bf16 GPU tensors of one dtype on one device, with a
+    contiguous last dimension and non-overlapping rows; ``ends`` holds E int64
+    values on that device, e.g. ``torch.bincount(expert, minlength=E).cumsum(0)``. It
+    is read there and nowhere checked: a value counts as at least the one before it
+    and as 0 to M.  Returns Y (M×N) of that dtype, fp32 sums rounded once; it can be
+    differentiated with respect to X and W, once (under create_graph, what depends on
+    the gradients raises RuntimeError).  An expert without rows has a gradient of 0,
+    rows behind the last end have one of 0 and reach no gradient.
+
+    Runs on torch's current stream, never waits for the device, and takes its
+    workspace (none for 16-byte aligned rows and N, K that are multiples of 8) from
+    torch's allocator; it may be captured into a graph, whose replays read ``ends``
+    anew, its backward pass with torch.autograd.grad, or with .backward() where no
+    eager graph of the same leaves is alive (autograd would accumulate on that graph's
+    stream, which ends the capture).  Under torch.compile it runs between the
+    compiled parts.  Raises TypeError / ValueError on tensors it cannot take,
+    NotImplementedError on dual tensors (there is no forward-mode derivative) and
+    while torch.jit.trace or make_fx records (they would not see the call), and
+    TgError on a non-zero status.
+    """
+    import torch
+
+    if torch.compiler.is_dynamo_compiling():  # the call stays between the compiled parts
+        return torch.compiler.disable(grouped_linear)(X, W, ends)
+    if X.dtype != W.dtype or X.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("X and W must both be float16 or both bfloat16")
+    if ends.dtype != torch.int64:
+        raise TypeError("ends must be int64")
+    if not X.is_cuda or W.device != X.device or ends.device != X.device:
+        raise ValueError("X, W and ends must be GPU tensors on the same device")
+    if X.dim() != 2 or W.dim() != 3 or ends.dim() != 1:
+        raise ValueError("X must be 2-D, W 3-D and ends 1-D")
+    if X.shape[1] != W.shape[2]:
+        raise ValueError(f"K mismatch: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
+    if ends.shape[0] != W.shape[0]:
+        raise ValueError(f"{ends.shape[0]} ends for {W.shape[0]} experts")
+    _row_stride(X, "X", X.shape[1])
+    _weight_strides(W)
+    _refuse_modes("grouped_linear", X, W)
+    ends = ends.contiguous()
+    if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
+        return _grouped_function().apply(X, W, ends)
+    return _grouped_forward(X, W, ends)
+
+
+@functools.lru_cache(maxsize=None)
+def _embedding_names():
+    import torch
+
+    return {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+
+
+def _embedding_forward(tokens, W, scale):
+    import torch
+
+    (V, K), M, dev = W.shape, tokens.numel(), W.device
+    Y = torch.empty((*tokens.shape, K), dtype=W.dtype, device=dev)
+    _on_device(dev, getattr(_lib(), "tg_embedding_" + _embedding_names()[W.dtype]),
+               (tokens.data_ptr(), W.data_ptr(), Y.data_ptr(), M, V, K, _row_stride(W, "W", K), max(K, 1), scale,
+                torch.cuda.current_stream(dev).cuda_stream), "embedding")
+    return Y
+
+
+@functools.lru_cache(maxsize=1024)
+def _embedding_size(M, V, K):
+    return max(0, _lib().tg_embedding_bwd_workspace_bytes(M, V, K))
+
+
+def _embedding_backward(tokens, dY, V, scale, padding):
+    import torch
+
+    M, K, dev = tokens.numel(), dY.shape[-1], dY.device
+    dY = _rows(dY.reshape(M, K))
+    dW = torch.empty((V, K), dtype=dY.dtype, device=dev)
+    size = _embedding_size(M, V, K)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _on_device(dev, getattr(_lib(), "tg_embedding_bwd_" + _embedding_names()[dY.dtype]),
+               (tokens.data_ptr(), dY.data_ptr(), dW.data_ptr(), M, V, K, _row_stride(dY, "dY", K), max(K, 1), scale,
+                padding, ws.data_ptr(), size, torch.cuda.current_stream(dev).cuda_stream), "embedding (backward)")
+    return dW
+
+
+@functools.lru_cache(maxsize=None)
+def _embedding_function():
+    import torch
+
+    class Gradient(torch.autograd.Function):
+        """dW as a value with a graph, for create_graph: what depends on it would
+        need a second derivative, which there is none of, and raises."""
+
+        @staticmethod
+        def forward(ctx, *how):
+            return _embedding_backward(*how)
+
+        @staticmethod
+        def backward(ctx, *_):
+            raise RuntimeError("embedding can be differentiated once")
+
+    class Embedding(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, tokens, W, scale, padding):
+            ctx.save_for_backward(tokens)
+            ctx.how = W.shape[0], scale, padding
+            return _embedding_forward(tokens, W, scale)
+
+        @staticmethod
+        def backward(ctx, dY):
+            tokens, = ctx.saved_tensors
+            _refuse_modes("embedding (backward)", dY)
+            gradient = Gradient.apply if torch.is_grad_enabled() else _embedding_backward
+            return None, gradient(tokens, dY, *ctx.how), None, None
+
+    return Embedding
+
+
+def embedding(tokens, W, scale: float = 1.0, padding_idx: int | None = None):
+    """Embedding lookup: Y[...] = scale·W[tokens[...]].
+
+    ``tokens`` holds int64 indices in any shape, W (V×K) is a fp32, fp16 or bf16 GPU
+    tensor on the same device with a contiguous last dimension and non-overlapping
+    rows; the result has the shape of tokens and K behind it, and W's dtype.  It can be
+    differentiated with respect to W, once (under create_graph, what depends on the
+    gradient raises RuntimeError): dW[v] = scale·Σ dY over the tokens v, summed in
+    fp32 in the order of the tokens and rounded once, so that it is the same at every
+    call.  Row ``padding_idx`` gets no gradient (its row of Y is read as any other).
+    A token outside [0, V) makes its row NaN and adds to no gradient.
+
+    It gathers any rows: the tokens' hidden states in the order that ``grouped_linear``
+    takes them, with a gradient that adds up what a token's experts send back.
+
+    Runs on torch's current stream, never waits for the device, and takes its
+    workspace from torch's allocator; capture into graphs, torch.compile and the
+    exceptions are as for ``grouped_linear``.
+    """
+    import torch
+
+    if torch.compiler.is_dynamo_compiling():  # the call stays between the compiled parts
+        return torch.compiler.disable(embedding)(tokens, W, scale, padding_idx)
+    if W.dtype not in _embedding_names():
+        raise TypeError("W must be float32, float16 or bfloat16")
+    if tokens.dtype != torch.int64:
+        raise TypeError("tokens must be int64")
+    if not W.is_cuda or tokens.device != W.device:
+        raise ValueError("tokens and W must be GPU tensors on the same device")
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
+    V, K = W.shape
+    if not math.isfinite(scale) or abs(scale) > 3.4028234663852886e38:
+        raise ValueError("scale must be a finite fp32 number")
+    if padding_idx is not None and not 0 <= padding_idx < V:
+        raise ValueError(f"padding_idx must be in [0, {V})")
+    _row_stride(W, "W", K)
+    _refuse_modes("embedding", W)
+    tokens = tokens.contiguous()
+    if torch.is_grad_enabled() and W.requires_grad:
+        return _embedding_function().apply(tokens, W, float(scale), -1 if padding_idx is None else padding_idx)
+    return _embedding_forward(tokens, W, float(scale))
+
+
+@functools.lru_cache(maxsize=None)
+def _adamw_types():
+    import torch
+
+    return {torch.float32: TG_ADAMW_F32, torch.float16: TG_ADAMW_F16, torch.bfloat16: TG_ADAMW_BF16}
+
+
+def _same_dtype(ts, name, allowed):
+    """The dtype that all of ts have, one of ``allowed``."""
+    dtypes = {t.dtype for t in ts}
+    if len(dtypes) != 1 or not dtypes <= allowed:
+        raise TypeError(f"{name} must all be of one dtype among "
+                        f"{', '.join(sorted(str(d).replace('torch.', '') for d in allowed))}")
+    return dtypes.pop()
+
+
+def _scalar(x, name, dtype, dev):
+    """The address of a one-element GPU tensor, or None for a number."""
+    import torch
+
+    if not isinstance(x, torch.Tensor):
+        return None
+    if x.dtype != dtype or x.numel() != 1 or x.device != dev:
+        raise ValueError(f"{name} must be a number or a one-element {str(dtype).replace('torch.', '')} tensor on the "
+                         "device of the parameters")
+    return x.data_ptr()
+
+
+def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_decay, g_scale, copies):
+    import torch
+
+    if torch.compiler.is_dynamo_compiling():  # the call stays between the compiled parts
+        return torch.compiler.disable(_adamw)(what, params, grads, moments, scales, step, lr, betas, eps,
+                                              weight_decay, g_scale, copies)
+    bits = 8 if scales else 32
+    lists = [list(params), list(grads)] + [list(x) for x in moments + scales] + ([list(copies)] if copies is not None else [])
+    params, grads = lists[:2]
+    count = len(params)
+    if any(len(x) != count for x in lists):
+        raise ValueError("there must be as many gradients, moments and copies as parameters")
+    if count == 0:
+        return
+    dev = params[0].device
+    if not params[0].is_cuda:
+        raise ValueError("params must be GPU tensors")
+    f32, half = torch.float32, {torch.float16, torch.bfloat16}
+    p_type = _same_dtype(params, "params", {f32} | half)
+    g_type = _same_dtype(grads, "grads", {f32} | half if p_type == f32 else {p_type})
+    for x, name in zip(lists[2:4], ("exp_avgs", "exp_avg_sqs") if bits == 32 else ("exp_avgs", "roots")):
+        _same_dtype(x, name, {f32} if bits == 32 else {torch.float8_e4m3fn})
+    if scales:
+        for x, name in zip(lists[4:6], ("exp_avg_scales", "root_scales")):
+            _same_dtype(x, name, {f32})
+    copy_type = None
+    if copies is not None:
+        if p_type != f32:
+            raise ValueError("copies are for float32 parameters")
+        copy_type = _same_dtype(lists[-1], "copies", half)
+    _refuse_modes(what, *params, *grads)
+    index, sizes = dev.index, [p.numel() for p in params]
+    blocks = [(n + TG_ADAMW_BLOCK - 1) // TG_ADAMW_BLOCK for n in sizes] if scales else None
+    for k, x in enumerate(lists):
+        want = blocks if scales and k in (4, 5) else sizes
+        if [t.numel() for t in x] != want:
+            raise ValueError("gradients, moments and copies must have as many elements as their parameter"
+                             + (f", scales one for each {TG_ADAMW_BLOCK} of them" if scales else ""))
+        if not all(t.is_contiguous() for t in x):
+            raise ValueError("parameters, gradients, moments and copies must be contiguous")
+        if not all(t.is_cuda and t.get_device() == index for t in x):
+            raise ValueError("all tensors must be on one GPU")
+    for g, p in zip(grads, params):
+        if g.shape != p.shape:
+            raise ValueError(f"a gradient of shape {tuple(g.shape)} for a parameter of shape {tuple(p.shape)}")
+    if torch.is_grad_enabled() and any(t.requires_grad and not t.is_leaf for x in lists[:1] + lists[2:] for t in x):
+        raise ValueError("params, moments and copies that are results of autograd cannot be updated in place")
+    types = _adamw_types()
+    b1, b2 = betas
+    lr_at, step_at = _scalar(lr, "lr", f32, dev), _scalar(step, "step", torch.int64, dev)
+    config = tg_adamw_config(0.0 if lr_at else lr, b1, b2, eps, weight_decay, 1 if step_at else step, lr_at, step_at,
+                             _scalar(g_scale, "grad_scale", f32, dev), types[p_type], types[g_type],
+                             types[copy_type] if copy_type else 0, bits)
+    if g_scale is not None and not isinstance(g_scale, torch.Tensor):
+        raise TypeError("grad_scale must be a tensor")
+    where = [[t.data_ptr() for t in x] for x in lists]
+    none = [None] * count
+    table = (tg_adamw_tensor * count)(*zip(where[0], where[1], where[2], where[3], *(where[4:6] if scales else (none, none)),
+                                           where[-1] if copies is not None else none, sizes))
+    _on_device(dev, _lib().tg_adamw, (ctypes.addressof(table), count, ctypes.byref(config),
+                                      torch.cuda.current_stream(dev).cuda_stream), what)
+    for x in lists[:1] + lists[2:]:
+        torch.autograd.graph.increment_version([t for t in x if not t.is_inference()])
+
+
+def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+          weight_decay: float = 1e-2, grad_scale=None, copies=None) -> None:
+    """One AdamW step over lists of tensors, in place:
+
+        m ← β1·m + (1 − β1)·g,   v ← β2·v + (1 − β2)·g²
+        p ← (1 − lr·wd)·p − lr/(1 − β1^step)·m / (√v/√(1 − β2^step) + eps)
+
+    ``params`` are contiguous fp32, fp16 or bf16 GPU tensors of one dtype on one
+    device, ``grads`` tensors of their shapes and dtype (or any one of the three where
+    the parameters are fp32), ``exp_avgs`` and ``exp_avg_sqs`` the moments m and v,
+    fp32 and zeros before the first step.  ``step`` counts from 1.  ``copies``, where
+    given, are fp16 or bf16 tensors of fp32 parameters' sizes that receive them rounded.
+    ``grad_scale``, a one-element fp32 tensor on the device, multiplies the gradients
+    (the factor that clips their norm, or a loss scale's inverse).
+
+    ``lr`` and ``step`` may be one-element tensors on the device (fp32 and int64): a
+    call captured into a graph reads them anew at each replay.  Nothing is advanced
+    here.  All tensors are taken in few launches; the arithmetic is fp32 throughout
+    (include/tg_adamw.h).  Parameters may require grad; what is written counts as
+    modified in place.
+
+    Runs on torch's current stream without a workspace.  Under torch.compile it runs
+    between the compiled parts.  Raises TypeError / ValueError on tensors it cannot
+    take, NotImplementedError on dual tensors and while torch.jit.trace or make_fx
+    records, and TgError on a non-zero status, among them tensors that share memory.
+    """
+    _adamw("adamw", params, grads, [exp_avgs, exp_avg_sqs], [], step, lr, betas, eps, weight_decay, grad_scale, copies)
+
+
+def adamw_8bit_state(p):
+    """The moments of one parameter before the first ``adamw_8bit`` step: (exp_avg,
+    exp_avg_scale, root, root_scale), zeros.  A moment's values are those of the E4M3
+    tensor times their block's scale: ``exp_avg.float().flatten() *
+    exp_avg_scale.repeat_interleave(256)[:p.numel()]``, and the second moment is the square of the root's."""
+    import torch
+
+    blocks = (p.numel() + TG_ADAMW_BLOCK - 1) // TG_ADAMW_BLOCK
+
+    def codes():
+        return torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
+
+    def scales():
+        return torch.zeros(blocks, dtype=torch.float32, device=p.device)
+
+    return codes(), scales(), codes(), scales()
+
+
+def adamw_8bit(params, grads, exp_avgs, exp_avg_scales, roots, root_scales, step, lr=1e-3, betas=(0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 1e-2, grad_scale=None, copies=None) -> None:
+    """``adamw`` with moments held in 8 bits: E4M3 tensors of the parameters' sizes
+    with one fp32 scale for each 256 elements, of m and of √v (``adamw_8bit_state``
+    makes them).  The step itself uses the moments before they are rounded; a rounding
+    is at most 2^-4 of the value.  include/tg_adamw.h says what is held of small,
+    infinite and NaN values.  Everything else is as for ``adamw``."""
+    _adamw("adamw_8bit", params, grads, [exp_avgs, roots], [exp_avg_scales, root_scales], step, lr, betas, eps,
+           weight_decay, grad_scale, copies)

@@ -1,0 +1,322 @@
+"""Host-side checks of the training operators that need no GPU: refusals, workspace
+sizes, plans, and a C99 caller of the headers."""
+import ctypes
+import itertools
+import os
+import shutil
+import subprocess
+
+import pytest
+
+tg = pytest.importorskip("dense_fp16_gemm_02_amd")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 1 << 20          # 16-byte aligned, never dereferenced
+BIG = 1 << 62
+LIM = 1 << 31
+
+
+# ------------------------------------------------------------------ grouped
+def y(X=A, W=A, ends=A, Y=A, M=5, E=2, N=8, K=16, ldx=16, ldw=16, ws_=128, ldy=8, ws=None, size=0, fn=None):
+    return (fn or tg.tg_grouped_f16)(X, W, ends, Y, M, E, N, K, ldx, ldw, ws_, ldy, ws, size, None)
+
+
+def dx(dY=A, W=A, ends=A, dX=A, M=5, E=2, N=8, K=16, lddy=8, ldw=16, ws_=128, lddx=16, ws=None, size=0, fn=None):
+    return (fn or tg.tg_grouped_dx_bf16)(dY, W, ends, dX, M, E, N, K, lddy, ldw, ws_, lddx, ws, size, None)
+
+
+def dw(dY=A, X=A, ends=A, dW=A, M=5, E=2, N=8, K=16, lddy=8, ldx=16, lddw=16, dws=128, ws=None, size=0, fn=None):
+    return (fn or tg.tg_grouped_dw_bf16)(dY, X, ends, dW, M, E, N, K, lddy, ldx, lddw, dws, ws, size, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(E=-1), dict(N=-1), dict(K=-1), dict(ldx=15), dict(ldw=15), dict(ws_=-1), dict(ldy=7), dict(X=None),
+    dict(W=None), dict(ends=None), dict(Y=None), dict(X=A + 1), dict(W=A + 1), dict(Y=A + 1), dict(ends=A + 4),
+    dict(X=A + 2), dict(X=A + 2, ws=A + 8, size=BIG), dict(K=15), dict(ldw=17, ws_=136), dict(ws_=129),
+    dict(N=0, K=-1), dict(E=0, Y=None), dict(K=0, ldx=0, ldw=0, Y=None),
+])
+def test_grouped_refuses(kw):
+    for fn in (tg.tg_grouped_f16, tg.tg_grouped_bf16):
+        assert y(fn=fn, **kw) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(lddy=7), dict(ldw=15), dict(ws_=-5), dict(lddx=15), dict(dY=None), dict(W=None), dict(ends=None),
+    dict(dX=None), dict(dY=A + 2), dict(N=7, lddy=7), dict(dX=A + 1), dict(N=0, lddy=0, dX=None),
+])
+def test_grouped_dx_refuses(kw):
+    for fn in (tg.tg_grouped_dx_f16, tg.tg_grouped_dx_bf16):
+        assert dx(fn=fn, **kw) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(E=-1), dict(lddy=7), dict(ldx=15), dict(lddw=15), dict(dws=127), dict(dY=None), dict(X=None), dict(ends=None),
+    dict(dW=None), dict(X=A + 2), dict(K=15), dict(M=0, dW=None), dict(dws=-1),
+])
+def test_grouped_dw_refuses(kw):
+    for fn in (tg.tg_grouped_dw_f16, tg.tg_grouped_dw_bf16):
+        assert dw(fn=fn, **kw) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=LIM), dict(E=1 << 16), dict(N=1 << 21, ldy=1 << 21), dict(K=1 << 21, ldx=1 << 21, ldw=1 << 21), dict(ldx=LIM),
+    dict(ldw=LIM), dict(ws_=1 << 42), dict(ldy=LIM), dict(M=LIM - 1, E=1, N=1 << 20, ldy=1 << 20),
+])
+def test_grouped_too_large(kw):
+    assert y(**kw) == tg.TG_ERR_TOO_LARGE
+    sizes = {**dict(M=5, E=2, N=8, K=16, ldx=16, ldw=16, ws_=128), **kw}
+    if "ldy" not in kw or "N" in kw:
+        assert tg.tg_grouped_workspace_bytes(tg.TG_GROUPED_Y, A, A, *(sizes[k] for k in ("M", "E", "N", "K", "ldx", "ldw", "ws_"))) == -1
+    if kw == dict(E=1 << 16):
+        assert dx(**kw) == dw(**kw) == tg.TG_ERR_TOO_LARGE
+
+
+def test_grouped_dw_too_large():
+    assert dw(lddw=LIM, dws=1 << 40) == dw(dws=1 << 42) == dx(lddx=LIM) == tg.TG_ERR_TOO_LARGE
+    assert dw(E=65535, N=1 << 12, K=1 << 12, lddy=1 << 12, ldx=1 << 12, lddw=1 << 12, dws=1 << 24) == tg.TG_ERR_TOO_LARGE
+
+
+def test_grouped_nothing_to_do():
+    for kw in (dict(M=0), dict(N=0, ldy=0)):
+        assert y(X=None, W=None, ends=None, Y=None, **kw) == tg.TG_OK
+    for kw in (dict(M=0), dict(K=0, ldw=0, lddx=0)):
+        assert dx(dY=None, W=None, ends=None, dX=None, **kw) == tg.TG_OK
+    for kw in (dict(E=0), dict(N=0, lddy=0), dict(K=0, ldx=0, lddw=0)):
+        assert dw(dY=None, X=None, ends=None, dW=None, **kw) == tg.TG_OK
+
+
+def test_grouped_workspaces():
+    size = tg.tg_grouped_workspace_bytes
+    for product in (tg.TG_GROUPED_Y, tg.TG_GROUPED_DX, tg.TG_GROUPED_DW):
+        assert size(product, A, A, 100, 4, 64, 128, 128, 128, 64 * 128) == 0
+        assert size(product, A + 2, A, 100, 4, 64, 128, 128, 128, 64 * 128) > 0
+        assert size(product, A, A, 0, 4, 63, 128, 128, 128, 64 * 128) == 0
+        assert size(product, A, A, -1, 4, 64, 128, 128, 128, 64 * 128) == -1
+    assert size(3, A, A, 100, 4, 64, 128, 128, 128, 64 * 128) == size(-1, A, A, 100, 4, 64, 128, 128, 128, 64 * 128) == -1
+    n = size(tg.TG_GROUPED_Y, A, A, 100, 4, 64, 127, 127, 127, 64 * 127)
+    assert n >= 2 * (100 + 4 * 64) * 128 and n % 256 == 0
+    args = dict(M=100, E=4, N=64, K=127, ldx=127, ldw=127, ws_=64 * 127, ldy=64)
+    assert y(**args, ws=A, size=n - 1) == y(**args, ws=A + 128, size=n) == y(**args, ws=None, size=n) == tg.TG_ERR_INVALID_ARG
+    # one row or one expert: the strides between them do not count
+    assert size(tg.TG_GROUPED_Y, A, A, 1, 1, 64, 128, 131, 128, 5) == 0
+    assert size(tg.TG_GROUPED_Y, A, A, 2, 1, 64, 128, 131, 128, 5) > 0
+
+
+@pytest.mark.parametrize("product,args,name", [
+    (tg.TG_GROUPED_Y, (A, A, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "y_16x64"),
+    (tg.TG_GROUPED_Y, (A, A, 16384, 8, 14336, 4096, 4096, 4096, 14336 * 4096), "y_256x256"),
+    (tg.TG_GROUPED_DX, (A, A, 16384, 8, 14336, 4096, 14336, 4096, 14336 * 4096), "dx_256x256"),
+    (tg.TG_GROUPED_DW, (A, A, 16384, 8, 14336, 4096, 14336, 4096, 0), "dw_256x256"),
+    (tg.TG_GROUPED_Y, (A, A + 2, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "pack_b y_16x64"),
+    (tg.TG_GROUPED_Y, (A + 2, A, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "pack_a y_16x64"),
+    (tg.TG_GROUPED_Y, (A, A, 5, 0, 8, 16, 16, 16, 128), "zero"),
+    (tg.TG_GROUPED_DX, (A, A, 5, 2, 0, 16, 0, 16, 0), "zero"),
+    (tg.TG_GROUPED_DW, (A, A, 0, 2, 8, 16, 8, 16, 0), "zero"),
+    (tg.TG_GROUPED_DW, (A, A, 0, 0, 8, 16, 8, 16, 0), ""),
+    (tg.TG_GROUPED_Y, (A, A, 0, 2, 8, 16, 16, 16, 128), ""),
+])
+def test_grouped_plans(product, args, name):
+    assert tg.tg_grouped_plan(product, *args) == (tg.TG_OK, name)
+
+
+# ---------------------------------------------------------------- embedding
+def look(tokens=A, W=A, Y=A, M=4, V=6, K=8, ldw=8, ldy=8, scale=1.0, fn=None):
+    return (fn or tg.tg_embedding_f32)(tokens, W, Y, M, V, K, ldw, ldy, scale, None)
+
+
+def back(tokens=A, dY=A, dW=A, M=4, V=6, K=8, lddy=8, lddw=8, scale=1.0, padding=-1, ws=A, size=BIG, fn=None):
+    return (fn or tg.tg_embedding_bwd_f32)(tokens, dY, dW, M, V, K, lddy, lddw, scale, padding, ws, size, None)
+
+
+@pytest.mark.parametrize("kw", [dict(M=-1), dict(V=-1), dict(K=-1), dict(ldw=7), dict(ldy=7), dict(tokens=None),
+                                dict(W=None), dict(Y=None), dict(tokens=A + 4), dict(W=A + 1), dict(Y=A + 1)])
+def test_embedding_refuses(kw):
+    for fn in (tg.tg_embedding_f32, tg.tg_embedding_f16, tg.tg_embedding_bf16):
+        assert look(fn=fn, **kw) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(M=-1), dict(V=-1), dict(K=-1), dict(lddy=7), dict(lddw=7), dict(tokens=None),
+                                dict(dY=None), dict(dW=None), dict(tokens=A + 2), dict(dY=A + 1), dict(dW=A + 1),
+                                dict(ws=None), dict(ws=A + 64), dict(size=10), dict(M=0, dW=None)])
+def test_embedding_backward_refuses(kw):
+    for fn in (tg.tg_embedding_bwd_f32, tg.tg_embedding_bwd_f16, tg.tg_embedding_bwd_bf16):
+        assert back(fn=fn, **kw) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(M=LIM), dict(V=LIM), dict(K=LIM, ldw=LIM, ldy=LIM), dict(ldw=LIM), dict(ldy=LIM),
+                                dict(M=1 << 30, K=1 << 10, ldw=1 << 10, ldy=1 << 10)])
+def test_embedding_too_large(kw):
+    assert look(**kw) == tg.TG_ERR_TOO_LARGE
+
+
+@pytest.mark.parametrize("kw", [dict(M=LIM), dict(V=LIM), dict(M=1 << 30, V=1 << 30), dict(lddy=LIM), dict(lddw=LIM),
+                                dict(V=1 << 30, K=1 << 10, lddy=1 << 10, lddw=1 << 10)])
+def test_embedding_backward_too_large(kw):
+    assert back(**kw) == tg.TG_ERR_TOO_LARGE
+    if "lddy" not in kw:
+        s = {**dict(M=4, V=6, K=8), **{k: v for k, v in kw.items() if len(k) == 1}}
+        assert tg.tg_embedding_bwd_workspace_bytes(s["M"], s["V"], s["K"]) == -1 or "lddw" in kw
+
+
+def test_embedding_nothing_to_do_and_workspaces():
+    assert look(M=0, tokens=None, W=None, Y=None) == look(K=0, tokens=None, W=None, Y=None, ldw=0, ldy=0) == tg.TG_OK
+    for kw in (dict(V=0), dict(K=0, lddy=0, lddw=0)):
+        assert back(tokens=None, dY=None, dW=None, ws=None, size=0, **kw) == tg.TG_OK
+    n = tg.tg_embedding_bwd_workspace_bytes(100, 1000, 64)
+    assert n > 0 and n % 256 == 0
+    args = dict(M=100, V=1000, K=64, lddy=64, lddw=64)
+    assert back(**args, size=n - 1) == tg.TG_ERR_INVALID_ARG
+    assert tg.tg_embedding_bwd_workspace_bytes(-1, 5, 5) == -1
+    assert tg.tg_embedding_bwd_workspace_bytes(0, 5, 0) == 0 == tg.tg_embedding_bwd_workspace_bytes(3, 0, 8)
+    for M, V, K in itertools.product((0, 1, 8192, 8193, 1 << 20), (1, 255, 1 << 17, 1 << 24), (1, 64, 4096)):
+        if (M + V) * K < 1 << 40:
+            # far below the gradients' own size where there are many rows
+            assert 0 < tg.tg_embedding_bwd_workspace_bytes(M, V, K) <= 24 * M + (M + V) * (K + 16) + (1 << 18)
+
+
+# ------------------------------------------------------------------- adamw
+def tensor(base=A, n=1000, bits=32, pb=4, gb=4, **kw):
+    """One tensor whose roles lie 1 MiB apart."""
+    t = dict(p=base, g=base + (1 << 20), m=base + (2 << 20), v=base + (3 << 20), n=n, copy=None,
+             m_scale=base + (4 << 20) if bits == 8 else None, v_scale=base + (5 << 20) if bits == 8 else None)
+    t.update(kw)
+    return tg.tg_adamw_tensor(**t)
+
+
+def config(**kw):
+    c = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, lr_at=None, step_at=None, g_scale=None,
+             p_type=tg.TG_ADAMW_F32, g_type=tg.TG_ADAMW_F32, copy_type=0, bits=32)
+    c.update(kw)
+    return tg.tg_adamw_config(**c)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lr=-1.0), dict(lr=NAN), dict(lr=INF), dict(beta1=-0.1), dict(beta1=1.0), dict(beta1=NAN), dict(beta2=1.0),
+    dict(beta2=-1.0), dict(eps=-1e-8), dict(eps=NAN), dict(eps=INF), dict(weight_decay=-0.1), dict(weight_decay=INF),
+    dict(step=0), dict(step=-3), dict(p_type=3), dict(g_type=-1), dict(p_type=tg.TG_ADAMW_F16, g_type=tg.TG_ADAMW_BF16),
+    dict(p_type=tg.TG_ADAMW_F16), dict(bits=16), dict(bits=0), dict(lr_at=A + 2), dict(step_at=A + 4), dict(g_scale=A + 1),
+])
+def test_adamw_refuses_settings(kw):
+    assert tg.tg_adamw([tensor()], config(**kw)) == tg.TG_ERR_INVALID_ARG
+    assert tg.tg_adamw([], config(**kw)) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=-1), dict(p=None), dict(g=None), dict(m=None), dict(v=None), dict(p=A + 2), dict(g=A + 1), dict(m=A + 2),
+    dict(v=A + 3), dict(g=A), dict(m=A), dict(v=A + 4), dict(m=A + (3 << 20) + 3996), dict(copy=A + (6 << 20)),
+    dict(copy=A + (6 << 20) + 1),
+])
+def test_adamw_refuses_tensors(kw):
+    assert tg.tg_adamw([tensor(**kw)], config()) == tg.TG_ERR_INVALID_ARG
+    assert tg.tg_adamw([tensor(A + (64 << 20)), tensor(**kw)], config()) == tg.TG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(m_scale=None), dict(v_scale=None), dict(m_scale=A + 2), dict(v_scale=A + (2 << 20)),
+                                dict(m_scale=A + (5 << 20) + 12)])
+def test_adamw_8bit_refuses_tensors(kw):
+    assert tg.tg_adamw([tensor(bits=8, **kw)], config(bits=8)) == tg.TG_ERR_INVALID_ARG
+
+
+def test_adamw_refuses_shared_memory():
+    a, b = tensor(), tensor(A + (64 << 20))
+    c = config()
+    assert tg.tg_adamw([a, a], c) == tg.TG_ERR_INVALID_ARG
+    for role in ("p", "m", "v"):
+        for other in ("p", "g", "m", "v"):
+            x = tensor(A + (64 << 20), **{other: getattr(a, role) + 400})
+            assert tg.tg_adamw([a, x], c) == tg.TG_ERR_INVALID_ARG, (role, other)
+            assert tg.tg_adamw([x, a], c) == tg.TG_ERR_INVALID_ARG, (role, other)
+    for at in (b.p + 3996, b.m, b.v):
+        assert tg.tg_adamw([a, b], config(lr_at=at)) == tg.TG_ERR_INVALID_ARG
+        assert tg.tg_adamw([a, b], config(g_scale=at)) == tg.TG_ERR_INVALID_ARG
+    copy = config(copy_type=tg.TG_ADAMW_BF16)
+    assert tg.tg_adamw([a, tensor(A + (64 << 20), copy=a.p)], copy) == tg.TG_ERR_INVALID_ARG
+    assert tg.tg_adamw([tensor(pb=2, copy=A + (7 << 20))], config(p_type=2, g_type=2, copy_type=2)) == tg.TG_ERR_INVALID_ARG
+
+
+def test_adamw_too_large_and_empty():
+    assert tg.tg_adamw([tensor(n=1 << 35)], config()) == tg.TG_ERR_TOO_LARGE
+    assert tg.tg_adamw([], config()) == tg.TG_OK
+    assert tg.tg_adamw([tensor(n=0, p=None, g=None, m=None, v=None)] * 3, config()) == tg.TG_OK
+    lib = tg.load()
+    assert lib.tg_adamw(None, 0, ctypes.byref(config()), None) == tg.TG_OK
+    assert lib.tg_adamw(None, 1, ctypes.byref(config()), None) == tg.TG_ERR_INVALID_ARG
+    assert lib.tg_adamw(None, -1, ctypes.byref(config()), None) == tg.TG_ERR_INVALID_ARG
+    assert lib.tg_adamw(None, 0, None, None) == tg.TG_ERR_INVALID_ARG
+
+
+# ----------------------------------------------------------------- wrappers
+def test_wrappers_refuse_tensors_they_cannot_take():
+    torch = pytest.importorskip("torch")
+    X, W, ends = torch.zeros(4, 16).half(), torch.zeros(2, 8, 16).half(), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU"):
+        tg.grouped_linear(X, W, ends)
+    with pytest.raises(TypeError):
+        tg.grouped_linear(X.float(), W.float(), ends)
+    with pytest.raises(TypeError):
+        tg.grouped_linear(X, W.bfloat16(), ends)
+    with pytest.raises(TypeError):
+        tg.grouped_linear(X, W, ends.int())
+    tokens, T = torch.zeros(4, dtype=torch.int64), torch.zeros(8, 16)
+    with pytest.raises(ValueError, match="GPU"):
+        tg.embedding(tokens, T)
+    with pytest.raises(TypeError):
+        tg.embedding(tokens.int(), T)
+    with pytest.raises(TypeError):
+        tg.embedding(tokens, T.double())
+    p = [torch.zeros(4)]
+    with pytest.raises(ValueError, match="GPU"):
+        tg.adamw(p, p, p, p, 1)
+    with pytest.raises(ValueError, match="as many"):
+        tg.adamw(p, p + p, p, p, 1)
+    tg.adamw([], [], [], [], 1)
+
+
+PROGRAM = r"""
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+#include "tg_gemm.h"
+#include "tg_grouped.h"
+#include "tg_embed.h"
+#include "tg_adamw.h"
+
+int main(void)
+{
+    const void *X = (const void *)(uintptr_t)0x100000, *W = (const void *)(uintptr_t)0x200000;
+    char name[64];
+    tg_adamw_tensor t;
+    tg_adamw_config c;
+    int fails = 0;
+    if (tg_grouped_plan(TG_GROUPED_Y, X, W, 8, 64, 1024, 2048, 2048, 2048, 2097152, name, sizeof name) != TG_OK) ++fails;
+    if (strcmp(name, "y_16x64") != 0) ++fails;
+    if (tg_grouped_plan(TG_GROUPED_Y, X, W, 8, 64, 1024, 2048, 2048, 2048, 2097152, name, 4) != TG_OK || strcmp(name, "y_1") != 0) ++fails;
+    if (tg_grouped_bf16(X, W, 0, 0, 4, 2, 8, 16, 16, 16, 128, 8, 0, 0, 0) != TG_ERR_INVALID_ARG) ++fails;
+    if (tg_embedding_f16(0, W, 0, 4, 8, 16, 16, 16, 1.0f, 0) != TG_ERR_INVALID_ARG) ++fails;
+    if (tg_embedding_bwd_workspace_bytes(4, 8, 16) <= 0) ++fails;
+    memset(&t, 0, sizeof t);
+    memset(&c, 0, sizeof c);
+    c.bits = 32, c.step = 1, c.beta1 = 0.9, c.beta2 = 0.999, c.p_type = TG_ADAMW_F32, c.g_type = TG_ADAMW_BF16;
+    if (tg_adamw(&t, 1, &c, 0) != TG_OK) ++fails;
+    t.n = TG_ADAMW_BLOCK;
+    if (tg_adamw(&t, 1, &c, 0) != TG_ERR_INVALID_ARG) ++fails;
+    printf("fails %d\n", fails);
+    return fails;
+}
+"""
+
+
+def test_c99_caller(tmp_path):
+    cc = shutil.which("gcc")
+    if not cc:
+        pytest.skip("gcc not available")
+    src, exe = tmp_path / "p.c", tmp_path / "p"
+    src.write_text(PROGRAM)
+    lib = os.path.dirname(tg.lib_path())
+    subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", f"-I{os.path.join(ROOT, 'include')}",
+                    str(src), "-o", str(exe), tg.lib_path(), f"-Wl,-rpath,{lib}"], check=True)
+    p = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert p.returncode == 0, p.stdout
