@@ -4,7 +4,7 @@
 // The lookup copies rows, 16 bytes a lane.
 //
 // The gradient sorts the tokens (a stable radix sort of (token, row of dY)
-// pairs, 8 bits a pass) and walks two sorted lists at once, the sorted tokens and
+// pairs) and walks two sorted lists at once, the sorted tokens and
 // the rows of dW, each row after its tokens: a token adds its row of dY to the sum
 // in registers, a row stores the sum and clears it.  The walk is cut into equal
 // pieces of the two lists taken together (the "merge path" partition of Merrill
@@ -30,7 +30,10 @@ using namespace pt;
 template <typename E>
 constexpr int VEC = 16 / (int)sizeof(E);  // elements of a lane
 
-// 16 bytes at the alignment of an element, `n` elements of them inside the row
+// 16 bytes at the alignment of an element, `n` elements of them inside the row.
+// A store of aligned ones is spelled out: the compiler splits it otherwise where it
+// knows the values (rows of zeros: 1 GB of them in 300 us instead of 220).
+typedef float f32x4_row __attribute__((ext_vector_type(4)));
 template <typename E>
 __device__ inline void load_row(E (&x)[VEC<E>], const E *p, int n)
 {
@@ -42,10 +45,18 @@ __device__ inline void load_row(E (&x)[VEC<E>], const E *p, int n)
             x[e] = e < n ? p[e] : (E)0.0f;
     }
 }
-template <typename E>
+// NT: past the caches.
+template <bool NT = false, typename E>
 __device__ inline void store_row(const E (&x)[VEC<E>], E *p, int n)
 {
-    if (n >= VEC<E>) {
+    if (n >= VEC<E> && (uintptr_t)p % 16 == 0) {
+        f32x4_row v;
+        __builtin_memcpy(&v, x, 16);
+        if constexpr (NT)
+            __builtin_nontemporal_store(v, reinterpret_cast<f32x4_row *>(p));
+        else
+            *reinterpret_cast<f32x4_row *>(p) = v;
+    } else if (n >= VEC<E>) {
         __builtin_memcpy(p, x, 16);
     } else {
 #pragma unroll
@@ -65,8 +76,12 @@ struct LookArgs {
     int segments;  // of 64 lanes · LOOK_STEPS to a row
     float scale;
 };
-// A wave takes LOOK_STEPS·64 lanes of one row.
-template <typename E>
+// A wave takes LOOK_STEPS·64 lanes of one row.  Bound by memory.  NT: Y is too large
+// to be kept for its reader anyway; without it Y displaces W from the last-level cache
+// (65536 tokens of 32000×2048 fp16, 268 MB of Y: 64 us, 86 without; 8192 of
+// 131072×4096 bf16, 64 MiB: 23.5 and 24.9).
+constexpr int64_t NT_BYTES = (int64_t)64 << 20;
+template <typename E, bool NT>
 __global__ __launch_bounds__(LOOK_THREADS) void embedding_kernel(LookArgs a)
 {
     const int lane = threadIdx.x & 63;
@@ -82,7 +97,7 @@ __global__ __launch_bounds__(LOOK_THREADS) void embedding_kernel(LookArgs a)
 #pragma unroll
         for (int k = 0; k < LOOK_STEPS; ++k) {
             const int64_t c = c0 + k * (64 * VEC<E>);
-            load_row(x[k], src + c, in && c < a.K ? (int)imin((int)(a.K - c), VEC<E>) : 0);
+            load_row(x[k], src + c, in && c < a.K ? imin((int)(a.K - c), VEC<E>) : 0);
         }
 #pragma unroll
         for (int k = 0; k < LOOK_STEPS; ++k) {
@@ -91,23 +106,25 @@ __global__ __launch_bounds__(LOOK_THREADS) void embedding_kernel(LookArgs a)
             for (int e = 0; e < VEC<E>; ++e)
                 x[k][e] = in ? (E)((float)x[k][e] * a.scale) : (E)NAN;
             if (c < a.K)
-                store_row(x[k], dst + c, (int)imin((int)(a.K - c), VEC<E>));
+                store_row<NT>(x[k], dst + c, imin((int)(a.K - c), VEC<E>));
         }
     }
 }
 
 // -------------------------------------------------------------------- sort
-constexpr int SORT_THREADS = 1024, SORT_WAVES = SORT_THREADS / 64, SORT_PER = 8;
-constexpr int SORT_TILE = SORT_THREADS * SORT_PER;  // pairs of a workgroup
-constexpr int DIGITS = 256;
+// A stable radix sort in as few passes as digits of up to 9 bits allow (two for
+// up to 2^18 rows).
+constexpr int SORT_PER = 8;              // pairs of a lane
+constexpr int DIGIT_BITS = 9, DIGITS = 1 << DIGIT_BITS;
+constexpr int FEW = 256, MANY = 1024;    // threads of a workgroup
 struct SortArgs {
     const int64_t *tokens;          // first pass
     const uint32_t *key_in, *at_in; // later passes
     uint32_t *key, *at;
-    uint32_t *count;                // [digit][workgroup]
+    uint32_t *count;                // [workgroup][digit]
     int M, V;
     int64_t padding;
-    int tiles, shift, passes;
+    int tiles, shift, bits, passes;  // bits: of a digit
 };
 // A token that adds to no row sorts behind all rows.
 __device__ inline uint32_t token_key(const SortArgs &a, int i)
@@ -115,102 +132,134 @@ __device__ inline uint32_t token_key(const SortArgs &a, int i)
     const int64_t t = a.tokens[i];
     return t >= 0 && t < a.V && t != a.padding ? (uint32_t)t : (uint32_t)a.V;
 }
-// Item r of this lane: a wave's items are consecutive, 64 to a round.
-__device__ inline int sort_item(int wave, int lane, int r) { return wave * (64 * SORT_PER) + r * 64 + lane; }
+// Items of a wave, so that few are spread over all waves.
+template <int THREADS>
+__device__ inline int wave_items(int items)
+{
+    return 64 * ((items + THREADS - 1) / THREADS);
+}
+// Item r of this lane: a wave's items are consecutive, 64 to a round.  Past the
+// wave's: INT_MAX.
+__device__ inline int sort_item(int wave, int lane, int r, int per)
+{
+    return 64 * r < per ? wave * per + r * 64 + lane : 0x7fffffff;
+}
 
+template <int THREADS>
 struct SortShared {
-    uint32_t wave_count[SORT_WAVES][DIGITS];  // of a digit in a wave, then where the wave's first of it goes
-    uint32_t wave_sum[SORT_WAVES];
+    static constexpr int WAVES = THREADS / 64;
+    uint32_t wave_count[WAVES][DIGITS];  // of a digit in a wave, then where the wave's first of it goes
+    uint32_t wave_sum[WAVES];
     uint32_t base[DIGITS];
 };
+// Exclusive sum of x over the workgroup's threads.
+template <int THREADS>
+__device__ inline uint32_t sum_before(uint32_t x, uint32_t *wave_sum)
+{
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    uint32_t upto = x;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = __shfl_up(upto, o);
+        upto += lane >= o ? y : 0;
+    }
+    if (lane == 63)
+        wave_sum[wave] = upto;
+    __syncthreads();
+    uint32_t before = upto - x;
+    for (int w = 0; w < wave; ++w)
+        before += wave_sum[w];
+    __syncthreads();
+    return before;
+}
 // For each of this lane's items its place among the workgroup's items, ordered
 // by digit and, within one, as they came.  Lanes of a wave that hold the same
 // digit find each other with one ballot per bit.
-__device__ inline void sort_places(SortShared &s, const uint32_t (&key)[SORT_PER], int items, int shift,
+template <int THREADS>
+__device__ inline void sort_places(SortShared<THREADS> &s, const uint32_t (&key)[SORT_PER], int items, int shift, int bits,
                                    uint32_t (&place)[SORT_PER])
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    constexpr int WAVES = THREADS / 64;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), per = wave_items<THREADS>(items);
+    const uint32_t mask = (1u << bits) - 1;
     for (int d = lane; d < DIGITS; d += 64)
         s.wave_count[wave][d] = 0;
     __builtin_amdgcn_wave_barrier();
     volatile uint32_t *mine = s.wave_count[wave];
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r) {
-        const bool live = sort_item(wave, lane, r) < items;
-        const uint32_t d = (key[r] >> shift) & (DIGITS - 1);
-        uint64_t same = __ballot(live);
+        place[r] = 0;
+        if (sort_item(wave, 0, r, per) >= items)  // the same for the whole wave
+            continue;
+        const bool live = sort_item(wave, lane, r, per) < items;
+        const uint32_t d = (key[r] >> shift) & mask;
+        const uint64_t all = __ballot(live);
+        uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            const uint64_t set = __ballot((d >> b) & 1);
-            same &= (d >> b) & 1 ? set : ~set;
+        for (int b = 0; b < DIGIT_BITS; ++b) {
+            const uint32_t bit = (d >> b) & 1, flip = bit - 1;  // all ones where the bit is clear
+            const uint64_t set = __ballot(bit);
+            lo &= (uint32_t)set ^ flip;
+            hi &= (uint32_t)(set >> 32) ^ flip;
         }
-        const uint32_t before = (uint32_t)__popcll(same & ((1ull << lane) - 1));
+        const uint32_t before = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
         const uint32_t seen = mine[d];
         __builtin_amdgcn_wave_barrier();
         if (live && before == 0)
-            mine[d] = seen + (uint32_t)__popcll(same);
+            mine[d] = seen + (uint32_t)(__popc(lo) + __popc(hi));
         __builtin_amdgcn_wave_barrier();
         place[r] = seen + before;
     }
     __syncthreads();
-    // exclusive sums over (digit, wave), four waves of one digit to a thread
-    constexpr int QUADS = SORT_WAVES / 4;
-    static_assert(DIGITS * QUADS == SORT_THREADS, "a thread for four counts");
-    const int d = tid / QUADS, w0 = 4 * (tid % QUADS);
-    uint32_t c[4], sum = 0;
+    // exclusive sums over (digit, wave): a thread takes all waves of some digits,
+    // or some waves of one
+    constexpr int EACH = WAVES * DIGITS / THREADS;  // counts of a thread: DIGITS / 64
+    static_assert(EACH % WAVES == 0 || WAVES % EACH == 0, "whole digits, or one digit's waves");
+    uint32_t c[EACH], sum = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        c[w] = s.wave_count[w0 + w][d];
-        sum += c[w];
+    for (int k = 0; k < EACH; ++k) {
+        c[k] = s.wave_count[(tid * EACH + k) % WAVES][(tid * EACH + k) / WAVES];
+        sum += c[k];
     }
-    uint32_t upto = sum;
+    uint32_t at = sum_before<THREADS>(sum, s.wave_sum);
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t x = __shfl_up(upto, o);
-        upto += lane >= o ? x : 0;
-    }
-    if (lane == 63)
-        s.wave_sum[wave] = upto;
-    __syncthreads();
-    uint32_t at = upto - sum;
-    for (int w = 0; w < wave; ++w)
-        at += s.wave_sum[w];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        s.wave_count[w0 + w][d] = at;
-        at += c[w];
+    for (int k = 0; k < EACH; ++k) {
+        s.wave_count[(tid * EACH + k) % WAVES][(tid * EACH + k) / WAVES] = at;
+        at += c[k];
     }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r)
-        place[r] += s.wave_count[wave][(key[r] >> shift) & (DIGITS - 1)];
+        place[r] += s.wave_count[wave][(key[r] >> shift) & mask];
 }
 
-// All passes of at most SORT_TILE tokens, by one workgroup.
-__global__ __launch_bounds__(SORT_THREADS) void sort_small_kernel(SortArgs a)
+// All passes of at most MANY·SORT_PER tokens, by one workgroup.
+constexpr int SORT_SMALL = MANY * SORT_PER;
+__global__ __launch_bounds__(MANY) void sort_small_kernel(SortArgs a)
 {
-    __shared__ SortShared s;
-    __shared__ uint32_t keys[SORT_TILE], ats[SORT_TILE];
+    __shared__ SortShared<MANY> s;
+    __shared__ uint32_t keys[SORT_SMALL], ats[SORT_SMALL];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int per = wave_items<MANY>(a.M);
     uint32_t key[SORT_PER], at[SORT_PER], place[SORT_PER];
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r) {
-        const int i = sort_item(wave, lane, r);
+        const int i = sort_item(wave, lane, r, per);
         key[r] = i < a.M ? token_key(a, i) : 0;
         at[r] = (uint32_t)i;
     }
     for (int p = 0; p < a.passes; ++p) {
-        sort_places(s, key, a.M, 8 * p, place);
+        sort_places<MANY>(s, key, a.M, a.bits * p, a.bits, place);
 #pragma unroll
         for (int r = 0; r < SORT_PER; ++r)
-            if (sort_item(wave, lane, r) < a.M) {
+            if (sort_item(wave, lane, r, per) < a.M) {
                 keys[place[r]] = key[r];
                 ats[place[r]] = at[r];
             }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < SORT_PER; ++r) {
-            const int i = sort_item(wave, lane, r);
+            const int i = sort_item(wave, lane, r, per);
             if (i < a.M) {
                 key[r] = keys[i];
                 at[r] = ats[i];
@@ -220,7 +269,7 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_small_kernel(SortArgs a)
     }
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r) {
-        const int i = sort_item(wave, lane, r);
+        const int i = sort_item(wave, lane, r, per);
         if (i < a.M) {
             a.key[i] = key[r];
             a.at[i] = at[r];
@@ -229,78 +278,85 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_small_kernel(SortArgs a)
 }
 
 // How often each digit occurs in each workgroup's pairs.
-template <bool FIRST>
-__global__ __launch_bounds__(SORT_THREADS) void sort_count_kernel(SortArgs a)
+template <int THREADS, bool FIRST>
+__global__ __launch_bounds__(THREADS) void sort_count_kernel(SortArgs a)
 {
     __shared__ uint32_t count[DIGITS];
     const int tid = threadIdx.x;
-    if (tid < DIGITS)
-        count[tid] = 0;
+    for (int d = tid; d < DIGITS; d += THREADS)
+        count[d] = 0;
     __syncthreads();
-    const int i0 = (int)blockIdx.x * SORT_TILE;
+    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * SORT_PER);
+    const uint32_t mask = (1u << a.bits) - 1;
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r) {
-        const int i = i0 + r * SORT_THREADS + tid;
+        const int64_t i = i0 + r * THREADS + tid;
         if (i < a.M)
-            atomicAdd(&count[((FIRST ? token_key(a, i) : a.key_in[i]) >> a.shift) & (DIGITS - 1)], 1u);
+            atomicAdd(&count[((FIRST ? token_key(a, (int)i) : a.key_in[i]) >> a.shift) & mask], 1u);
     }
     __syncthreads();
-    if (tid < DIGITS)
-        a.count[(int64_t)tid * a.tiles + blockIdx.x] = count[tid];
+    for (int d = tid; d < DIGITS; d += THREADS)
+        a.count[(int64_t)blockIdx.x * DIGITS + d] = count[d];
 }
 // One pass: each pair to its place.
-template <bool FIRST>
-__global__ __launch_bounds__(SORT_THREADS) void sort_scatter_kernel(SortArgs a)
+template <int THREADS, bool FIRST>
+__global__ __launch_bounds__(THREADS) void sort_scatter_kernel(SortArgs a)
 {
-    __shared__ SortShared s;
+    __shared__ SortShared<THREADS> s;
+    __shared__ uint32_t part[2][THREADS > DIGITS ? THREADS : DIGITS];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int i0 = (int)blockIdx.x * SORT_TILE, items = imin(a.M - i0, SORT_TILE);
+    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * SORT_PER);
+    const int items = (int)(a.M - i0 < THREADS * SORT_PER ? a.M - i0 : THREADS * SORT_PER), per = wave_items<THREADS>(items);
     uint32_t key[SORT_PER], at[SORT_PER], place[SORT_PER];
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r) {
-        const int i = sort_item(wave, lane, r);
-        key[r] = i < items ? (FIRST ? token_key(a, i0 + i) : a.key_in[i0 + i]) : 0;
+        const int i = sort_item(wave, lane, r, per);
+        key[r] = i < items ? (FIRST ? token_key(a, (int)(i0 + i)) : a.key_in[i0 + i]) : 0;
         at[r] = i < items ? (FIRST ? (uint32_t)(i0 + i) : a.at_in[i0 + i]) : 0;
     }
     // where this workgroup's first pair of each digit goes: behind all pairs of
     // smaller digits, and those of its digit in the workgroups before
-    constexpr int PARTS = SORT_THREADS / DIGITS;
-    const int d = tid / PARTS, part = tid % PARTS;
-    uint32_t all = 0, before = 0;
-    const uint32_t *row = a.count + (int64_t)d * a.tiles;
-    for (int b = part; b < a.tiles; b += PARTS) {
-        const uint32_t c = row[b];
-        all += c;
-        before += b < (int)blockIdx.x ? c : 0;
+    constexpr int SPLIT = THREADS > DIGITS ? THREADS / DIGITS : 1;  // threads that share a digit's counts
+    for (int q = tid; q < DIGITS * SPLIT; q += THREADS) {
+        const int d = q % DIGITS;
+        part[0][q] = part[1][q] = 0;
+        if (d >> a.bits)  // not a digit
+            continue;
+        uint32_t all = 0, before = 0;
+#pragma unroll 8
+        for (int b = q / DIGITS; b < a.tiles; b += SPLIT) {
+            const uint32_t c = a.count[(int64_t)b * DIGITS + d];
+            all += c;
+            before += b < (int)blockIdx.x ? c : 0;
+        }
+        part[0][q] = all, part[1][q] = before;
     }
-#pragma unroll
-    for (int o = 1; o < PARTS; o <<= 1) {
-        all += __shfl_xor(all, o);
-        before += __shfl_xor(before, o);
-    }
-    uint32_t upto = part == PARTS - 1 ? all : 0;
-    const uint32_t own = upto;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t x = __shfl_up(upto, o);
-        upto += lane >= o ? x : 0;
-    }
-    if (lane == 63)
-        s.wave_sum[wave] = upto;
     __syncthreads();
-    uint32_t base = upto - own + before;
-    for (int w = 0; w < wave; ++w)
-        base += s.wave_sum[w];
-    if (part == PARTS - 1)
-        s.base[d] = base;
-    __syncthreads();
-    sort_places(s, key, items, a.shift, place);
+    constexpr int EACH = DIGITS > THREADS ? DIGITS / THREADS : 1;  // consecutive digits of a thread
+    uint32_t all[EACH], before[EACH], sum = 0;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int d = tid * EACH + k;
+        all[k] = before[k] = 0;
+        if (d < DIGITS)
+            for (int q = d; q < DIGITS * SPLIT; q += DIGITS)
+                all[k] += part[0][q], before[k] += part[1][q];
+        sum += all[k];
+    }
+    uint32_t base = sum_before<THREADS>(sum, s.wave_sum);
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        if (tid * EACH + k < DIGITS)
+            s.base[tid * EACH + k] = base + before[k];
+        base += all[k];
+    }
+    sort_places<THREADS>(s, key, items, a.shift, a.bits, place);
     // (behind sort_places wave_count[0][d] is the digit's first place in the workgroup)
 #pragma unroll
     for (int r = 0; r < SORT_PER; ++r)
-        if (sort_item(wave, lane, r) < items) {
-            const uint32_t dig = (key[r] >> a.shift) & (DIGITS - 1);
-            const uint32_t to = s.base[dig] + place[r] - s.wave_count[0][dig];
+        if (sort_item(wave, lane, r, per) < items) {
+            const uint32_t d = (key[r] >> a.shift) & ((1u << a.bits) - 1);
+            const uint32_t to = s.base[d] + place[r] - s.wave_count[0][d];
             a.key[to] = key[r];
             a.at[to] = at[r];
         }
@@ -380,26 +436,34 @@ __global__ __launch_bounds__(WALK_THREADS) void embedding_walk_kernel(WalkArgs a
     int v = v0;
     const auto part = [&](float *to) {
         float *dst = to + (int64_t)piece * a.K + c;
-#pragma unroll
-        for (int e = 0; e < VEC<E>; ++e)
-            if (e < n)
-                dst[e] = acc[e];
-    };
-    const auto close = [&] {  // row v ends
-        if (v == open) {
-            part(a.head);
-        } else {
-            E x[VEC<E>];
+        if (n == VEC<E>)
+            __builtin_memcpy(dst, acc, sizeof acc);
+        else
 #pragma unroll
             for (int e = 0; e < VEC<E>; ++e)
-                x[e] = some ? (E)(acc[e] * a.scale) : (E)0.0f;
-            store_row(x, dW + (int64_t)v * a.lddw, n);
-        }
+                if (e < n)
+                    dst[e] = acc[e];
+    };
+    const auto close_before = [&](int k) {  // rows v .. k - 1 end
+        if (v < k && (some || v == open)) {
+            if (v == open) {
+                part(a.head);
+            } else {
+                E x[VEC<E>];
 #pragma unroll
-        for (int e = 0; e < VEC<E>; ++e)
-            acc[e] = 0.0f;
-        some = false;
-        ++v;
+                for (int e = 0; e < VEC<E>; ++e)
+                    x[e] = (E)(acc[e] * a.scale);
+                store_row(x, dW + (int64_t)v * a.lddw, n);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC<E>; ++e)
+                acc[e] = 0.0f;
+            some = false;
+            ++v;
+        }
+        const E zero[VEC<E>] = {};
+        for (; v < k; ++v)
+            store_row(zero, dW + (int64_t)v * a.lddw, n);
     };
     bool done = false;
     for (int b = i0; b < i1 && !done; b += 64) {
@@ -418,8 +482,7 @@ __global__ __launch_bounds__(WALK_THREADS) void embedding_walk_kernel(WalkArgs a
             for (int q = 0; q < AHEAD; ++q)
                 if (u + q < live) {
                     const int k = __builtin_amdgcn_readlane((int)keys, u + q);
-                    while (v < k)
-                        close();
+                    close_before(k);
 #pragma unroll
                     for (int e = 0; e < VEC<E>; ++e)
                         acc[e] += (float)x[q][e];
@@ -428,8 +491,7 @@ __global__ __launch_bounds__(WALK_THREADS) void embedding_walk_kernel(WalkArgs a
         }
         done = live < cnt;
     }
-    while (v < v1)
-        close();
+    close_before(v1);
     if (some)  // row v goes on in the next piece
         part(a.tail);
 }
@@ -437,7 +499,7 @@ __global__ __launch_bounds__(WALK_THREADS) void embedding_walk_kernel(WalkArgs a
 // A row that several pieces share: their parts in order.  A workgroup takes
 // JOIN pieces' ends; a wave adds up a row of few parts by itself, all of them a
 // long one, in WALK_WAVES runs of parts.
-constexpr int JOIN = 16, LONG_ROW = 32;
+constexpr int JOIN = 4, LONG_ROW = 16;
 template <typename E>
 __global__ __launch_bounds__(WALK_THREADS) void embedding_join_kernel(WalkArgs a)
 {
@@ -450,9 +512,16 @@ __global__ __launch_bounds__(WALK_THREADS) void embedding_join_kernel(WalkArgs a
     const int2 mine = lane < JOIN && end < a.pieces ? a.carried[end] : make_int2(-1, 0);
     const auto add = [&](float (&acc)[VEC<E>], const float *from, int64_t piece) {
         const float *p = from + piece * a.K + c;
+        float x[VEC<E>] = {};
+        if (n == VEC<E>)
+            __builtin_memcpy(x, p, sizeof x);
+        else
+#pragma unroll
+            for (int e = 0; e < VEC<E>; ++e)
+                x[e] = e < n ? p[e] : 0.0f;
 #pragma unroll
         for (int e = 0; e < VEC<E>; ++e)
-            acc[e] += e < n ? p[e] : 0.0f;
+            acc[e] += x[e];
     };
     const auto finish = [&](const float (&acc)[VEC<E>], int row) {
         E x[VEC<E>];
@@ -522,11 +591,13 @@ int lookup(const int64_t *tokens, const void *W, void *Y, int64_t M, int64_t V, 
     LookArgs a = {tokens, W, Y, M, V, K, V > 1 ? ldw : 0, M > 1 ? ldy : 0, 0, scale};
     a.segments = (int)cdiv(K, 64 * LOOK_STEPS * VEC<E>);
     const int64_t grid = std::min(cdiv(M * a.segments, LOOK_THREADS / 64), (int64_t)1 << 20);
-    return launch(embedding_kernel<E>, grid, LOOK_THREADS, stream, a) ? TG_OK : TG_ERR_LAUNCH;
+    const bool ok = M * K * (int64_t)sizeof(E) >= NT_BYTES ? launch(embedding_kernel<E, true>, grid, LOOK_THREADS, stream, a)
+                                                           : launch(embedding_kernel<E, false>, grid, LOOK_THREADS, stream, a);
+    return ok ? TG_OK : TG_ERR_LAUNCH;
 }
 
 struct Plan {
-    int passes, tiles;       // of the sort
+    int passes, bits, tiles, threads;  // of the sort
     int piece, pieces;       // of the walk
     int64_t key, at, key2, at2, count, carried, head, tail, bytes;  // offsets in the workspace
 };
@@ -536,17 +607,25 @@ int validate(int64_t M, int64_t V, int64_t K)
         return TG_ERR_INVALID_ARG;
     return M >= LIMIT || V >= LIMIT || K >= LIMIT || M + V >= LIMIT || (M + V) * K >= MOST ? TG_ERR_TOO_LARGE : TG_OK;
 }
-// Pieces of 32 items where there are few, so that some 32768 waves share the work; of
-// up to 256 where there are many, as every piece has room for two rows of fp32 sums.
+// Pieces of 32 items where there are few, of 64 otherwise (with gradient: 333 tokens
+// on 50001×1000 fp32 70 us with 32, 80 with 64; 65536 on 32000×2048 fp16 238 and 219,
+// where every piece leaves two rows of fp32 sums; 128 are slower everywhere).  More
+// only to keep the launch within its limit.
 Plan make_plan(int64_t M, int64_t V, int64_t K)
 {
     Plan p = {};
-    for (int64_t keys = V + 1; keys > 1; keys = cdiv(keys, DIGITS))
-        ++p.passes;
-    p.tiles = (int)cdiv(M, SORT_TILE);
+    int bits = 1;
+    while ((int64_t)1 << bits < V + 1)
+        ++bits;
+    p.passes = (int)cdiv(bits, DIGIT_BITS);
+    p.bits = (int)cdiv(bits, p.passes);
+    // small workgroups spread a short sort over the chip; every workgroup reads all
+    // workgroups' counts, so that a long one takes large ones
+    p.threads = M <= SORT_SMALL || M > 128 * FEW * SORT_PER ? MANY : FEW;
+    p.tiles = (int)cdiv(M, p.threads * SORT_PER);
     const int64_t segments = cdiv(K, 64 * 4);  // of the widest type
-    p.piece = 32;
-    while (p.piece < 256 && cdiv(M + V, p.piece) * segments > 65536)
+    p.piece = cdiv(M + V, 32) * segments <= 16384 ? 32 : 64;
+    while (p.piece < 256 && cdiv(M + V, p.piece) * segments > (int64_t)1 << 22)
         p.piece *= 2;
     p.pieces = (int)cdiv(M + V, p.piece);
     int64_t used = 0;
@@ -589,21 +668,32 @@ int gradient(const int64_t *tokens, const void *dY, void *dW, int64_t M, int64_t
     char *const base = reinterpret_cast<char *>(ws);
     const auto words = [&](int64_t at) { return reinterpret_cast<uint32_t *>(base + at); };
     bool ok = true;
-    SortArgs s = {tokens, nullptr, nullptr, words(p.key), words(p.at), nullptr, (int)M, (int)V, padding, p.tiles, 0, p.passes};
+    SortArgs s = {};
+    s.tokens = tokens, s.M = (int)M, s.V = (int)V, s.padding = padding;
+    s.key = words(p.key), s.at = words(p.at);
+    s.tiles = p.tiles, s.bits = p.bits, s.passes = p.passes;
     if (p.tiles == 1) {
-        ok = launch(sort_small_kernel, 1, SORT_THREADS, stream, s);
+        ok = launch(sort_small_kernel, 1, MANY, stream, s);
     } else if (p.tiles > 1) {
         s.count = words(p.count);
+        const auto pass = [&](auto threads, auto first) {
+            constexpr int T = decltype(threads)::value;
+            constexpr bool F = decltype(first)::value;
+            return launch(sort_count_kernel<T, F>, p.tiles, T, stream, s) &&
+                   launch(sort_scatter_kernel<T, F>, p.tiles, T, stream, s);
+        };
         // the pairs go back and forth so that the last pass ends in (key, at)
         for (int q = 0; ok && q < p.passes; ++q) {
             const bool to_first = (p.passes - 1 - q) % 2 == 0;
             s.key = words(to_first ? p.key : p.key2), s.at = words(to_first ? p.at : p.at2);
             s.key_in = words(to_first ? p.key2 : p.key), s.at_in = words(to_first ? p.at2 : p.at);
-            s.shift = 8 * q;
-            ok = q == 0 ? launch(sort_count_kernel<true>, p.tiles, SORT_THREADS, stream, s) &&
-                              launch(sort_scatter_kernel<true>, p.tiles, SORT_THREADS, stream, s)
-                        : launch(sort_count_kernel<false>, p.tiles, SORT_THREADS, stream, s) &&
-                              launch(sort_scatter_kernel<false>, p.tiles, SORT_THREADS, stream, s);
+            s.shift = p.bits * q;
+            if (p.threads == FEW)
+                ok = q == 0 ? pass(std::integral_constant<int, FEW>{}, std::true_type{})
+                            : pass(std::integral_constant<int, FEW>{}, std::false_type{});
+            else
+                ok = q == 0 ? pass(std::integral_constant<int, MANY>{}, std::true_type{})
+                            : pass(std::integral_constant<int, MANY>{}, std::false_type{});
         }
     }
     WalkArgs w = {};

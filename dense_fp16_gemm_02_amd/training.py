@@ -14,6 +14,7 @@ Argument marshalling, checks and autograd glue only, as in the package.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import math
@@ -196,79 +197,89 @@ def tg_adamw(tensors, config: tg_adamw_config, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ torch
-def _on_device(dev, fn, args, what):
-    """fn(*args) with dev as the current device."""
+@functools.lru_cache(maxsize=None)
+def _cuda():
+    """torch's current stream (as an address) and current device by index: what
+    torch.cuda.current_stream and current_device look up, without the objects around
+    it (2 of some 10 us of a small call)."""
     import torch
 
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args)
+    return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _call(index, fn, args, what):
+    """fn(*args, stream) on torch's current stream of device ``index``, as the current device."""
+    stream, device = _cuda()
+    if device() == index:
+        st = fn(*args, stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args)
+        import torch
+
+        with torch.cuda.device(index):
+            st = fn(*args, stream(index))
     if st:
         raise _pkg().TgError(st, what)
 
 
 @functools.lru_cache(maxsize=1024)
-def _grouped_size(product, a_aligned, b_aligned, M, E, N, K, lda, ldb, w_stride):
-    """Workspace bytes; of the pointers only their alignment counts."""
-    return max(0, _lib().tg_grouped_workspace_bytes(product, 4096 if a_aligned else 4098, 4096 if b_aligned else 4098,
-                                                    M, E, N, K, lda, ldb, w_stride))
-
-
-def _grouped_call(product, A, B, ends, D, N, K, ldd, d_stride=0):
-    """Workspace, stream and device around one product of the library."""
+def _grouped_plan(product, dtype, a_aligned, b_aligned, M, E, N, K, lda, ldb, w_stride):
+    """Entry point and workspace bytes; of the pointers only their alignment counts."""
     import torch
 
+    name = ("tg_grouped_", "tg_grouped_dx_", "tg_grouped_dw_")[product] + ("f16" if dtype == torch.float16 else "bf16")
+    size = _lib().tg_grouped_workspace_bytes(product, 4096 if a_aligned else 4098, 4096 if b_aligned else 4098, M, E,
+                                             N, K, lda, ldb, w_stride)
+    return getattr(_lib(), name), max(0, size)
+
+
+def _grouped_call(product, A, B, lda, ldb, w_stride, ends, D, N, K, ldd, d_stride=0):
+    """Workspace, stream and device around one product of the library."""
+    a, b = A.data_ptr(), B.data_ptr()
     M, E = A.shape[0], ends.shape[0]
-    dw = product == TG_GROUPED_DW
-    lda = _row_stride(A, "X" if product == TG_GROUPED_Y else "dY", A.shape[1])
-    if dw:
-        ldb, w_stride = _row_stride(B, "X", K), 0
-    else:
-        ldb, w_stride = _weight_strides(B)
-    a, b, dev = A.data_ptr(), B.data_ptr(), A.device
-    size = _grouped_size(product, a % 16 == 0, b % 16 == 0, M, E, N, K, lda, ldb, w_stride)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    name = ("tg_grouped_", "tg_grouped_dx_", "tg_grouped_dw_")[product] + ("f16" if A.dtype == torch.float16 else "bf16")
-    tail = (ldd, d_stride) if dw else (w_stride, ldd)
-    _on_device(dev, getattr(_lib(), name),
-               (a, b, ends.data_ptr(), D.data_ptr(), M, E, N, K, lda, ldb, *tail, _p(ws), size,
-                torch.cuda.current_stream(dev).cuda_stream),
-               "grouped_linear (backward)" if product else "grouped_linear")
+    fn, size = _grouped_plan(product, A.dtype, a % 16 == 0, b % 16 == 0, M, E, N, K, lda, ldb, w_stride)
+    ws = _bytes(A, size) if size else None
+    last = (ldd, d_stride) if product == TG_GROUPED_DW else (w_stride, ldd)
+    _call(A.get_device(), fn, (a, b, ends.data_ptr(), D.data_ptr(), M, E, N, K, lda, ldb, *last, _p(ws), size),
+          "grouped_linear (backward)" if product else "grouped_linear")
+
+
+def _bytes(like, size):
+    """A workspace on the device of ``like``."""
+    import torch
+
+    return torch.empty(size, dtype=torch.uint8, device=like.device)
 
 
 def _weight_strides(W):
     """Row and expert strides of the weights; experts may share memory, rows may not."""
     E, N, K = W.shape
-    if K > 1 and W.stride(2) != 1:
+    stride = W.stride()
+    if K > 1 and stride[2] != 1:
         raise ValueError("W must have a contiguous last dimension")
-    ldw = W.stride(1) if N > 1 else max(K, 1)
+    ldw = stride[1] if N > 1 else max(K, 1)
     if ldw < K:
         raise ValueError(f"W has row stride {ldw} < row length {K}; pass a tensor with non-overlapping rows")
-    return ldw, W.stride(0) if E > 1 else N * ldw
+    return ldw, stride[0] if E > 1 else N * ldw
 
 
-def _grouped_forward(X, W, ends):
-    import torch
-
+def _grouped_forward(X, W, ends, strides):
     N, K = W.shape[1:]
-    Y = torch.empty((X.shape[0], N), dtype=X.dtype, device=X.device)
-    _grouped_call(TG_GROUPED_Y, X, W, ends, Y, N, K, max(N, 1))
+    Y = X.new_empty((X.shape[0], N))
+    _grouped_call(TG_GROUPED_Y, X, W, *strides, ends, Y, N, K, max(N, 1))
     return Y
 
 
-def _grouped_backward(X, W, ends, dY, need_x, need_w):
-    import torch
-
+def _grouped_backward(X, W, ends, dY, strides, need_x, need_w):
     N, K = W.shape[1:]
+    ldx, ldw, w_stride = strides
+    ldy = _row_stride(dY, "dY", N)
     dX = dW = None
     if need_x:
-        dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-        _grouped_call(TG_GROUPED_DX, dY, W, ends, dX, N, K, max(K, 1))
+        dX = X.new_empty(X.shape)
+        _grouped_call(TG_GROUPED_DX, dY, W, ldy, ldw, w_stride, ends, dX, N, K, max(K, 1))
     if need_w:
-        dW = torch.empty(W.shape, dtype=W.dtype, device=W.device)
-        _grouped_call(TG_GROUPED_DW, dY, X, ends, dW, N, K, max(K, 1), N * max(K, 1))
+        dW = W.new_empty(W.shape)
+        _grouped_call(TG_GROUPED_DW, dY, X, ldy, ldx, 0, ends, dW, N, K, max(K, 1), N * max(K, 1))
     return dX, dW
 
 
@@ -297,16 +308,18 @@ def _grouped_function():
 
     class GroupedLinear(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, X, W, ends):
+        def forward(ctx, X, W, ends, strides):
             ctx.save_for_backward(X, W, ends)
-            return _grouped_forward(X, W, ends)
+            ctx.strides = strides
+            return _grouped_forward(X, W, ends, strides)
 
         @staticmethod
         def backward(ctx, dY):
             X, W, ends = ctx.saved_tensors
             _refuse_modes("grouped_linear (backward)", dY)
             gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
-            return (*gradients(X, W, ends, _rows(dY), ctx.needs_input_grad[0], ctx.needs_input_grad[1]), None)
+            need = ctx.needs_input_grad
+            return (*gradients(X, W, ends, _rows(dY), ctx.strides, need[0], need[1]), None, None)
 
     return GroupedLinear
 
@@ -352,13 +365,12 @@ def grouped_linear(X, W, ends):
         raise ValueError(f"K mismatch: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
     if ends.shape[0] != W.shape[0]:
         raise ValueError(f"{ends.shape[0]} ends for {W.shape[0]} experts")
-    _row_stride(X, "X", X.shape[1])
-    _weight_strides(W)
+    strides = (_row_stride(X, "X", X.shape[1]), *_weight_strides(W))
     _refuse_modes("grouped_linear", X, W)
     ends = ends.contiguous()
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
-        return _grouped_function().apply(X, W, ends)
-    return _grouped_forward(X, W, ends)
+        return _grouped_function().apply(X, W, ends, strides)
+    return _grouped_forward(X, W, ends, strides)
 
 
 @functools.lru_cache(maxsize=None)
@@ -368,14 +380,11 @@ def _embedding_names():
     return {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 
 
-def _embedding_forward(tokens, W, scale):
-    import torch
-
-    (V, K), M, dev = W.shape, tokens.numel(), W.device
-    Y = torch.empty((*tokens.shape, K), dtype=W.dtype, device=dev)
-    _on_device(dev, getattr(_lib(), "tg_embedding_" + _embedding_names()[W.dtype]),
-               (tokens.data_ptr(), W.data_ptr(), Y.data_ptr(), M, V, K, _row_stride(W, "W", K), max(K, 1), scale,
-                torch.cuda.current_stream(dev).cuda_stream), "embedding")
+def _embedding_forward(tokens, W, ldw, scale):
+    V, K = W.shape
+    Y = W.new_empty((*tokens.shape, K))
+    _call(W.get_device(), getattr(_lib(), "tg_embedding_" + _embedding_names()[W.dtype]),
+          (tokens.data_ptr(), W.data_ptr(), Y.data_ptr(), tokens.numel(), V, K, ldw, max(K, 1), scale), "embedding")
     return Y
 
 
@@ -385,16 +394,14 @@ def _embedding_size(M, V, K):
 
 
 def _embedding_backward(tokens, dY, V, scale, padding):
-    import torch
-
-    M, K, dev = tokens.numel(), dY.shape[-1], dY.device
+    M, K = tokens.numel(), dY.shape[-1]
     dY = _rows(dY.reshape(M, K))
-    dW = torch.empty((V, K), dtype=dY.dtype, device=dev)
+    dW = dY.new_empty((V, K))
     size = _embedding_size(M, V, K)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _on_device(dev, getattr(_lib(), "tg_embedding_bwd_" + _embedding_names()[dY.dtype]),
-               (tokens.data_ptr(), dY.data_ptr(), dW.data_ptr(), M, V, K, _row_stride(dY, "dY", K), max(K, 1), scale,
-                padding, ws.data_ptr(), size, torch.cuda.current_stream(dev).cuda_stream), "embedding (backward)")
+    ws = _bytes(dY, size)
+    _call(dY.get_device(), getattr(_lib(), "tg_embedding_bwd_" + _embedding_names()[dY.dtype]),
+          (tokens.data_ptr(), dY.data_ptr(), dW.data_ptr(), M, V, K, _row_stride(dY, "dY", K), max(K, 1), scale, padding,
+           ws.data_ptr(), size), "embedding (backward)")
     return dW
 
 
@@ -416,17 +423,17 @@ def _embedding_function():
 
     class Embedding(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, tokens, W, scale, padding):
+        def forward(ctx, tokens, W, ldw, scale, padding):
             ctx.save_for_backward(tokens)
             ctx.how = W.shape[0], scale, padding
-            return _embedding_forward(tokens, W, scale)
+            return _embedding_forward(tokens, W, ldw, scale)
 
         @staticmethod
         def backward(ctx, dY):
             tokens, = ctx.saved_tensors
             _refuse_modes("embedding (backward)", dY)
             gradient = Gradient.apply if torch.is_grad_enabled() else _embedding_backward
-            return None, gradient(tokens, dY, *ctx.how), None, None
+            return None, gradient(tokens, dY, *ctx.how), None, None, None
 
     return Embedding
 
@@ -467,12 +474,12 @@ def embedding(tokens, W, scale: float = 1.0, padding_idx: int | None = None):
         raise ValueError("scale must be a finite fp32 number")
     if padding_idx is not None and not 0 <= padding_idx < V:
         raise ValueError(f"padding_idx must be in [0, {V})")
-    _row_stride(W, "W", K)
+    ldw = _row_stride(W, "W", K)
     _refuse_modes("embedding", W)
     tokens = tokens.contiguous()
     if torch.is_grad_enabled() and W.requires_grad:
-        return _embedding_function().apply(tokens, W, float(scale), -1 if padding_idx is None else padding_idx)
-    return _embedding_forward(tokens, W, float(scale))
+        return _embedding_function().apply(tokens, W, ldw, float(scale), -1 if padding_idx is None else padding_idx)
+    return _embedding_forward(tokens, W, ldw, float(scale))
 
 
 @functools.lru_cache(maxsize=None)
@@ -480,6 +487,14 @@ def _adamw_types():
     import torch
 
     return {torch.float32: TG_ADAMW_F32, torch.float16: TG_ADAMW_F16, torch.bfloat16: TG_ADAMW_BF16}
+
+
+@functools.lru_cache(maxsize=None)
+def _adamw_tools():
+    import torch
+    from torch.autograd import forward_ad
+
+    return forward_ad, torch.autograd.graph.increment_version
 
 
 def _same_dtype(ts, name, allowed):
@@ -520,6 +535,8 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
     dev = params[0].device
     if not params[0].is_cuda:
         raise ValueError("params must be GPU tensors")
+    if any([t.is_sparse for t in grads]):
+        raise TypeError("grads must be dense")
     f32, half = torch.float32, {torch.float16, torch.bfloat16}
     p_type = _same_dtype(params, "params", {f32} | half)
     g_type = _same_dtype(grads, "grads", {f32} | half if p_type == f32 else {p_type})
@@ -533,7 +550,8 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
         if p_type != f32:
             raise ValueError("copies are for float32 parameters")
         copy_type = _same_dtype(lists[-1], "copies", half)
-    _refuse_modes(what, *params, *grads)
+    dual_level, increment_version = _adamw_tools()
+    _refuse_modes(what, *(params + grads if dual_level._current_level >= 0 else ()))
     index, sizes = dev.index, [p.numel() for p in params]
     blocks = [(n + TG_ADAMW_BLOCK - 1) // TG_ADAMW_BLOCK for n in sizes] if scales else None
     for k, x in enumerate(lists):
@@ -541,14 +559,14 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
         if [t.numel() for t in x] != want:
             raise ValueError("gradients, moments and copies must have as many elements as their parameter"
                              + (f", scales one for each {TG_ADAMW_BLOCK} of them" if scales else ""))
-        if not all(t.is_contiguous() for t in x):
+        if not all([t.is_contiguous() for t in x]):
             raise ValueError("parameters, gradients, moments and copies must be contiguous")
-        if not all(t.is_cuda and t.get_device() == index for t in x):
+        if {t.get_device() for t in x} != {index}:
             raise ValueError("all tensors must be on one GPU")
-    for g, p in zip(grads, params):
-        if g.shape != p.shape:
-            raise ValueError(f"a gradient of shape {tuple(g.shape)} for a parameter of shape {tuple(p.shape)}")
-    if torch.is_grad_enabled() and any(t.requires_grad and not t.is_leaf for x in lists[:1] + lists[2:] for t in x):
+    if [g.shape for g in grads] != [p.shape for p in params]:
+        raise ValueError("a gradient has another shape than its parameter")
+    written = lists[:1] + lists[2:]
+    if torch.is_grad_enabled() and not all([t.is_leaf for x in written for t in x if t.requires_grad]):
         raise ValueError("params, moments and copies that are results of autograd cannot be updated in place")
     types = _adamw_types()
     b1, b2 = betas
@@ -558,14 +576,15 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
                              types[copy_type] if copy_type else 0, bits)
     if g_scale is not None and not isinstance(g_scale, torch.Tensor):
         raise TypeError("grad_scale must be a tensor")
-    where = [[t.data_ptr() for t in x] for x in lists]
-    none = [None] * count
-    table = (tg_adamw_tensor * count)(*zip(where[0], where[1], where[2], where[3], *(where[4:6] if scales else (none, none)),
-                                           where[-1] if copies is not None else none, sizes))
-    _on_device(dev, _lib().tg_adamw, (ctypes.addressof(table), count, ctypes.byref(config),
-                                      torch.cuda.current_stream(dev).cuda_stream), what)
-    for x in lists[:1] + lists[2:]:
-        torch.autograd.graph.increment_version([t for t in x if not t.is_inference()])
+    # tg_adamw_tensor structures: eight words each, a word of all of them at a time
+    table = array.array("q", bytes(64 * count))
+    for word, x in zip((0, 1, 2, 3, 4, 5) if scales else (0, 1, 2, 3), lists):
+        table[word::8] = array.array("q", [t.data_ptr() for t in x])
+    if copies is not None:
+        table[6::8] = array.array("q", [t.data_ptr() for t in lists[-1]])
+    table[7::8] = array.array("q", sizes)
+    _call(index, _lib().tg_adamw, (table.buffer_info()[0], count, ctypes.byref(config)), what)
+    increment_version([t for x in written for t in x])
 
 
 def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

@@ -287,6 +287,16 @@ def test_parameters_that_require_grad_and_versions():
         tg.adamw([p * 2], [p.grad], [m], [v], 1)
 
 
+def test_inference_tensors():
+    with torch.inference_mode():
+        p, g, m, v = make([(40,)], torch.float32, torch.float32)
+        want = clones(p, m, v)
+        tg.adamw(p, g, m, v, 3, **HOW)
+    q = [[t + 0 for t in x] for x in want]  # ordinary tensors
+    tg.adamw(q[0], g, q[1], q[2], 3, **HOW)
+    assert torch.equal(p[0], q[0][0]) and torch.equal(m[0], q[1][0]) and torch.equal(v[0], q[2][0])
+
+
 def test_shared_memory_is_refused():
     p, g, m, v = make([(100,), (100,)], torch.float32, torch.float32)
     base = torch.zeros(150, device="cuda")
