@@ -21,85 +21,6 @@ namespace {
 using namespace pt;
 
 // ------------------------------------------------------------------- groups
-// Where group idx's rows end: expert idx, or the rows behind all of them (idx >= E).
-__device__ inline int group_end(const int64_t *ends, int E, int M, int idx)
-{
-    if (idx >= E)
-        return M;
-    const int64_t x = ends[idx];
-    return (int)(x < 0 ? 0 : x > M ? M : x);
-}
-// 64 groups from `base` on, one to a lane: first row, end, and the tile rows up to
-// and with it.  `row` and `tiles`: the end and the count of the groups before.
-template <int BM>
-__device__ inline void scan_groups(const int64_t *ends, int E, int M, int base, int lane, int row, int tiles,
-                                   int &lo, int &hi, int &upto)
-{
-    hi = imax(group_end(ends, E, M, base + lane), row);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int x = __shfl_up(hi, o);
-        hi = lane >= o ? imax(hi, x) : hi;
-    }
-    lo = __shfl_up(hi, 1);
-    lo = lane == 0 ? row : lo;
-    upto = (hi - lo + BM - 1) / BM;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int x = __shfl_up(upto, o);
-        upto += lane >= o ? x : 0;
-    }
-    upto += tiles;
-}
-struct Tile2d {
-    int e, lo, rows;  // group (E: the rows behind), its first row and their number
-    int tm, tn;
-};
-template <int BM>
-__device__ inline bool find_tile(const int64_t *ends, int E, int M, int tiles_n, Tile2d &t)
-{
-    const int lane = lane_id();
-    int lo, hi, upto, row = 0, tiles = 0;
-    for (int base = 0; base <= E; base += 64) {
-        scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
-        row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
-    }
-    if ((int64_t)blockIdx.x >= (int64_t)tiles * tiles_n)
-        return false;
-    const int logical = xcd_contiguous(blockIdx.x, tiles * tiles_n), tile_row = logical / tiles_n;
-    int base = 0;
-    if (E >= 64) {  // otherwise the registers still hold the only scan
-        row = tiles = 0;
-        for (;; base += 64) {
-            scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
-            if (__builtin_amdgcn_readlane(upto, 63) > tile_row)
-                break;
-            row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
-        }
-    }
-    const int at = uniform(__builtin_ctzll(__ballot(upto > tile_row)));
-    t.e = base + at;
-    t.lo = __builtin_amdgcn_readlane(lo, at);
-    t.rows = __builtin_amdgcn_readlane(hi, at) - t.lo;
-    const int rows_tiles = (t.rows + BM - 1) / BM;
-    const int first = __builtin_amdgcn_readlane(upto, at) - rows_tiles;
-    grouped_tile<4>(logical - first * tiles_n, rows_tiles, tiles_n, t.tm, t.tn);
-    return true;
-}
-// Expert e's rows.
-__device__ inline void find_rows(const int64_t *ends, int M, int e, int &lo, int &rows)
-{
-    const int lane = lane_id();
-    int before = 0;
-    for (int i = lane; i < e; i += 64)
-        before = imax(before, group_end(ends, e, M, i));
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        before = imax(before, __shfl_xor(before, o));
-    lo = uniform(before);
-    rows = uniform(imax(group_end(ends, e + 1, M, e) - before, 0));
-}
-
 // Workgroup id → tile where tiles differ in length, as those of weights with few
 // and many rows do: each XCD takes 32 consecutive tiles (one for each of its compute
 // units) of every 256, so that all eight work on the same experts at a time.  (With one
@@ -114,6 +35,93 @@ __host__ __device__ constexpr int xcd_chunks(int bid, int total)
         return whole + xcd_contiguous(bid - whole, total - whole);
     const int xcd = bid % NUM_XCD, local = bid / NUM_XCD;
     return (local / EACH * NUM_XCD + xcd) * EACH + local % EACH;
+}
+
+// Inclusive scan of values >= 0 over a wave, in DPP moves: within rows of 16 lanes,
+// then each row's last value on to the rows behind it (0 comes in from outside).
+template <typename Op>
+__device__ inline int scan64(int x, Op op)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));  // row_shr:1, 2, 4, 8
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));  // row_bcast:15 to rows 1 and 3
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));  // row_bcast:31 to rows 2 and 3
+#endif
+    return x;
+}
+// Where expert idx's rows end (past the experts: 0, which changes nothing).
+__device__ inline int group_end(const int64_t *ends, int E, int M, int idx)
+{
+    if (idx >= E)
+        return 0;
+    const int64_t x = ends[idx];
+    return (int)(x < 0 ? 0 : x > M ? M : x);
+}
+// 64 experts from `base` on, one to a lane: first row, end, and the tile rows up to
+// and with it.  `row` and `tiles`: the end and the tile rows of the experts before.
+template <int BM>
+__device__ inline void scan_groups(const int64_t *ends, int E, int M, int base, int lane, int row, int tiles,
+                                   int &lo, int &hi, int &upto)
+{
+    hi = scan64(imax(group_end(ends, E, M, base + lane), row), [](int x, int y) { return imax(x, y); });
+    lo = __shfl_up(hi, 1);
+    lo = lane == 0 ? row : lo;
+    upto = tiles + scan64((hi - lo + BM - 1) / BM, [](int x, int y) { return x + y; });
+}
+struct Tile2d {
+    int e, lo, rows;  // expert (E: the rows behind), its first row and their number
+    int tm, tn;
+};
+template <int BM>
+__device__ inline bool find_tile(const int64_t *ends, int E, int M, int tiles_n, Tile2d &t)
+{
+    const int lane = lane_id();
+    int lo, hi, upto, row = 0, tiles = 0;
+    for (int base = 0; base < E; base += 64) {
+        scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
+        row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
+    }
+    const int all = tiles + (M - row + BM - 1) / BM;  // with the rows behind
+    if ((int64_t)blockIdx.x >= (int64_t)all * tiles_n)
+        return false;
+    const int logical = xcd_chunks(blockIdx.x, all * tiles_n), tile_row = logical / tiles_n;
+    int first = tiles;
+    t.e = E, t.lo = row, t.rows = M - row;
+    if (tile_row < tiles) {
+        int base = 0;
+        if (E > 64) {  // otherwise the registers still hold the only scan
+            row = tiles = 0;
+            for (;; base += 64) {
+                scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
+                if (__builtin_amdgcn_readlane(upto, 63) > tile_row)
+                    break;
+                row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
+            }
+        }
+        const int at = uniform(__builtin_ctzll(__ballot(upto > tile_row)));
+        t.e = base + at;
+        t.lo = __builtin_amdgcn_readlane(lo, at);
+        t.rows = __builtin_amdgcn_readlane(hi, at) - t.lo;
+        first = __builtin_amdgcn_readlane(upto, at) - (t.rows + BM - 1) / BM;
+    }
+    grouped_tile<4>(logical - first * tiles_n, (t.rows + BM - 1) / BM, tiles_n, t.tm, t.tn);
+    return true;
+}
+// Expert e's rows.
+__device__ inline void find_rows(const int64_t *ends, int M, int e, int &lo, int &rows)
+{
+    const int lane = lane_id();
+    int before = 0;
+    for (int i = lane; i < e; i += 64)
+        before = imax(before, group_end(ends, e, M, i));
+#pragma unroll
+    for (int o = 32; o; o >>= 1)
+        before = imax(before, __shfl_xor(before, o));
+    lo = uniform(before);
+    rows = uniform(imax(group_end(ends, e + 1, M, e) - before, 0));
 }
 
 // ------------------------------------------------------------------ products
@@ -183,6 +191,92 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     const Operand w = {reinterpret_cast<const E *>(a.w) + (int64_t)t.e * a.w_stride, a.ldw, a.w_extent};
     T::run(smem, x, w, m0, n0, a.inner, acc);
     store_tile<E, T>(smem, acc, d, a.ldd, m0, n0, t.rows, a.cols, a.vec);
+}
+
+// Y of a few rows an expert where a tile of W for each compute unit is not there:
+// 16 rows × 32 columns to a workgroup, whose eight waves take every eighth 128-K piece of
+// the sum straight from memory to registers, all loads of two pieces ahead of their
+// products, and add up in LDS at the end.  Bound by the latency of its few
+// dependent steps; TIME_FEW.
+constexpr int FEW_M = 16, FEW_N = 32, FEW_WAVES = 8, FEW_K = 128, FEW_AHEAD = 2;
+template <typename E>
+__device__ inline typename El<E>::v8 load_chunk(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    union {
+        uint32_t __attribute__((ext_vector_type(4))) u;
+        typename El<E>::v8 v;
+    } x = {};
+#if defined(__HIP_DEVICE_COMPILE__)
+    x.u = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+#else
+    (void)r, (void)off;
+#endif
+    return x.v;
+}
+template <typename E>
+__global__ __launch_bounds__(64 * FEW_WAVES) void grouped_few_kernel(RowsArgs a)
+{
+    __shared__ f32x4 sums[FEW_WAVES][FEW_N / 16][64];
+    Tile2d t;
+    if (!find_tile<FEW_M>(a.ends, a.E, a.M, a.tiles_n, t))
+        return;
+    const int m0 = t.tm * FEW_M, n0 = t.tn * FEW_N;
+    E *d = reinterpret_cast<E *>(a.d) + (int64_t)t.lo * a.ldd;
+    if (t.e >= a.E) {
+        zero_tile<E, FEW_M, FEW_N, 64 * FEW_WAVES>(d, a.ldd, m0, n0, t.rows, a.cols);
+        return;
+    }
+    const int lane = lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const auto rsrc = [](const void *p) {
+        return __builtin_amdgcn_make_buffer_rsrc((void *)uniform(reinterpret_cast<const char *>(p)), (short)0, DMA_RANGE,
+                                                 BUFFER_WORD3);
+    };
+    const auto rx = rsrc(reinterpret_cast<const E *>(a.a) + (int64_t)(t.lo + m0) * a.lda);
+    const auto rw = rsrc(reinterpret_cast<const E *>(a.w) + (int64_t)t.e * a.w_stride + (int64_t)n0 * a.ldw);
+    // rows past the last one read it again: they feed only outputs that are not stored
+    const uint32_t x_off = (uint32_t)(2 * imin(r, t.rows - 1 - m0) * a.lda);
+    uint32_t w_off[FEW_N / 16];
+    f32x4 acc[FEW_N / 16];
+#pragma unroll
+    for (int j = 0; j < FEW_N / 16; ++j) {
+        w_off[j] = (uint32_t)(2 * imin(16 * j + r, a.w_extent - 1 - n0) * a.ldw);
+        acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    for (int k0 = wave * FEW_K; k0 < a.inner; k0 += FEW_AHEAD * FEW_WAVES * FEW_K) {
+        typename El<E>::v8 x[FEW_AHEAD][FEW_K / 32], w[FEW_AHEAD][FEW_K / 32][FEW_N / 16];
+#pragma unroll
+        for (int u = 0; u < FEW_AHEAD; ++u)
+#pragma unroll
+            for (int s = 0; s < FEW_K / 32; ++s) {
+                const int k = k0 + u * FEW_WAVES * FEW_K + 32 * s + 8 * g;
+                const bool in = k < a.inner;  // eight at a time: the sum's length is a multiple of 8
+                x[u][s] = load_chunk<E>(rx, in ? x_off + 2 * (uint32_t)k : DMA_OOB);
+#pragma unroll
+                for (int j = 0; j < FEW_N / 16; ++j)
+                    w[u][s][j] = load_chunk<E>(rw, in ? w_off[j] + 2 * (uint32_t)k : DMA_OOB);
+            }
+        __builtin_amdgcn_sched_barrier(0);  // all of them in flight
+#pragma unroll
+        for (int u = 0; u < FEW_AHEAD; ++u)
+#pragma unroll
+            for (int s = 0; s < FEW_K / 32; ++s)
+#pragma unroll
+                for (int j = 0; j < FEW_N / 16; ++j)
+                    acc[j] = El<E>::mfma(w[u][s][j], x[u][s], acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < FEW_N / 16; ++j)
+        sums[wave][j][lane] = acc[j];
+    __syncthreads();
+    // one element to a thread: row m, column n of the tile
+    static_assert(FEW_M * FEW_N == 64 * FEW_WAVES, "a thread for each element");
+    const int m = threadIdx.x / FEW_N, n = threadIdx.x % FEW_N, from = m + 16 * (n % 16 / 4);
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < FEW_WAVES; ++v)
+        sum += sums[v][n / 16][from][n % 4];
+    if (m0 + m < t.rows && n0 + n < a.cols)
+        d[(int64_t)(m0 + m) * a.ldd + n0 + n] = (E)sum;
 }
 
 // dW: tiles of one expert's weight, summed over its rows.
@@ -261,14 +355,14 @@ __global__ __launch_bounds__(256) void grouped_zero_kernel(uint16_t *d, int64_t 
 }
 
 // ------------------------------------------------------------------- plans
-enum Class { C256, C192, C128, C64, C64X128, C16X64, CLASSES };
-const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x128", "16x64"};
+enum Class { C256, C192, C128, C64, C64X128, CLASSES, FEW = CLASSES };
+const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x128", "16x32"};
 constexpr TileClass CLASS[] = {{256, 256, 1, 1.50, 1.50, 16.0},
                                {192, 192, 1, 1.15, 1.15, 9.0},
                                {128, 128, 2, 1.10, 0.50, 6.0},
                                {64, 64, 2, 0.50, 0.27, 4.0},
                                {64, 128, 2, 0.80, 0.45, 5.0},
-                               {16, 64, 4, 0.50, 0.27, 4.0}};
+                               {FEW_M, FEW_N, 2, 0.0, 0.0, 0.0}};
 template <typename E, bool TA, bool TB, typename F>
 bool with_tile(Class c, F f)
 {
@@ -285,10 +379,6 @@ bool with_tile(Class c, F f)
     case C64X128:
         if constexpr (!TA)
             return f(Tile<E, 64, 128, 1, 4, 3, TA, TB, STREAM, MASK>{});
-        [[fallthrough]];
-    case C16X64:
-        if constexpr (!TA)
-            return f(Tile<E, 16, 64, 1, 2, 3, TA, TB, STREAM, MASK>{});
         [[fallthrough]];
     default:
         return f(Tile<E, 64, 64, 2, 2, 3, TA, TB, false, MASK>{});
@@ -307,16 +397,23 @@ struct Plan {
     int64_t a_cols, b_cols;  // of the operands' rows
     int64_t a_bytes, b_bytes;
 };
+constexpr double FEW_TILES = 256.0;
 bool rows_ok(const void *p, int64_t ld, int64_t cols)
 {
     return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= MAX_DMA_LD;
 }
-// The experts that get a row, if M rows go to E experts evenly, and the tile rows
-// of their shares.
-double tile_rows(int64_t M, int64_t E, int bm)
+// Time in microseconds of a product over rows: `hit` experts with some `each` rows,
+// `cols` columns, `ktiles` K-tiles.  Experts' shares are not even, so how many tile
+// rows there are is known to some 10%, and the last round is taken as half full.
+// Within some 15% of 8192 and 4096 rows in 64 experts of 1024×2048 in all classes, where
+// the ratios between them decide.
+double rows_time(const TileClass &c, double hit, double each, int64_t cols, int64_t ktiles)
 {
-    const double hit = (double)std::min(M, E), each = (double)M / hit;
-    return hit * std::max(1.0, each / bm + 0.45);
+    const double n = 1.1 * hit * std::max(1.0, each / c.bm + 0.45) * (double)cdiv(cols, c.bn);
+    const double slots = (double)NUM_CU * c.per_cu, k = (double)ktiles;
+    if (n > slots)
+        return (n / slots + 0.6) * (k * c.ktile + c.fixed);
+    return k * (c.alone + (c.ktile - c.alone) * std::max(0.0, n - NUM_CU) / NUM_CU) + c.fixed;
 }
 Plan make_plan(const Call &q)
 {
@@ -342,17 +439,13 @@ Plan make_plan(const Call &q)
         p.grid = q.E * cdiv(q.N, CLASS[c].bm) * cdiv(q.K, CLASS[c].bn);
         return p;
     }
-    const double each = (double)q.M / (double)std::min(q.M, q.E);
-    if (each <= 16.0) {
-        p.c = C16X64;
-    } else if (each <= 48.0) {
-        p.c = C64X128;
+    const double hit = (double)std::min(q.M, q.E), each = (double)q.M / hit;
+    if (!dx && each <= FEW_M && hit * (double)cdiv(out, CLASS[C64X128].bn) <= FEW_TILES) {
+        p.c = FEW;
     } else {
         int c = 0;
-        const auto time = [&](int i) {
-            return tile_time(CLASS[i], (int64_t)(tile_rows(q.M, q.E, CLASS[i].bm) * (double)cdiv(out, CLASS[i].bn)), cdiv(inner, BK));
-        };
-        for (int i = 1; i < C64X128; ++i)
+        const auto time = [&](int i) { return rows_time(CLASS[i], hit, each, out, cdiv(inner, BK)); };
+        for (int i = 1; i < CLASSES; ++i)
             if (!(dx && i == C192) && time(i) < time(c))
                 c = i;
         p.c = (Class)c;
@@ -447,7 +540,8 @@ int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_
         const RowsArgs a = {A, B, ends, D, lda, ldb, w_stride, ldd, (int)q.M, (int)q.E,
                             (int)(y ? (p.pack_a || p.pack_b ? round_up(q.K, 8) : q.K) : q.N), (int)(y ? q.N : q.K), (int)cols, vec,
                             (int)cdiv(cols, CLASS[p.c].bn)};
-        ok = ok && (y ? with_tile<E, false, false>(p.c, [&](auto t) {
+        ok = ok && (p.c == FEW ? launch(grouped_few_kernel<E>, p.grid, 64 * FEW_WAVES, stream, a)
+                    : y ? with_tile<E, false, false>(p.c, [&](auto t) {
             return launch(grouped_rows_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
         }) : with_tile<E, false, true>(p.c, [&](auto t) {
             return launch(grouped_rows_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);

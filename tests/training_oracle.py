@@ -95,7 +95,8 @@ def adamw(p, g, m, v, step, lr, betas, eps, weight_decay, g_scale=1.0):
     products of a rounded factor, v of two with the square, so 3 and 5 roundings at
     most on the way to a term (one more for a scaled gradient) and one of the sum.
     The quotient has the error of m, half of v's, and the roundings of the root, its
-    factor, product, sum, quotient and rate."""
+    factor, product, sum and rate, and is itself a product with a reciprocal that is
+    off by at most one unit in the last place: 2 + 1 half units."""
     b1, b2 = betas
     p, g, m, v = (t.double() for t in (p, g, m, v))
     g = g * g_scale
@@ -110,7 +111,7 @@ def adamw(p, g, m, v, step, lr, betas, eps, weight_decay, g_scale=1.0):
     # √(v + t) − √v <= √t, and t/√v where v is larger
     troot = torch.minimum(torch.sqrt(tv), tv / torch.sqrt(v1).clamp_min(1e-300)) + 3 * E32 * torch.sqrt(v1)
     tdenom = 1.01 * troot / math.sqrt(1 - b2 ** step) + 2 * E32 * denom
-    tq = 1.01 * tm / denom + q.abs() * (1.01 * torch.minimum(tdenom / denom, torch.ones_like(denom)) + 2 * E32)
+    tq = 1.01 * tm / denom + q.abs() * (1.01 * torch.minimum(tdenom / denom, torch.ones_like(denom)) + 3 * E32)
     p1 = (1 - lr * weight_decay) * p - rate * q
     tp = 3 * E32 * p.abs() + rate * (1.01 * tq + 3 * E32 * q.abs()) + E32 * p1.abs() + 2.0 ** -148
     return (p1, m1, v1), (tp, tm, tv)
@@ -143,7 +144,8 @@ def decode(codes, scales):
 
 
 def adamw_in_f32(p, g, m, v, step, lr, betas, eps, weight_decay, g_scale=None):
-    """The step operation for operation in fp32 on the CPU: p (unrounded), m, v, √v."""
+    """The step operation for operation in fp32 on the CPU: p (unrounded), m, v, √v, and how
+    far p may be off where its quotient is within three half units instead of one half."""
     b1, b2 = betas
     f = lambda x: float(torch.tensor(x, dtype=torch.float64).float())  # noqa: E731  rounded once
     p, g, m, v = (t.detach().cpu().float() for t in (p, g, m, v))
@@ -152,5 +154,8 @@ def adamw_in_f32(p, g, m, v, step, lr, betas, eps, weight_decay, g_scale=None):
     m = m * f(b1) + g * f(1.0 - b1)
     v = v * f(b2) + (g * g) * f(1.0 - b2)
     r = v.double().sqrt().float()  # rounded to nearest, which torch's fp32 root is not always
-    p = p * f(1.0 - lr * weight_decay) - (m / (r * f(1.0 / math.sqrt(1.0 - b2 ** step)) + f(eps))) * f(lr / (1.0 - b1 ** step))
-    return p, m, v, r
+    update = (m / (r * f(1.0 / math.sqrt(1.0 - b2 ** step)) + f(eps))) * f(lr / (1.0 - b1 ** step))
+    p = p * f(1.0 - lr * weight_decay) - update
+    # the quotients' 4 half units apart, one rounding of the product with the rate and one
+    # of p in either computation
+    return p, m, v, r, (6 * E32 * update.abs().double() + 2 * E32 * p.abs().double()) * (1 + 2.0 ** -20) + 2.0 ** -147
