@@ -562,8 +562,8 @@ __host__ __device__ constexpr int stage_off(int r, int c)
 // Rows [0, R) of the staged block to D rows row0 + r (through `map` where it
 // is given: D row map[row0 + r]), columns col0 .., inside rows × cols; `vec`:
 // D's rows are 16-byte aligned.  WORKSPACE: they always are, and cols is a
-// multiple of 8.
-template <typename E, int R, int C, bool WORKSPACE = false>
+// multiple of 8.  NT: past the caches.
+template <typename E, int R, int C, bool WORKSPACE = false, bool NT = false>
 __device__ inline void store_block(const E *stg, E *__restrict__ D, int64_t ld, int row0, int col0, int rows,
                                    int cols, bool vec, const int *__restrict__ map, int lane)
 {
@@ -576,8 +576,13 @@ __device__ inline void store_block(const E *stg, E *__restrict__ D, int64_t ld, 
             const int at = p * 64 + lane, rc = at % CH, r = at / CH;
             const int row = row0 + r, col = col0 + 8 * rc;
             const V8 v = *reinterpret_cast<const V8 *>(stg + stage_off<C>(r, 8 * rc));
-            if (row < rows && (!WORKSPACE || col < cols))
-                *reinterpret_cast<V8 *>(D + (int64_t)(map ? map[row] : row) * ld + col) = v;
+            if (row < rows && (!WORKSPACE || col < cols)) {
+                V8 *const to = reinterpret_cast<V8 *>(D + (int64_t)(map ? map[row] : row) * ld + col);
+                if constexpr (NT)
+                    __builtin_nontemporal_store(v, to);
+                else
+                    *to = v;
+            }
         }
     } else {
 #pragma unroll 1

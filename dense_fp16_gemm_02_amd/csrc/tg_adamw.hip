@@ -138,8 +138,8 @@ __device__ inline Raw<uint8_t> encode(const float (&x)[PER_LANE], float &scale)
         top = max(top, (uint32_t)__shfl_xor((int)top, o));
     const float most = __uint_as_float(top);
     const bool held = !(most < FLUSH);
-    const float per = held ? TOP / most : 0.0f;
-    scale = held ? most / TOP : 0.0f;
+    const float per = held ? 1.0f / most * TOP : 0.0f;
+    scale = held ? most * (1.0f / TOP) : 0.0f;
     float q[PER_LANE];
 #pragma unroll
     for (int e = 0; e < PER_LANE; ++e) {

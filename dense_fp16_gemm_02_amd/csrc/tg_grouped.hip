@@ -71,44 +71,68 @@ __device__ inline void scan_groups(const int64_t *ends, int E, int M, int base, 
     lo = lane == 0 ? row : lo;
     upto = tiles + scan64((hi - lo + BM - 1) / BM, [](int x, int y) { return x + y; });
 }
+// The experts' tile rows, as far as a wave's registers hold them: the last 64.
+struct Groups {
+    int lo, hi, upto;  // of this lane's expert
+    int row, tiles;    // where the rows behind the experts begin; tile rows of the experts
+    int all;           // tile rows with the rows behind
+};
+template <int BM>
+__device__ inline Groups find_groups(const int64_t *ends, int E, int M)
+{
+    Groups g = {};
+    for (int base = 0; base < E; base += 64) {
+        scan_groups<BM>(ends, E, M, base, lane_id(), g.row, g.tiles, g.lo, g.hi, g.upto);
+        g.row = __builtin_amdgcn_readlane(g.hi, 63), g.tiles = __builtin_amdgcn_readlane(g.upto, 63);
+    }
+    g.all = g.tiles + (M - g.row + BM - 1) / BM;
+    return g;
+}
 struct Tile2d {
     int e, lo, rows;  // expert (E: the rows behind), its first row and their number
     int tm, tn;
 };
+// Tile `logical` of all: expert by expert, in groups of four tile rows.
 template <int BM>
-__device__ inline bool find_tile(const int64_t *ends, int E, int M, int tiles_n, Tile2d &t)
+__device__ inline Tile2d find_tile(Groups g, const int64_t *ends, int E, int M, int tiles_n, int logical)
 {
-    const int lane = lane_id();
-    int lo, hi, upto, row = 0, tiles = 0;
-    for (int base = 0; base < E; base += 64) {
-        scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
-        row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
-    }
-    const int all = tiles + (M - row + BM - 1) / BM;  // with the rows behind
-    if ((int64_t)blockIdx.x >= (int64_t)all * tiles_n)
-        return false;
-    const int logical = xcd_chunks(blockIdx.x, all * tiles_n), tile_row = logical / tiles_n;
-    int first = tiles;
-    t.e = E, t.lo = row, t.rows = M - row;
-    if (tile_row < tiles) {
+    const int tile_row = logical / tiles_n;
+    Tile2d t = {E, g.row, M - g.row, 0, 0};
+    int first = g.tiles;
+    if (tile_row < g.tiles) {
         int base = 0;
         if (E > 64) {  // otherwise the registers still hold the only scan
-            row = tiles = 0;
+            g.row = g.tiles = 0;
             for (;; base += 64) {
-                scan_groups<BM>(ends, E, M, base, lane, row, tiles, lo, hi, upto);
-                if (__builtin_amdgcn_readlane(upto, 63) > tile_row)
+                scan_groups<BM>(ends, E, M, base, lane_id(), g.row, g.tiles, g.lo, g.hi, g.upto);
+                if (__builtin_amdgcn_readlane(g.upto, 63) > tile_row)
                     break;
-                row = __builtin_amdgcn_readlane(hi, 63), tiles = __builtin_amdgcn_readlane(upto, 63);
+                g.row = __builtin_amdgcn_readlane(g.hi, 63), g.tiles = __builtin_amdgcn_readlane(g.upto, 63);
             }
         }
-        const int at = uniform(__builtin_ctzll(__ballot(upto > tile_row)));
+        const int at = uniform(__builtin_ctzll(__ballot(g.upto > tile_row)));
         t.e = base + at;
-        t.lo = __builtin_amdgcn_readlane(lo, at);
-        t.rows = __builtin_amdgcn_readlane(hi, at) - t.lo;
-        first = __builtin_amdgcn_readlane(upto, at) - (t.rows + BM - 1) / BM;
+        t.lo = __builtin_amdgcn_readlane(g.lo, at);
+        t.rows = __builtin_amdgcn_readlane(g.hi, at) - t.lo;
+        first = __builtin_amdgcn_readlane(g.upto, at) - (t.rows + BM - 1) / BM;
     }
     grouped_tile<4>(logical - first * tiles_n, (t.rows + BM - 1) / BM, tiles_n, t.tm, t.tn);
-    return true;
+    return t;
+}
+// The last round of a launch: where its tiles are at most half of the workgroups that
+// run at once, each is cut into parts along the sum, whose fp32 sums go to the
+// workspace and are added by a kernel behind it, in order.
+constexpr int MIN_PART = 8, MAX_PARTS = 32;  // K-tiles of a part, and parts
+struct Split {
+    int full, rest, parts;  // tiles of whole rounds; the others; parts of each of those
+};
+__device__ inline Split split_tiles(int total, int slots, int ktiles)
+{
+    Split s;
+    s.full = total / slots * slots;
+    s.rest = total - s.full;
+    s.parts = s.rest > 0 ? imax(imin(imin(slots / s.rest, ktiles / MIN_PART), MAX_PARTS), 1) : 1;
+    return s;
 }
 // Expert e's rows.
 __device__ inline void find_rows(const int64_t *ends, int M, int e, int &lo, int &rows)
@@ -127,7 +151,7 @@ __device__ inline void find_rows(const int64_t *ends, int M, int e, int &lo, int
 // ------------------------------------------------------------------ products
 template <typename E, typename T>
 __device__ inline void store_tile(E *smem, const f32x4 (&acc)[T::TM][T::TN], E *D, int64_t ld, int m0, int n0, int rows,
-                                  int cols, bool vec)
+                                  int cols, bool vec, bool nt)
 {
     using V4 = typename El<E>::v4;
     const int lane = lane_id();
@@ -146,7 +170,11 @@ __device__ inline void store_tile(E *smem, const f32x4 (&acc)[T::TM][T::TN], E *
                 d[v] = (E)acc[i][j][v];
             *reinterpret_cast<V4 *>(stg + stage_off<T::WTN>(16 * i + fr, 16 * j + fc)) = d;
         }
-    store_block<E, T::WTM, T::WTN>(stg, D, ld, m0 + wm * T::WTM, n0 + wn * T::WTN, rows, cols, vec, nullptr, lane);
+    if (nt)
+        store_block<E, T::WTM, T::WTN, false, true>(stg, D, ld, m0 + wm * T::WTM, n0 + wn * T::WTN, rows, cols, vec,
+                                                    nullptr, lane);
+    else
+        store_block<E, T::WTM, T::WTN>(stg, D, ld, m0 + wm * T::WTM, n0 + wn * T::WTN, rows, cols, vec, nullptr, lane);
 }
 // Zeros where a tile's product is over nothing.
 template <typename E, int BM, int BN, int THREADS>
@@ -156,6 +184,59 @@ __device__ inline void zero_tile(E *D, int64_t ld, int m0, int n0, int rows, int
     for (int r = m0 + (int)threadIdx.x / 64; r < r1; r += THREADS / 64)
         for (int c = n0 + lane_id(); c < c1; c += 64)
             D[r * ld + c] = (E)0.0f;
+}
+
+// A tile's fp32 sums, as the lanes hold them, to place `at` of the workspace's parts.
+template <typename T>
+__device__ inline void store_part(const f32x4 (&acc)[T::TM][T::TN], float *parts, int64_t at)
+{
+    f32x4 *to = reinterpret_cast<f32x4 *>(parts + at * (T::BM * T::BN)) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j)
+            to[(i * T::TN + j) * T::THREADS] = acc[i][j];
+}
+// `n` parts of a tile added in order, `step` places apart: of the 16-row strips that the
+// tile's waves hold, strip i.
+template <typename E, typename T>
+__device__ inline void join_parts(const float *parts, int64_t at, int64_t step, int n, int i, E *D, int64_t ld, int m0,
+                                  int n0, int rows, int cols, bool vec)
+{
+    using V4 = typename El<E>::v4;
+    const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
+    const int row = m0 + wave / T::WN * T::WTM + 16 * i + (lane & 15);
+    const int col0 = n0 + wave % T::WN * T::WTN + 4 * (lane >> 4);
+    E *d = D + (int64_t)row * ld;
+    const f32x4 *from = reinterpret_cast<const f32x4 *>(parts + at * (T::BM * T::BN)) + threadIdx.x;
+    f32x4 sum[T::TN];
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j)
+        sum[j] = from[(i * T::TN + j) * T::THREADS];
+    for (int z = 1; z < n; ++z) {
+        from += step * (T::BM * T::BN / 4);
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j)
+            sum[j] += from[(i * T::TN + j) * T::THREADS];
+    }
+    if (row >= rows)
+        return;
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) {
+        const int col = col0 + 16 * j;
+        V4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = (E)sum[j][e];
+        if (vec && col + 4 <= cols) {
+            *reinterpret_cast<V4 *>(d + col) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < cols)
+                    d[col + e] = v[e];
+        }
+    }
 }
 
 // Y (K-major W) and dX (transposed W): tiles of rows of one expert.
@@ -169,16 +250,36 @@ struct RowsArgs {
     int w_extent;  // rows (Y) or columns (dX) of a weight
     int cols;      // of d
     bool vec;      // d's rows are 16-byte aligned
+    bool nt;       // d is written past the caches
     int tiles_n;
+    float *parts;  // SPLIT: sums of the last round's parts, BM·BN to each of `slots`
+    int slots;     // workgroups that run at once
 };
-template <typename E, typename T>
+template <typename T>
+__device__ inline Operand weight_of(const RowsArgs &a, int e, int k0)
+{
+    return {reinterpret_cast<const uint16_t *>(a.w) + (int64_t)e * a.w_stride + (T::TB ? k0 * a.ldw : k0), a.ldw, a.w_extent};
+}
+__device__ inline Operand rows_of(const RowsArgs &a, const Tile2d &t, int k0)
+{
+    return {reinterpret_cast<const uint16_t *>(a.a) + (int64_t)t.lo * a.lda + k0, a.lda, t.rows};
+}
+// SPLIT: all whole rounds; the last one too where it is not cut into parts.
+template <typename E, typename T, bool SPLIT>
 __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_rows_kernel(
     RowsArgs a)
 {
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
-    Tile2d t;
-    if (!find_tile<T::BM>(a.ends, a.E, a.M, a.tiles_n, t))
+    const Groups g = find_groups<T::BM>(a.ends, a.E, a.M);
+    const int total = g.all * a.tiles_n;
+    int here = total;
+    if constexpr (SPLIT) {
+        const Split s = split_tiles(total, a.slots, (a.inner + BK - 1) / BK);
+        here = s.parts > 1 ? s.full : total;
+    }
+    if ((int)blockIdx.x >= here)
         return;
+    const Tile2d t = find_tile<T::BM>(g, a.ends, a.E, a.M, a.tiles_n, xcd_chunks(blockIdx.x, total));
     const int m0 = t.tm * T::BM, n0 = t.tn * T::BN;
     E *d = reinterpret_cast<E *>(a.d) + (int64_t)t.lo * a.ldd;
     if (t.e >= a.E) {
@@ -187,10 +288,52 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
     }
     f32x4 acc[T::TM][T::TN];
     T::clear(acc);
-    const Operand x = {reinterpret_cast<const E *>(a.a) + (int64_t)t.lo * a.lda, a.lda, t.rows};
-    const Operand w = {reinterpret_cast<const E *>(a.w) + (int64_t)t.e * a.w_stride, a.ldw, a.w_extent};
-    T::run(smem, x, w, m0, n0, a.inner, acc);
-    store_tile<E, T>(smem, acc, d, a.ldd, m0, n0, t.rows, a.cols, a.vec);
+    T::run(smem, rows_of(a, t, 0), weight_of<T>(a, t.e, 0), m0, n0, a.inner, acc);
+    store_tile<E, T>(smem, acc, d, a.ldd, m0, n0, t.rows, a.cols, a.vec, a.nt);
+}
+// The last round's parts, where it is cut into some: their fp32 sums, as the lanes
+// hold them.  (A kernel of its own: both ends of the tile product in one spill
+// registers at 256×256.)
+template <typename E, typename T>
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_parts_kernel(
+    RowsArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
+    const Groups g = find_groups<T::BM>(a.ends, a.E, a.M);
+    const int ktiles = (a.inner + BK - 1) / BK, part = (int)blockIdx.x;
+    const Split s = split_tiles(g.all * a.tiles_n, a.slots, ktiles);
+    if (s.parts < 2 || part >= s.rest * s.parts)
+        return;
+    const Tile2d t = find_tile<T::BM>(g, a.ends, a.E, a.M, a.tiles_n, s.full + part % s.rest);
+    const int m0 = t.tm * T::BM, n0 = t.tn * T::BN;
+    if (t.e >= a.E) {
+        if (part < s.rest)
+            zero_tile<E, T::BM, T::BN, T::THREADS>(reinterpret_cast<E *>(a.d) + (int64_t)t.lo * a.ldd, a.ldd, m0, n0, t.rows,
+                                                   a.cols);
+        return;
+    }
+    // K-tiles in memory order; the K-major product's partial one comes first
+    const int z = part / s.rest, shift = T::FIRST ? a.inner - ktiles * BK : 0;
+    const int k0 = imax(ktiles * z / s.parts * BK + shift, 0), k1 = imin(ktiles * (z + 1) / s.parts * BK + shift, a.inner);
+    f32x4 acc[T::TM][T::TN];
+    T::clear(acc);
+    T::run(smem, rows_of(a, t, k0), weight_of<T>(a, t.e, k0), m0, n0, k1 - k0, acc);
+    store_part<T>(acc, a.parts, part);
+}
+// The parts' sums: a workgroup takes one of the 16-row strips that a tile's waves hold.
+template <typename E, typename T>
+__global__ __launch_bounds__(T::THREADS) void grouped_join_kernel(RowsArgs a)
+{
+    const Groups g = find_groups<T::BM>(a.ends, a.E, a.M);
+    const Split s = split_tiles(g.all * a.tiles_n, a.slots, (a.inner + BK - 1) / BK);
+    const int tile = (int)blockIdx.x / T::TM, i = (int)blockIdx.x % T::TM;
+    if (s.parts < 2 || tile >= s.rest)
+        return;
+    const Tile2d t = find_tile<T::BM>(g, a.ends, a.E, a.M, a.tiles_n, s.full + tile);
+    if (t.e >= a.E)
+        return;  // the rows behind: written as zeros
+    join_parts<E, T>(a.parts, tile, s.rest, s.parts, i, reinterpret_cast<E *>(a.d) + (int64_t)t.lo * a.ldd, a.ldd,
+                     t.tm * T::BM, t.tn * T::BN, t.rows, a.cols, a.vec);
 }
 
 // Y of a few rows an expert where a tile of W for each compute unit is not there:
@@ -217,9 +360,10 @@ template <typename E>
 __global__ __launch_bounds__(64 * FEW_WAVES) void grouped_few_kernel(RowsArgs a)
 {
     __shared__ f32x4 sums[FEW_WAVES][FEW_N / 16][64];
-    Tile2d t;
-    if (!find_tile<FEW_M>(a.ends, a.E, a.M, a.tiles_n, t))
+    const Groups groups = find_groups<FEW_M>(a.ends, a.E, a.M);
+    if ((int)blockIdx.x >= groups.all * a.tiles_n)
         return;
+    const Tile2d t = find_tile<FEW_M>(groups, a.ends, a.E, a.M, a.tiles_n, xcd_chunks(blockIdx.x, groups.all * a.tiles_n));
     const int m0 = t.tm * FEW_M, n0 = t.tn * FEW_N;
     E *d = reinterpret_cast<E *>(a.d) + (int64_t)t.lo * a.ldd;
     if (t.e >= a.E) {
@@ -279,38 +423,63 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void grouped_few_kernel(RowsArgs a)
         d[(int64_t)(m0 + m) * a.ldd + n0 + n] = (E)sum;
 }
 
-// dW: tiles of one expert's weight, summed over its rows.
+// dW: tiles of one expert's weight, summed over its rows; PARTS: over a part of them,
+// where there are too few tiles to fill the chip.
 struct WeightArgs {
     const void *dy, *x;
     const int64_t *ends;
     void *dw;
     int64_t lddy, ldx, lddw, dw_stride;
     int M, E, N, K;
-    bool vec;
+    bool vec, nt;
     int tiles_m, tiles_n;
+    float *sums;  // PARTS
+    int parts;
 };
-template <typename E, typename T>
+template <typename E, typename T, bool PARTS>
 __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_weight_kernel(
     WeightArgs a)
 {
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
-    const int per = a.tiles_m * a.tiles_n;
-    const int logical = xcd_chunks(blockIdx.x, a.E * per), e = logical / per;
+    const int per = a.tiles_m * a.tiles_n, total = a.E * per;
+    const int z = PARTS ? (int)blockIdx.x / total : 0;
+    const int logical = xcd_chunks((int)blockIdx.x - z * total, total), e = logical / per;
     int tm, tn, lo, rows;
     grouped_tile<4>(logical - e * per, a.tiles_m, a.tiles_n, tm, tn);
     find_rows(a.ends, a.M, e, lo, rows);
     const int m0 = tm * T::BM, n0 = tn * T::BN;
     E *d = reinterpret_cast<E *>(a.dw) + (int64_t)e * a.dw_stride;
     if (rows == 0) {
-        zero_tile<E, T::BM, T::BN, T::THREADS>(d, a.lddw, m0, n0, a.N, a.K);
+        if (z == 0)
+            zero_tile<E, T::BM, T::BN, T::THREADS>(d, a.lddw, m0, n0, a.N, a.K);
         return;
+    }
+    if constexpr (PARTS) {
+        const int ktiles = (rows + BK - 1) / BK, k0 = (int)((int64_t)ktiles * z / a.parts) * BK;
+        rows = imin((int)((int64_t)ktiles * (z + 1) / a.parts) * BK, rows) - k0;
+        lo += k0;
     }
     f32x4 acc[T::TM][T::TN];
     T::clear(acc);
     const Operand dy = {reinterpret_cast<const E *>(a.dy) + (int64_t)lo * a.lddy, a.lddy, a.N};
     const Operand x = {reinterpret_cast<const E *>(a.x) + (int64_t)lo * a.ldx, a.ldx, a.K};
     T::run(smem, dy, x, m0, n0, rows, acc);
-    store_tile<E, T>(smem, acc, d, a.lddw, m0, n0, a.N, a.K, a.vec);
+    if constexpr (PARTS)
+        store_part<T>(acc, a.sums, (int64_t)z * total + logical);
+    else
+        store_tile<E, T>(smem, acc, d, a.lddw, m0, n0, a.N, a.K, a.vec, a.nt);
+}
+template <typename E, typename T>
+__global__ __launch_bounds__(T::THREADS) void grouped_weight_join_kernel(WeightArgs a)
+{
+    const int per = a.tiles_m * a.tiles_n, logical = (int)blockIdx.x / T::TM, e = logical / per;
+    int tm, tn, lo, rows;
+    grouped_tile<4>(logical - e * per, a.tiles_m, a.tiles_n, tm, tn);
+    find_rows(a.ends, a.M, e, lo, rows);
+    if (rows == 0)
+        return;  // written as zeros
+    join_parts<E, T>(a.sums, logical, (int64_t)a.E * per, a.parts, (int)blockIdx.x % T::TM,
+                     reinterpret_cast<E *>(a.dw) + (int64_t)e * a.dw_stride, a.lddw, tm * T::BM, tn * T::BN, a.N, a.K, a.vec);
 }
 
 // ------------------------------------------------------------------- packing
@@ -322,25 +491,27 @@ struct PackArgs {
     uint16_t *dst;
     int64_t ld, stride, rows, per, cols, cols8;
     const int64_t *ends;
-    int M;
+    int M, run;  // run: rows of a workgroup, of one weight
 };
 __global__ __launch_bounds__(256) void grouped_pack_kernel(PackArgs a)
 {
-    const int64_t chunks = a.cols8 / 8;
-    // a workgroup takes whole runs of rows of one weight
-    const int64_t runs = cdiv(a.per, 64);
+    const int chunks = (int)(a.cols8 / 8);
+    const int64_t runs = cdiv(a.per, a.run);
     for (int64_t b = blockIdx.x; b < (a.rows / a.per) * runs; b += gridDim.x) {
-        const int64_t e = b / runs, r0 = (b - e * runs) * 64, r1 = r0 + 64 < a.per ? r0 + 64 : a.per;
+        const int64_t e = b / runs, r0 = (b - e * runs) * a.run;
+        const int n = (int)(a.per - r0 < a.run ? a.per - r0 : a.run);
         if (a.ends) {
-            int lo, n;
-            find_rows(a.ends, a.M, (int)e, lo, n);
-            if (n == 0)
+            int lo, rows;
+            find_rows(a.ends, a.M, (int)e, lo, rows);
+            if (rows == 0)
                 continue;
         }
-        for (int64_t i = threadIdx.x; i < (r1 - r0) * chunks; i += 256) {
-            const int64_t r = r0 + i / chunks, c = i % chunks * 8;
-            *reinterpret_cast<uint4 *>(a.dst + (e * a.per + r) * a.cols8 + c) =
-                load8(a.src + e * a.stride + r * a.ld, c, a.cols, false);
+        const uint16_t *src = a.src + e * a.stride + r0 * a.ld;
+        uint16_t *dst = a.dst + (e * a.per + r0) * a.cols8;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < (int64_t)n * chunks; i += 256) {
+            const int64_t r = i / chunks, c = (i - r * chunks) * 8;
+            *reinterpret_cast<uint4 *>(dst + r * a.cols8 + c) = load8(src + r * a.ld, c, a.cols, false);
         }
     }
 }
@@ -396,8 +567,11 @@ struct Plan {
     bool pack_a, pack_b;
     int64_t a_cols, b_cols;  // of the operands' rows
     int64_t a_bytes, b_bytes;
+    int slots;               // Y, dX with the last round in parts: the workgroups that run at once; 0 otherwise
+    int parts;               // dW: into how many its sums are cut
+    int64_t parts_bytes;
 };
-constexpr double FEW_TILES = 256.0;
+constexpr double FEW_TILES = 512.0, SPLIT_US = 60.0;
 bool rows_ok(const void *p, int64_t ld, int64_t cols)
 {
     return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= MAX_DMA_LD;
@@ -407,13 +581,40 @@ bool rows_ok(const void *p, int64_t ld, int64_t cols)
 // rows there are is known to some 10%, and the last round is taken as half full.
 // Within some 15% of 8192 and 4096 rows in 64 experts of 1024×2048 in all classes, where
 // the ratios between them decide.
-double rows_time(const TileClass &c, double hit, double each, int64_t cols, int64_t ktiles)
+struct Estimate {
+    double time;
+    bool split;  // whether the last round, or the only one, is cut into parts
+};
+// Cutting takes two more launches and the parts' way through memory, some 12 us (and
+// 4 us where the groups then leave nothing to cut): it is for rounds that take
+// longer, and for few of them.
+Estimate rows_time(const TileClass &c, double hit, double each, int64_t cols, int64_t ktiles)
 {
     const double n = 1.1 * hit * std::max(1.0, each / c.bm + 0.45) * (double)cdiv(cols, c.bn);
     const double slots = (double)NUM_CU * c.per_cu, k = (double)ktiles;
     if (n > slots)
-        return (n / slots + 0.6) * (k * c.ktile + c.fixed);
-    return k * (c.alone + (c.ktile - c.alone) * std::max(0.0, n - NUM_CU) / NUM_CU) + c.fixed;
+        return {(n / slots + 0.6) * (k * c.ktile + c.fixed), n <= 12.0 * slots && k * c.ktile >= SPLIT_US};
+    const double whole = k * (c.alone + (c.ktile - c.alone) * std::max(0.0, n - NUM_CU) / NUM_CU) + c.fixed;
+    const double parts = std::min(std::min(slots / n, k / MIN_PART), (double)MAX_PARTS);
+    const double cut = k * c.ktile / std::max(1.0, std::floor(parts)) + c.fixed + 12.0;
+    return {std::min(whole, cut), cut < whole || k * c.ktile >= SPLIT_US};
+}
+// dW's tiles and into how many parts its sums are cut, 1 or as many as fill the chip.
+struct WeightEstimate {
+    double time;
+    int parts;
+};
+WeightEstimate weight_time(const TileClass &c, const Call &q)
+{
+    const int64_t n = q.E * cdiv(q.N, c.bm) * cdiv(q.K, c.bn), ktiles = cdiv(cdiv(q.M, q.E), BK);
+    const int64_t slots = NUM_CU * c.per_cu;
+    const double whole = tile_time(c, n, ktiles);
+    const int64_t parts = std::min(std::min(slots / n, ktiles / MIN_PART), (int64_t)MAX_PARTS);
+    if (parts < 2)
+        return {whole, 1};
+    // the parts are written and read in fp32
+    const double cut = tile_time(c, n * parts, cdiv(ktiles, parts)) + 8.0 + (double)(n * parts * c.bm * c.bn) * 8.0 / 4e6;
+    return cut < whole ? WeightEstimate{cut, (int)parts} : WeightEstimate{whole, 1};
 }
 Plan make_plan(const Call &q)
 {
@@ -429,33 +630,44 @@ Plan make_plan(const Call &q)
     const int64_t out = dx ? q.K : q.N, inner = dx ? q.N : q.K;
     if (dw) {
         int c = 0;
-        const auto time = [&](int i) {
-            return tile_time(CLASS[i], q.E * cdiv(q.N, CLASS[i].bm) * cdiv(q.K, CLASS[i].bn), cdiv(cdiv(q.M, q.E), BK));
-        };
         for (int i = 1; i < C64X128; ++i)
-            if (time(i) < time(c))
+            if (weight_time(CLASS[i], q).time < weight_time(CLASS[c], q).time)
                 c = i;
+        const int64_t n = q.E * cdiv(q.N, CLASS[c].bm) * cdiv(q.K, CLASS[c].bn);
         p.c = (Class)c;
-        p.grid = q.E * cdiv(q.N, CLASS[c].bm) * cdiv(q.K, CLASS[c].bn);
+        p.parts = weight_time(CLASS[c], q).parts;
+        p.grid = n * p.parts;
+        p.parts_bytes = p.parts > 1 ? 4 * p.grid * CLASS[c].bm * CLASS[c].bn : 0;
         return p;
     }
     const double hit = (double)std::min(q.M, q.E), each = (double)q.M / hit;
-    if (!dx && each <= FEW_M && hit * (double)cdiv(out, CLASS[C64X128].bn) <= FEW_TILES) {
+    const double few = hit * std::max(1.0, each / FEW_M + 0.45) * (double)cdiv(out, FEW_N);
+    bool split = false;
+    if (!dx && few <= FEW_TILES) {
         p.c = FEW;
     } else {
         int c = 0;
         const auto time = [&](int i) { return rows_time(CLASS[i], hit, each, out, cdiv(inner, BK)); };
         for (int i = 1; i < CLASSES; ++i)
-            if (!(dx && i == C192) && time(i) < time(c))
+            if (!(dx && i == C192) && time(i).time < time(c).time)
                 c = i;
         p.c = (Class)c;
+        split = time(c).split;
     }
     const int64_t bm = CLASS[p.c].bm;
     // each group adds at most bm - 1 rows to whole tiles
     p.grid = (q.M + std::min(q.E + 1, q.M) * (bm - 1)) / bm * cdiv(out, CLASS[p.c].bn);
+    if (split) {
+        p.slots = NUM_CU * CLASS[p.c].per_cu;
+        p.parts_bytes = (int64_t)4 * p.slots * bm * CLASS[p.c].bn;
+    }
     return p;
 }
 
+// Results from this size on are written past the caches, which they would fill for
+// nothing (dW of 8 experts of 14336×4096 from 128 rows 308 -> 237 us, of 64 of 1024×2048 from
+// 16384 rows 163 -> 115; Y of 16384×14336 1522 -> 1505).
+constexpr int64_t NT_BYTES = (int64_t)64 << 20;
 constexpr int64_t LIM = (int64_t)1 << 31, LIM_STRIDE = (int64_t)1 << 42;
 // Whether anything is multiplied: otherwise the result is zeros, or nothing.
 bool multiplies(const Call &q) { return q.M > 0 && q.E > 0 && q.N > 0 && q.K > 0; }
@@ -480,9 +692,11 @@ int64_t copy_grid(int64_t n) { return std::max((int64_t)1, std::min(n, (int64_t)
 bool pack(const void *src, void *dst, int64_t ld, int64_t stride, int64_t batch, int64_t per, int64_t cols,
           const int64_t *ends, int64_t M, void *stream)
 {
-    const PackArgs a = {reinterpret_cast<const uint16_t *>(src), reinterpret_cast<uint16_t *>(dst), ld, stride, batch * per,
-                        per, cols, round_up(cols, 8), ends, (int)M};
-    return launch(grouped_pack_kernel, copy_grid(batch * cdiv(per, 64)), 256, stream, a);
+    PackArgs a = {reinterpret_cast<const uint16_t *>(src), reinterpret_cast<uint16_t *>(dst), ld, stride, batch * per,
+                  per, cols, round_up(cols, 8), ends, (int)M, 0};
+    // some 16 KB a workgroup
+    a.run = (int)std::min(per, std::max((int64_t)1, 1024 / (a.cols8 / 8)));
+    return launch(grouped_pack_kernel, copy_grid(batch * cdiv(per, a.run)), 256, stream, a);
 }
 
 // `ldd`, `d_stride`: of the result
@@ -510,7 +724,7 @@ int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_
                    : TG_ERR_LAUNCH;
     }
     const Plan p = make_plan(q);
-    const int64_t need = p.a_bytes + p.b_bytes;
+    const int64_t need = p.a_bytes + p.b_bytes + p.parts_bytes;
     if (!ends || (uintptr_t)ends % 8 || (need > 0 && (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < need)))
         return TG_ERR_INVALID_ARG;
     if (gfx950_status() != 1)
@@ -529,23 +743,46 @@ int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_
         B = to, ldb = round_up(p.b_cols, 8), w_stride = q.N * ldb;
     }
     const bool vec = ldd % 8 == 0 && (uintptr_t)D % 16 == 0 && (!dw || q.E == 1 || d_stride % 8 == 0);
+    const bool nt = 2 * batch * rows * cols >= NT_BYTES;
+    float *const sums = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + p.a_bytes + p.b_bytes);
     if (dw) {
-        const WeightArgs a = {A, B, ends, D, lda, ldb, ldd, q.E > 1 ? d_stride : 0, (int)q.M, (int)q.E, (int)q.N, (int)q.K, vec,
-                              (int)cdiv(q.N, CLASS[p.c].bm), (int)cdiv(q.K, CLASS[p.c].bn)};
+        WeightArgs a = {};
+        a.dy = A, a.x = B, a.ends = ends, a.dw = D;
+        a.lddy = lda, a.ldx = ldb, a.lddw = ldd, a.dw_stride = q.E > 1 ? d_stride : 0;
+        a.M = (int)q.M, a.E = (int)q.E, a.N = (int)q.N, a.K = (int)q.K;
+        a.vec = vec, a.nt = nt;
+        a.tiles_m = (int)cdiv(q.N, CLASS[p.c].bm), a.tiles_n = (int)cdiv(q.K, CLASS[p.c].bn);
+        a.sums = sums, a.parts = p.parts;
         ok = ok && with_tile<E, true, true>(p.c, [&](auto t) {
-            return launch(grouped_weight_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
+            using T = decltype(t);
+            if (p.parts == 1)
+                return launch(grouped_weight_kernel<E, T, false>, p.grid, T::THREADS, stream, a);
+            return launch(grouped_weight_kernel<E, T, true>, p.grid, T::THREADS, stream, a) &&
+                   launch(grouped_weight_join_kernel<E, T>, p.grid / p.parts * T::TM, T::THREADS, stream, a);
         });
     } else {
-        // behind a packed A the sum may run over its zeros: not over W's rows behind N
-        const RowsArgs a = {A, B, ends, D, lda, ldb, w_stride, ldd, (int)q.M, (int)q.E,
-                            (int)(y ? (p.pack_a || p.pack_b ? round_up(q.K, 8) : q.K) : q.N), (int)(y ? q.N : q.K), (int)cols, vec,
-                            (int)cdiv(cols, CLASS[p.c].bn)};
-        ok = ok && (p.c == FEW ? launch(grouped_few_kernel<E>, p.grid, 64 * FEW_WAVES, stream, a)
-                    : y ? with_tile<E, false, false>(p.c, [&](auto t) {
-            return launch(grouped_rows_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
-        }) : with_tile<E, false, true>(p.c, [&](auto t) {
-            return launch(grouped_rows_kernel<E, decltype(t)>, p.grid, t.THREADS, stream, a);
-        }));
+        RowsArgs a = {};
+        a.a = A, a.w = B, a.ends = ends, a.d = D;
+        a.lda = lda, a.ldw = ldb, a.w_stride = w_stride, a.ldd = ldd;
+        a.M = (int)q.M, a.E = (int)q.E;
+        // over a packed row's zeros, but not over W's rows behind N
+        a.inner = (int)(y ? (p.pack_a || p.pack_b ? round_up(q.K, 8) : q.K) : q.N);
+        a.w_extent = (int)(y ? q.N : q.K), a.cols = (int)cols;
+        a.vec = vec, a.nt = nt;
+        a.tiles_n = (int)cdiv(cols, CLASS[p.c].bn);
+        a.parts = sums, a.slots = p.slots;
+        const auto run = [&](auto t) {
+            using T = decltype(t);
+            if (p.slots == 0)
+                return launch(grouped_rows_kernel<E, T, false>, p.grid, T::THREADS, stream, a);
+            return launch(grouped_rows_kernel<E, T, true>, p.grid, T::THREADS, stream, a) &&
+                   launch(grouped_parts_kernel<E, T>, p.slots, T::THREADS, stream, a) &&
+                   launch(grouped_join_kernel<E, T>, (int64_t)p.slots / 2 * T::TM, T::THREADS, stream, a);
+        };
+        if (p.c == FEW)
+            ok = ok && launch(grouped_few_kernel<E>, p.grid, 64 * FEW_WAVES, stream, a);
+        else
+            ok = ok && (y ? with_tile<E, false, false>(p.c, run) : with_tile<E, false, true>(p.c, run));
     }
     return ok ? TG_OK : TG_ERR_LAUNCH;
 }
@@ -560,7 +797,7 @@ extern "C" int64_t tg_grouped_workspace_bytes(int product, const void *A, const 
     if (!multiplies(q))
         return 0;
     const Plan p = make_plan(q);
-    return p.a_bytes + p.b_bytes;
+    return p.a_bytes + p.b_bytes + p.parts_bytes;
 }
 
 #define TG_GROUPED_ENTRIES(suffix, E)                                                                                 \
@@ -607,7 +844,7 @@ extern "C" int tg_grouped_plan(int product, const void *A, const void *B, int64_
     }
     const Plan p = make_plan(q);
     static const char *const WHAT[] = {"y", "dx", "dw"};
-    snprintf(name, (size_t)name_len, "%s%s%s_%s", p.pack_a ? "pack_a " : "", p.pack_b ? "pack_b " : "", WHAT[product],
-             CLASS_NAME[p.c]);
+    snprintf(name, (size_t)name_len, "%s%s%s_%s%s", p.pack_a ? "pack_a " : "", p.pack_b ? "pack_b " : "", WHAT[product],
+             CLASS_NAME[p.c], p.slots || p.parts > 1 ? "_split" : "");
     return st;
 }

@@ -18,7 +18,8 @@
  *
  * Moments in 8 bits.  A tensor is cut into blocks of TG_ADAMW_BLOCK consecutive
  * elements, the last one possibly shorter.  A block of m is held as E4M3 values
- * in units of a fp32 scale, (its largest magnitude)/448; for v its root √v is
+ * in units of a fp32 scale, its largest magnitude times 1/448 (a value x as
+ * x·(1/largest·448), each operation rounded to nearest); for v its root √v is
  * held, the same way, whose exponents span half of v's.  A rounding is at most
  * 2^-4 of the value (and 2^-10 of the unit below 2^-6 of it); the step itself takes
  * m and √v as they are before they are rounded.  Three rules keep the division safe:

@@ -129,11 +129,11 @@ def encode(x, root):
     top = b.abs().amax(1)
     held = ~(top < 2.0 ** -110)
     top_or_one = torch.where(held, top, torch.ones_like(top))
-    q = b * torch.where(held, 448.0 / top_or_one, torch.zeros_like(top))[:, None]
+    q = b * torch.where(held, torch.ones_like(top) / top_or_one * 448.0, torch.zeros_like(top))[:, None]
     if root:
         q = torch.where(q > 0, torch.clamp(q, min=2.0 ** -9), q)
     codes = torch.clamp(q, -448.0, 448.0).to(torch.float8_e4m3fn)
-    return codes.view(-1)[:n].view(x.shape), torch.where(held, top / 448.0, torch.zeros_like(top))
+    return codes.view(-1)[:n].view(x.shape), torch.where(held, top * float(torch.tensor(1.0) / torch.tensor(448.0)), torch.zeros_like(top))
 
 
 def decode(codes, scales):
