@@ -592,10 +592,14 @@ __device__ inline void store_block(const E *stg, E *__restrict__ D, int64_t ld, 
             const V8 v = *reinterpret_cast<const V8 *>(stg + stage_off<C>(r, 8 * rc));
             if (row < rows) {
                 E *dst = D + (int64_t)(map ? map[row] : row) * ld + col;
+                if (col + 8 <= cols) {
+                    __builtin_memcpy(dst, &v, 16);  // at the alignment of an element
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (col + e < cols)
-                        dst[e] = v[e];
+                    for (int e = 0; e < 8; ++e)
+                        if (col + e < cols)
+                            dst[e] = v[e];
+                }
             }
         }
     }

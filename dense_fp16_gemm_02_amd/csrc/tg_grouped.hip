@@ -12,6 +12,7 @@
 #include "proj_tile.hpp"
 
 #include <algorithm>
+#include <math.h>
 #include <stdio.h>
 
 #include "tg_gemm.h"
@@ -24,9 +25,9 @@ using namespace pt;
 // Workgroup id → tile where tiles differ in length, as those of weights with few
 // and many rows do: each XCD takes 32 consecutive tiles (one for each of its compute
 // units) of every 256, so that all eight work on the same experts at a time.  (With one
-// eighth of all tiles for each XCD, the XCD with the largest expert ends last:
+// eighth of all tiles for each XCD, the XCD with the largest expert ends last: dW of
 // 16384 rows in 8 experts of 14336×4096, the largest with 1.8 times the mean,
-// 2633 us; so TIME_DW.)
+// 2633 us instead of 1707; Y 1580 instead of 1529, as its tiles share more.)
 __host__ __device__ constexpr int xcd_chunks(int bid, int total)
 {
     constexpr int EACH = NUM_CU / NUM_XCD;
@@ -137,18 +138,102 @@ __device__ inline Split split_tiles(int total, int slots, int ktiles)
 // Expert e's rows.
 __device__ inline void find_rows(const int64_t *ends, int M, int e, int &lo, int &rows)
 {
-    const int lane = lane_id();
+    const int lane = lane_id(), end = group_end(ends, e + 1, M, e);
     int before = 0;
     for (int i = lane; i < e; i += 64)
         before = imax(before, group_end(ends, e, M, i));
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        before = imax(before, __shfl_xor(before, o));
-    lo = uniform(before);
-    rows = uniform(imax(group_end(ends, e + 1, M, e) - before, 0));
+    lo = __builtin_amdgcn_readlane(scan64(before, [](int x, int y) { return imax(x, y); }), 63);
+    rows = uniform(imax(end - lo, 0));
 }
 
 // ------------------------------------------------------------------ products
+// The tile product with one stage of LDS instead of rings: 128×128 in 32 KiB and at
+// most 128 registers, so that four workgroups run on a compute unit.  A workgroup
+// waits for each K-tile; the others' products, loads and stores fill the time.  For
+// short sums, where a tile's first loads and its stores take longer than its
+// products (dW from 128 rows in 8 experts of 14336×4096, 940 MB: 156 us, 302 with the
+// rings; from 4096 rows in 64 experts of 1024×2048 69 and 102, in 8 of 4096×4096 159 and
+// 190; dX of 8192 rows in the 64 85 and 92).
+template <typename E, bool TA, bool TB>
+struct OneStage : Tile<E, 128, 128, 2, 2, 2, TA, TB> {
+    using T = Tile<E, 128, 128, 2, 2, 2, TA, TB>;
+    using V8 = typename El<E>::v8;
+    static constexpr int LDS_ELEMS = T::STAGE_A + T::STAGE_B;
+    static constexpr bool FIRST = false;  // the partial K-tile comes last, masked
+    static_assert(T::BM * T::BN <= LDS_ELEMS, "the block's 16-bit image fits the stage");
+
+    // K a multiple of 8 where an operand is K-major
+    __device__ static __attribute__((always_inline)) void run(E *smem, const Operand &a, const Operand &b, int x0a,
+                                                              int x0b, int K, f32x4 (&acc)[T::TM][T::TN])
+    {
+        x0a = uniform(x0a), x0b = uniform(x0b), K = uniform(K);
+        const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / T::WN, wn = wave % T::WN;
+        E *const sa = smem, *const sb = smem + T::STAGE_A;
+        uint32_t a_off[T::PA], b_off[T::PB];
+        T::template dma_offsets<TA, T::BM>(a_off, a.ld, x0a, a.extent, lane, wave);
+        T::template dma_offsets<TB, T::BN>(b_off, b.ld, x0b, b.extent, lane, wave);
+        const char *const a_base = uniform(reinterpret_cast<const char *>(a.p) + 2 * (TA ? (int64_t)x0a : x0a * a.ld));
+        const char *const b_base = uniform(reinterpret_cast<const char *>(b.p) + 2 * (TB ? (int64_t)x0b : x0b * b.ld));
+        // a transposed operand's buffer ends with its last K row; a K-major one's
+        // chunks past K are masked
+        const auto rsrc = [](const char *base, int64_t ld, bool trans, int t, int k, int x0) {
+            return __builtin_amdgcn_make_buffer_rsrc((void *)(base + t * (trans ? 2 * BK * ld : 2 * BK)), (short)0,
+                                                     trans ? imax(k * (2 * (int)ld) - 2 * x0, 0) : DMA_RANGE, BUFFER_WORD3);
+        };
+        const int kc = 8 * ((lane & 7) ^ kmajor_swz(8 * wave + (lane >> 3)));
+        const auto read = [&](const E *st, auto trans, auto bx, int x, int kk) {
+            constexpr int BX = decltype(bx)::value;
+            if constexpr (decltype(trans)::value) {
+                const E *from = st + trans_off<BX>(8 * (lane >> 4) + ((lane & 15) >> 2), x + 4 * (lane & 3)) + kk * 32 * BX;
+                union {
+                    s16x4 h[2];
+                    V8 v;
+                } u;
+                u.h[0] = lds_read_tr(from);
+                u.h[1] = lds_read_tr(from + 4 * BX);
+                return u.v;
+            } else {
+                return *reinterpret_cast<const V8 *>(st + kmajor_off(x + (lane & 15), kk * 4 + (lane >> 4)));
+            }
+        };
+        for (int t = 0; t * BK < K; ++t) {
+            const int k = imin(K - t * BK, BK);
+            const auto ra = rsrc(a_base, a.ld, TA, t, k, x0a), rb = rsrc(b_base, b.ld, TB, t, k, x0b);
+            const bool past = kc >= k;
+            if (t > 0)
+                barrier_lds();  // every wave has read the K-tile before
+#pragma unroll
+            for (int p = 0; p < T::PA; ++p)
+                dma16(ra, sa + (p * T::NW + wave) * 512, !TA && past ? DMA_OOB : a_off[p]);
+#pragma unroll
+            for (int p = 0; p < T::PB; ++p)
+                dma16(rb, sb + (p * T::NW + wave) * 512, !TB && past ? DMA_OOB : b_off[p]);
+            wait_vmem<0>();
+            barrier_lds();
+            for (int kk = 0; kk < (k > 32 ? 2 : 1); ++kk) {
+                V8 fa[T::TM], fb[T::TN];
+#pragma unroll
+                for (int q = 0; q < T::TM; ++q)
+                    fa[q] = read(sa, std::bool_constant<TA>{}, std::integral_constant<int, T::BM>{}, wm * T::WTM + q * 16, kk);
+#pragma unroll
+                for (int q = 0; q < T::TN; ++q)
+                    fb[q] = read(sb, std::bool_constant<TB>{}, std::integral_constant<int, T::BN>{}, wn * T::WTN + q * 16, kk);
+#pragma unroll
+                for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < T::TN; ++j)
+                        acc[i][j] = El<E>::mfma(fb[j], fa[i], acc[i][j]);
+            }
+        }
+    }
+};
+// Waves of a tile's kernels on each SIMD unit.
+template <typename T>
+constexpr int waves_of()
+{
+    return T::LDS_ELEMS <= 128 * 128 ? 4 : T::BM * T::BN > 128 * 128 ? 1 : 2;
+}
+
 template <typename E, typename T>
 __device__ inline void store_tile(E *smem, const f32x4 (&acc)[T::TM][T::TN], E *D, int64_t ld, int m0, int n0, int rows,
                                   int cols, bool vec, bool nt)
@@ -266,7 +351,7 @@ __device__ inline Operand rows_of(const RowsArgs &a, const Tile2d &t, int k0)
 }
 // SPLIT: all whole rounds; the last one too where it is not cut into parts.
 template <typename E, typename T, bool SPLIT>
-__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_rows_kernel(
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(waves_of<T>()) void grouped_rows_kernel(
     RowsArgs a)
 {
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
@@ -295,7 +380,7 @@ __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 
 // hold them.  (A kernel of its own: both ends of the tile product in one spill
 // registers at 256×256.)
 template <typename E, typename T>
-__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_parts_kernel(
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(waves_of<T>()) void grouped_parts_kernel(
     RowsArgs a)
 {
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
@@ -340,7 +425,8 @@ __global__ __launch_bounds__(T::THREADS) void grouped_join_kernel(RowsArgs a)
 // 16 rows × 32 columns to a workgroup, whose eight waves take every eighth 128-K piece of
 // the sum straight from memory to registers, all loads of two pieces ahead of their
 // products, and add up in LDS at the end.  Bound by the latency of its few
-// dependent steps; TIME_FEW.
+// dependent steps (8 of 64 experts of 1024×2048 with a row each, weights not in the
+// caches: 12 us, 19 with 64×64 tiles; 16 rows of 8192×8192 35 and 43).
 constexpr int FEW_M = 16, FEW_N = 32, FEW_WAVES = 8, FEW_K = 128, FEW_AHEAD = 2;
 template <typename E>
 __device__ inline typename El<E>::v8 load_chunk(__amdgpu_buffer_rsrc_t r, uint32_t off)
@@ -437,7 +523,7 @@ struct WeightArgs {
     int parts;
 };
 template <typename E, typename T, bool PARTS>
-__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(T::BM *T::BN > 128 * 128 ? 1 : 2) void grouped_weight_kernel(
+__global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(waves_of<T>()) void grouped_weight_kernel(
     WeightArgs a)
 {
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
@@ -508,9 +594,10 @@ __global__ __launch_bounds__(256) void grouped_pack_kernel(PackArgs a)
         }
         const uint16_t *src = a.src + e * a.stride + r0 * a.ld;
         uint16_t *dst = a.dst + (e * a.per + r0) * a.cols8;
-#pragma unroll 4
-        for (int64_t i = threadIdx.x; i < (int64_t)n * chunks; i += 256) {
-            const int64_t r = i / chunks, c = (i - r * chunks) * 8;
+        // (fewer than 2^18 chunks a row, and more than one row only of up to 1024)
+#pragma unroll 2
+        for (int i = threadIdx.x; i < n * chunks; i += 256) {
+            const int r = i / chunks, c = (i - r * chunks) * 8;
             *reinterpret_cast<uint4 *>(dst + r * a.cols8 + c) = load8(src + r * a.ld, c, a.cols, false);
         }
     }
@@ -526,14 +613,44 @@ __global__ __launch_bounds__(256) void grouped_zero_kernel(uint16_t *d, int64_t 
 }
 
 // ------------------------------------------------------------------- plans
-enum Class { C256, C192, C128, C64, C64X128, CLASSES, FEW = CLASSES };
-const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x128", "16x32"};
-constexpr TileClass CLASS[] = {{256, 256, 1, 1.50, 1.50, 16.0},
-                               {192, 192, 1, 1.15, 1.15, 9.0},
-                               {128, 128, 2, 1.10, 0.50, 6.0},
-                               {64, 64, 2, 0.50, 0.27, 4.0},
-                               {64, 128, 2, 0.80, 0.45, 5.0},
-                               {FEW_M, FEW_N, 2, 0.0, 0.0, 0.0}};
+enum Class { C256, C192, C128, C64, C64X128, ONE, CLASSES, FEW = CLASSES };
+const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x128", "128x128x4", "16x32"};
+// Tiles, workgroups per compute unit, and microseconds: per K-tile with all of them
+// running and with one a unit, and per tile besides.  Here and below the numbers were
+// fitted to the times of every class for 760 problems on one MI355X (1 to 16384 rows, 1
+// to 128 experts, N and K from 64 to 14336, weights not in the caches): what is
+// chosen takes 2.5% (Y), 1.5% (dX) and 1.5% (dW) more than the best of them in the geometric
+// mean, at most 1.5 times as much.
+struct RowsModel {
+    TileClass c[CLASSES];
+    double more, tail;    // tile rows: how many more than of even shares, and of a share's last tile
+    double rate, reread;  // of the weights: bytes a microsecond; what an expert's second and third tile row add
+    double last, cut;     // what a last round takes beside the tiles in it, whole and in parts
+    double split, base;   // microseconds: of the two launches more, of any
+};
+constexpr RowsModel Y_MODEL = {{{256, 256, 1, 1.08, 1.08, 16.4},
+                                {192, 192, 1, 0.89, 0.84, 8.5},
+                                {128, 128, 2, 1.50, 0.71, 5.5},
+                                {64, 64, 2, 0.37, 0.28, 3.8},
+                                {64, 128, 2, 0.89, 0.59, 4.2},
+                                {128, 128, 4, 2.30, 1.05, 4.5}},
+                               1.11, 0.35, 4.4e6, 0.50, 0.60, 0.38, 11.8, 3.1};
+constexpr RowsModel DX_MODEL = {{{256, 256, 1, 1.54, 1.48, 14.5},
+                                 {},
+                                 {128, 128, 2, 0.92, 0.81, 7.9},
+                                 {64, 64, 2, 0.47, 0.29, 4.2},
+                                 {64, 128, 2, 0.85, 0.37, 4.4},
+                                 {128, 128, 4, 2.06, 1.77, 5.9}},
+                                1.49, 0.22, 4.8e6, 0.17, 0.41, 0.29, 8.1, 2.4};
+constexpr double STREAM_RATE = 5.8e6;
+// of dW, and the rate in TB/s at which it writes
+constexpr TileClass DW_CLASS[] = {{256, 256, 1, 1.26, 1.26, 16.4},
+                                  {192, 192, 1, 1.38, 0.94, 9.0},
+                                  {128, 128, 2, 0.95, 0.53, 5.9},
+                                  {64, 64, 2, 0.62, 0.30, 4.0},
+                                  {},
+                                  {128, 128, 4, 1.76, 1.38, 5.0}};
+constexpr double DW_RATE[] = {3.4, 2.6, 3.1, 1.5, 0.0, 5.9};
 template <typename E, bool TA, bool TB, typename F>
 bool with_tile(Class c, F f)
 {
@@ -547,6 +664,8 @@ bool with_tile(Class c, F f)
         [[fallthrough]];
     case C128:
         return f(Tile<E, 128, 128, 2, 2, 2, TA, TB, false, MASK>{});
+    case ONE:
+        return f(OneStage<E, TA, TB>{});
     case C64X128:
         if constexpr (!TA)
             return f(Tile<E, 64, 128, 1, 4, 3, TA, TB, STREAM, MASK>{});
@@ -563,7 +682,7 @@ struct Call {
 };
 struct Plan {
     Class c;
-    int64_t grid;
+    int64_t bm, bn, grid;
     bool pack_a, pack_b;
     int64_t a_cols, b_cols;  // of the operands' rows
     int64_t a_bytes, b_bytes;
@@ -571,49 +690,75 @@ struct Plan {
     int parts;               // dW: into how many its sums are cut
     int64_t parts_bytes;
 };
-constexpr double FEW_TILES = 512.0, SPLIT_US = 60.0;
 bool rows_ok(const void *p, int64_t ld, int64_t cols)
 {
     return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= MAX_DMA_LD;
 }
-// Time in microseconds of a product over rows: `hit` experts with some `each` rows,
-// `cols` columns, `ktiles` K-tiles.  Experts' shares are not even, so how many tile
-// rows there are is known to some 10%, and the last round is taken as half full.
-// Within some 15% of 8192 and 4096 rows in 64 experts of 1024×2048 in all classes, where
-// the ratios between them decide.
+// Time in microseconds of `n` tiles with `ktiles` K-tiles each; how many there are is
+// known to some 10% only, so that rounds are not counted whole.
+double rounds_time(const TileClass &c, double n, double ktiles, double last)
+{
+    const double slots = (double)NUM_CU * c.per_cu;
+    if (n > slots)
+        return (n / slots + last) * (ktiles * c.ktile + c.fixed);
+    return ktiles * (c.alone + (c.ktile - c.alone) * std::max(0.0, (n - NUM_CU) / std::max(1.0, slots - NUM_CU))) + c.fixed;
+}
 struct Estimate {
     double time;
     bool split;  // whether the last round, or the only one, is cut into parts
 };
-// Cutting takes two more launches and the parts' way through memory, some 12 us (and
-// 4 us where the groups then leave nothing to cut): it is for rounds that take
-// longer, and for few of them.
-Estimate rows_time(const TileClass &c, double hit, double each, int64_t cols, int64_t ktiles)
+// A product over M rows of E experts.  Weights are read for each tile row, but
+// mostly from a cache where they are shared; 64×128 tiles of Y stream them past the
+// caches, which is faster for one tile row an expert and much slower for several.
+// How many rows an expert has is known for one expert only.
+Estimate rows_time(const RowsModel &m, int cls, bool stream, int64_t M, int64_t E, int64_t cols, int64_t inner)
 {
-    const double n = 1.1 * hit * std::max(1.0, each / c.bm + 0.45) * (double)cdiv(cols, c.bn);
-    const double slots = (double)NUM_CU * c.per_cu, k = (double)ktiles;
-    if (n > slots)
-        return {(n / slots + 0.6) * (k * c.ktile + c.fixed), n <= 12.0 * slots && k * c.ktile >= SPLIT_US};
-    const double whole = k * (c.alone + (c.ktile - c.alone) * std::max(0.0, n - NUM_CU) / NUM_CU) + c.fixed;
-    const double parts = std::min(std::min(slots / n, k / MIN_PART), (double)MAX_PARTS);
-    const double cut = k * c.ktile / std::max(1.0, std::floor(parts)) + c.fixed + 12.0;
-    return {std::min(whole, cut), cut < whole || k * c.ktile >= SPLIT_US};
+    const TileClass &c = m.c[cls];
+    const double hit = (double)std::min(M, E), each = (double)M / hit;
+    const double tile_rows = E == 1 ? (double)cdiv(M, c.bm) : std::max(1.0, each / c.bm + m.tail);
+    const double n = (E == 1 ? 1.0 : m.more) * hit * tile_rows * (double)cdiv(cols, c.bn);
+    const double slots = (double)NUM_CU * c.per_cu, k = (double)cdiv(inner, BK);
+    const double weights = 2.0 * hit * (double)cols * (double)inner, others = 2.0 * (double)M * (double)(cols + inner);
+    const double again = stream ? 2.0 * (tile_rows - 1.0) * (tile_rows - 1.0) : m.reread * (std::min(tile_rows, 3.0) - 1.0);
+    const double memory = weights * (1.0 + again) / (stream ? STREAM_RATE : m.rate) + others / 5e6 + m.base;
+    const double whole = rounds_time(c, n, k, m.last);
+    double cut = 1e30;
+    if (n > slots) {
+        if (n <= 12.0 * slots)
+            cut = rounds_time(c, n, k, m.cut) + m.split;
+    } else {
+        const double parts = std::floor(std::min(std::min(slots / n, k / MIN_PART), (double)MAX_PARTS));
+        if (parts >= 2.0)
+            cut = k * c.ktile / parts + c.fixed + m.split;
+    }
+    const double a = std::max(whole, memory), b = std::max(cut, memory + 4.0);
+    return {std::min(a, b), b < a};
 }
-// dW's tiles and into how many parts its sums are cut, 1 or as many as fill the chip.
+double few_time(int64_t M, int64_t E, int64_t cols, int64_t inner)
+{
+    const double hit = (double)std::min(M, E), each = (double)M / hit;
+    const double tile_rows = E == 1 ? (double)cdiv(M, FEW_M) : std::max(1.0, each / FEW_M + Y_MODEL.tail);
+    const double n = hit * tile_rows * (double)cdiv(cols, FEW_N);
+    return std::max(1.1 + 3.5 * (double)cdiv(inner, 2048) * std::max(1.0, n / 512.0),
+                    2.0 * hit * (double)cols * (double)inner * tile_rows / 4.5e6 + Y_MODEL.base);
+}
+// dW, and into how many parts its sums are cut: 1, or as many as fill the chip.
 struct WeightEstimate {
     double time;
     int parts;
 };
-WeightEstimate weight_time(const TileClass &c, const Call &q)
+WeightEstimate weight_time(int cls, const Call &q)
 {
+    const TileClass &c = DW_CLASS[cls];
     const int64_t n = q.E * cdiv(q.N, c.bm) * cdiv(q.K, c.bn), ktiles = cdiv(cdiv(q.M, q.E), BK);
-    const int64_t slots = NUM_CU * c.per_cu;
-    const double whole = tile_time(c, n, ktiles);
-    const int64_t parts = std::min(std::min(slots / n, ktiles / MIN_PART), (int64_t)MAX_PARTS);
+    const double memory = 2.0 * (double)q.E * (double)q.N * (double)q.K / (DW_RATE[cls] * 1e6) + 4.0;
+    const double whole = std::max(rounds_time(c, (double)n, (double)ktiles, 0.55), memory);
+    const int64_t parts = std::min(std::min(NUM_CU * (int64_t)c.per_cu / n, ktiles / MIN_PART), (int64_t)MAX_PARTS);
     if (parts < 2)
         return {whole, 1};
     // the parts are written and read in fp32
-    const double cut = tile_time(c, n * parts, cdiv(ktiles, parts)) + 8.0 + (double)(n * parts * c.bm * c.bn) * 8.0 / 4e6;
+    const double cut = std::max(rounds_time(c, (double)(n * parts), (double)cdiv(ktiles, parts), 0.55), memory) + 1.7 +
+                       (double)(n * parts * c.bm * c.bn) * 8.0 / 4e6;
     return cut < whole ? WeightEstimate{cut, (int)parts} : WeightEstimate{whole, 1};
 }
 Plan make_plan(const Call &q)
@@ -630,36 +775,30 @@ Plan make_plan(const Call &q)
     const int64_t out = dx ? q.K : q.N, inner = dx ? q.N : q.K;
     if (dw) {
         int c = 0;
-        for (int i = 1; i < C64X128; ++i)
-            if (weight_time(CLASS[i], q).time < weight_time(CLASS[c], q).time)
+        for (int i = 1; i < CLASSES; ++i)
+            if (i != C64X128 && weight_time(i, q).time < weight_time(c, q).time)
                 c = i;
-        const int64_t n = q.E * cdiv(q.N, CLASS[c].bm) * cdiv(q.K, CLASS[c].bn);
-        p.c = (Class)c;
-        p.parts = weight_time(CLASS[c], q).parts;
-        p.grid = n * p.parts;
-        p.parts_bytes = p.parts > 1 ? 4 * p.grid * CLASS[c].bm * CLASS[c].bn : 0;
+        p.c = (Class)c, p.bm = DW_CLASS[c].bm, p.bn = DW_CLASS[c].bn;
+        p.parts = weight_time(c, q).parts;
+        p.grid = q.E * cdiv(q.N, p.bm) * cdiv(q.K, p.bn) * p.parts;
+        p.parts_bytes = p.parts > 1 ? 4 * p.grid * p.bm * p.bn : 0;
         return p;
     }
-    const double hit = (double)std::min(q.M, q.E), each = (double)q.M / hit;
-    const double few = hit * std::max(1.0, each / FEW_M + 0.45) * (double)cdiv(out, FEW_N);
-    bool split = false;
-    if (!dx && few <= FEW_TILES) {
-        p.c = FEW;
-    } else {
-        int c = 0;
-        const auto time = [&](int i) { return rows_time(CLASS[i], hit, each, out, cdiv(inner, BK)); };
-        for (int i = 1; i < CLASSES; ++i)
-            if (!(dx && i == C192) && time(i).time < time(c).time)
-                c = i;
-        p.c = (Class)c;
-        split = time(c).split;
-    }
-    const int64_t bm = CLASS[p.c].bm;
+    const auto time = [&](int i) {
+        return rows_time(dx ? DX_MODEL : Y_MODEL, i, !dx && i == C64X128, q.M, q.E, out, inner);
+    };
+    int c = 0;
+    for (int i = 1; i < CLASSES; ++i)
+        if (!(dx && i == C192) && time(i).time < time(c).time)
+            c = i;
+    const bool few = !dx && few_time(q.M, q.E, out, inner) < time(c).time, split = !few && time(c).split;
+    p.c = few ? FEW : (Class)c;
+    p.bm = few ? FEW_M : Y_MODEL.c[c].bm, p.bn = few ? FEW_N : Y_MODEL.c[c].bn;
     // each group adds at most bm - 1 rows to whole tiles
-    p.grid = (q.M + std::min(q.E + 1, q.M) * (bm - 1)) / bm * cdiv(out, CLASS[p.c].bn);
+    p.grid = (q.M + std::min(q.E + 1, q.M) * (p.bm - 1)) / p.bm * cdiv(out, p.bn);
     if (split) {
-        p.slots = NUM_CU * CLASS[p.c].per_cu;
-        p.parts_bytes = (int64_t)4 * p.slots * bm * CLASS[p.c].bn;
+        p.slots = NUM_CU * Y_MODEL.c[c].per_cu;
+        p.parts_bytes = (int64_t)4 * p.slots * p.bm * p.bn;
     }
     return p;
 }
@@ -743,7 +882,7 @@ int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_
         B = to, ldb = round_up(p.b_cols, 8), w_stride = q.N * ldb;
     }
     const bool vec = ldd % 8 == 0 && (uintptr_t)D % 16 == 0 && (!dw || q.E == 1 || d_stride % 8 == 0);
-    const bool nt = 2 * batch * rows * cols >= NT_BYTES;
+    const bool nt = 2 * batch * rows * cols >= NT_BYTES && ldd % 64 == 0 && (uintptr_t)D % 128 == 0;
     float *const sums = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + p.a_bytes + p.b_bytes);
     if (dw) {
         WeightArgs a = {};
@@ -751,7 +890,7 @@ int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_
         a.lddy = lda, a.ldx = ldb, a.lddw = ldd, a.dw_stride = q.E > 1 ? d_stride : 0;
         a.M = (int)q.M, a.E = (int)q.E, a.N = (int)q.N, a.K = (int)q.K;
         a.vec = vec, a.nt = nt;
-        a.tiles_m = (int)cdiv(q.N, CLASS[p.c].bm), a.tiles_n = (int)cdiv(q.K, CLASS[p.c].bn);
+        a.tiles_m = (int)cdiv(q.N, p.bm), a.tiles_n = (int)cdiv(q.K, p.bn);
         a.sums = sums, a.parts = p.parts;
         ok = ok && with_tile<E, true, true>(p.c, [&](auto t) {
             using T = decltype(t);
@@ -769,7 +908,7 @@ int product(const Call &q, const int64_t *ends, void *D, int64_t ldd, int64_t d_
         a.inner = (int)(y ? (p.pack_a || p.pack_b ? round_up(q.K, 8) : q.K) : q.N);
         a.w_extent = (int)(y ? q.N : q.K), a.cols = (int)cols;
         a.vec = vec, a.nt = nt;
-        a.tiles_n = (int)cdiv(cols, CLASS[p.c].bn);
+        a.tiles_n = (int)cdiv(cols, p.bn);
         a.parts = sums, a.slots = p.slots;
         const auto run = [&](auto t) {
             using T = decltype(t);

@@ -8,6 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 tg = pytest.importorskip("dense_fp16_gemm_02_amd")
 
+import grouped_cases as cases  # noqa: E402
 import training_oracle as oracle  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -76,6 +77,29 @@ def test_sizes(M, E, N, K, dtype):
 def test_odd_sizes(M, E, N, K, dtype):
     """Rows that are copied to aligned ones first."""
     check(*make(M, E, N, K, dtype))
+
+
+@pytest.mark.parametrize("kind", ["skewed", "behind", "first"])
+@pytest.mark.parametrize("case", cases.GROUPED, ids=lambda c: "x".join(map(str, c[:4])))
+def test_kernels(case, kind):
+    """Every kernel, its operands packed; the same sizes rounded up to a multiple of 8 take it as they lie."""
+    M, E, N, K = case[:4]
+    dtype = DTYPES[len(kind) % 2]
+    check(*make(M, E, N, K, dtype, kind))
+    if kind == "skewed":
+        check(*make(M, E, (N + 7) // 8 * 8, (K + 7) // 8 * 8, DTYPES[0], kind))
+
+
+@pytest.mark.parametrize("case", cases.LONG, ids=lambda c: c[4])
+def test_long_sums_of_dw(case):
+    M, E, N, K = case[:4]
+    X, W, ends, dY = make(M, E, N, K, torch.bfloat16)
+    w = W.requires_grad_()
+    dW, = torch.autograd.grad(tg.grouped_linear(X, w, ends), w, dY)
+    a = 0
+    for e, b in enumerate(ends.tolist()):
+        close(dW[e], *oracle._product(dY[a:b].t(), X[a:b], torch.bfloat16), "dW")
+        a = b
 
 
 @pytest.mark.parametrize("kind", ["even", "first", "last", "none", "behind", "skewed"])

@@ -103,12 +103,12 @@ def test_grouped_workspaces():
 
 
 @pytest.mark.parametrize("product,args,name", [
-    (tg.TG_GROUPED_Y, (A, A, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "y_16x64"),
+    (tg.TG_GROUPED_Y, (A, A, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "y_16x32"),
     (tg.TG_GROUPED_Y, (A, A, 16384, 8, 14336, 4096, 4096, 4096, 14336 * 4096), "y_256x256"),
-    (tg.TG_GROUPED_DX, (A, A, 16384, 8, 14336, 4096, 14336, 4096, 14336 * 4096), "dx_256x256"),
+    (tg.TG_GROUPED_DX, (A, A, 16384, 8, 14336, 4096, 14336, 4096, 14336 * 4096), "dx_256x256_split"),
     (tg.TG_GROUPED_DW, (A, A, 16384, 8, 14336, 4096, 14336, 4096, 0), "dw_256x256"),
-    (tg.TG_GROUPED_Y, (A, A + 2, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "pack_b y_16x64"),
-    (tg.TG_GROUPED_Y, (A + 2, A, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "pack_a y_16x64"),
+    (tg.TG_GROUPED_Y, (A, A + 2, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "pack_b y_16x32"),
+    (tg.TG_GROUPED_Y, (A + 2, A, 8, 64, 1024, 2048, 2048, 2048, 1024 * 2048), "pack_a y_16x32"),
     (tg.TG_GROUPED_Y, (A, A, 5, 0, 8, 16, 16, 16, 128), "zero"),
     (tg.TG_GROUPED_DX, (A, A, 5, 2, 0, 16, 0, 16, 0), "zero"),
     (tg.TG_GROUPED_DW, (A, A, 0, 2, 8, 16, 8, 16, 0), "zero"),
@@ -292,7 +292,7 @@ int main(void)
     tg_adamw_config c;
     int fails = 0;
     if (tg_grouped_plan(TG_GROUPED_Y, X, W, 8, 64, 1024, 2048, 2048, 2048, 2097152, name, sizeof name) != TG_OK) ++fails;
-    if (strcmp(name, "y_16x64") != 0) ++fails;
+    if (strcmp(name, "y_16x32") != 0) ++fails;
     if (tg_grouped_plan(TG_GROUPED_Y, X, W, 8, 64, 1024, 2048, 2048, 2048, 2097152, name, 4) != TG_OK || strcmp(name, "y_1") != 0) ++fails;
     if (tg_grouped_bf16(X, W, 0, 0, 4, 2, 8, 16, 16, 16, 128, 8, 0, 0, 0) != TG_ERR_INVALID_ARG) ++fails;
     if (tg_embedding_f16(0, W, 0, 4, 8, 16, 16, 16, 1.0f, 0) != TG_ERR_INVALID_ARG) ++fails;
