@@ -69,7 +69,8 @@ def test_tokens(M, V, K, kind):
 
 
 @pytest.mark.parametrize("M,V", [(8191, 100), (8192, 65535), (8193, 65536), (16384, 255), (16385, 256), (40000, 1 << 17),
-                                 (40000, (1 << 24) + 5), (100000, 2)])
+                                 (40000, (1 << 24) + 5), (100000, 2), (131072, 1000), (131073, 1000), (262145, 70000),
+                                 (524289, 300), (1500001, 100), (3000017, 1 << 19)])
 def test_sorts_of_every_length(M, V):
     """One workgroup's sort and several; one, two, three and four digits."""
     gen = torch.Generator().manual_seed(M + V)
