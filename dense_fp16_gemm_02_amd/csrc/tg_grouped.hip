@@ -619,7 +619,7 @@ const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x
 // running and with one a unit, and per tile besides.  Here and below the numbers were
 // fitted to the times of every class for 760 problems on one MI355X (1 to 16384 rows, 1
 // to 128 experts, N and K from 64 to 14336, weights not in the caches): what is
-// chosen takes 2.5% (Y), 1.5% (dX) and 1.5% (dW) more than the best of them in the geometric
+// chosen takes 2.3% (Y), 1.5% (dX) and 1.5% (dW) more than the best of them in the geometric
 // mean, at most 1.5 times as much.
 struct RowsModel {
     TileClass c[CLASSES];
@@ -632,7 +632,7 @@ constexpr RowsModel Y_MODEL = {{{256, 256, 1, 1.08, 1.08, 16.4},
                                 {192, 192, 1, 0.89, 0.84, 8.5},
                                 {128, 128, 2, 1.50, 0.71, 5.5},
                                 {64, 64, 2, 0.37, 0.28, 3.8},
-                                {64, 128, 2, 0.89, 0.59, 4.2},
+                                {64, 128, 2, 0.77, 0.50, 4.8},
                                 {128, 128, 4, 2.30, 1.05, 4.5}},
                                1.11, 0.35, 4.4e6, 0.50, 0.60, 0.38, 11.8, 3.1};
 constexpr RowsModel DX_MODEL = {{{256, 256, 1, 1.54, 1.48, 14.5},
@@ -642,7 +642,10 @@ constexpr RowsModel DX_MODEL = {{{256, 256, 1, 1.54, 1.48, 14.5},
                                  {64, 128, 2, 0.85, 0.37, 4.4},
                                  {128, 128, 4, 2.06, 1.77, 5.9}},
                                 1.49, 0.22, 4.8e6, 0.17, 0.41, 0.29, 8.1, 2.4};
-constexpr double STREAM_RATE = 5.8e6;
+// The 64×128 tiles of Y read W past the caches: its rate in whole 128-byte lines, and
+// where rows end within a line, which is then read for both (76 experts of 1600×1464 and
+// 2881 rows: 130 us, 108 with 64×64 tiles; 64 of 1024×2048 and 1100 rows: 47 and 67).
+constexpr double STREAM_RATE = 7.3e6, STREAM_RATE_CUT = 3.6e6;
 // of dW, and the rate in TB/s at which it writes
 constexpr TileClass DW_CLASS[] = {{256, 256, 1, 1.26, 1.26, 16.4},
                                   {192, 192, 1, 1.38, 0.94, 9.0},
@@ -711,7 +714,8 @@ struct Estimate {
 // mostly from a cache where they are shared; 64×128 tiles of Y stream them past the
 // caches, which is faster for one tile row an expert and much slower for several.
 // How many rows an expert has is known for one expert only.
-Estimate rows_time(const RowsModel &m, int cls, bool stream, int64_t M, int64_t E, int64_t cols, int64_t inner)
+// `stream`: that rate, or 0.
+Estimate rows_time(const RowsModel &m, int cls, double stream, int64_t M, int64_t E, int64_t cols, int64_t inner)
 {
     const TileClass &c = m.c[cls];
     const double hit = (double)std::min(M, E), each = (double)M / hit;
@@ -719,8 +723,8 @@ Estimate rows_time(const RowsModel &m, int cls, bool stream, int64_t M, int64_t 
     const double n = (E == 1 ? 1.0 : m.more) * hit * tile_rows * (double)cdiv(cols, c.bn);
     const double slots = (double)NUM_CU * c.per_cu, k = (double)cdiv(inner, BK);
     const double weights = 2.0 * hit * (double)cols * (double)inner, others = 2.0 * (double)M * (double)(cols + inner);
-    const double again = stream ? 2.0 * (tile_rows - 1.0) * (tile_rows - 1.0) : m.reread * (std::min(tile_rows, 3.0) - 1.0);
-    const double memory = weights * (1.0 + again) / (stream ? STREAM_RATE : m.rate) + others / 5e6 + m.base;
+    const double again = stream > 0.0 ? 1.4 * (tile_rows - 1.0) * (tile_rows - 1.0) : m.reread * (std::min(tile_rows, 3.0) - 1.0);
+    const double memory = weights * (1.0 + again) / (stream > 0.0 ? stream : m.rate) + others / 5e6 + m.base;
     const double whole = rounds_time(c, n, k, m.last);
     double cut = 1e30;
     if (n > slots) {
@@ -784,8 +788,10 @@ Plan make_plan(const Call &q)
         p.parts_bytes = p.parts > 1 ? 4 * p.grid * p.bm * p.bn : 0;
         return p;
     }
+    const int64_t row = p.pack_b ? round_up(q.K, 8) : q.ldb;
+    const double stream = row % 64 == 0 ? STREAM_RATE : STREAM_RATE_CUT;
     const auto time = [&](int i) {
-        return rows_time(dx ? DX_MODEL : Y_MODEL, i, !dx && i == C64X128, q.M, q.E, out, inner);
+        return rows_time(dx ? DX_MODEL : Y_MODEL, i, !dx && i == C64X128 ? stream : 0.0, q.M, q.E, out, inner);
     };
     int c = 0;
     for (int i = 1; i < CLASSES; ++i)
