@@ -50,7 +50,7 @@ __host__ __device__ inline Factors factors(double lr, double b1, double b2, doub
     f.keep = (float)(1.0 - lr * wd);
     f.rate = (float)(lr / (1.0 - pow(b1, t)));
     f.root = (float)(1.0 / sqrt(1.0 - pow(b2, t)));
-    f.eps = (float)eps;
+    f.eps = eps < 0x1p-126 ? 0.0f : (float)eps;  // a reciprocal takes no subnormal number
     return f;
 }
 

@@ -339,8 +339,8 @@ def grouped_linear(X, W, ends):
     rows behind the last end have one of 0 and reach no gradient.
 
     Runs on torch's current stream, never waits for the device, and takes its
-    workspace (none for 16-byte aligned rows and N, K that are multiples of 8) from
-    torch's allocator; it may be captured into a graph, whose replays read ``ends``
+    workspace (for operands without 16-byte aligned rows, and for sums cut into parts)
+    from torch's allocator; it may be captured into a graph, whose replays read ``ends``
     anew, its backward pass with torch.autograd.grad, or with .backward() where no
     eager graph of the same leaves is alive (autograd would accumulate on that graph's
     stream, which ends the capture).  Under torch.compile it runs between the
@@ -535,8 +535,12 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
     dev = params[0].device
     if not params[0].is_cuda:
         raise ValueError("params must be GPU tensors")
-    if any([t.is_sparse for t in grads]):
-        raise TypeError("grads must be dense")
+    try:
+        dense = not any([t.is_sparse for t in grads])
+    except AttributeError:  # None, where a parameter has no gradient
+        dense = False
+    if not dense:
+        raise TypeError("grads must be dense tensors")
     f32, half = torch.float32, {torch.float16, torch.bfloat16}
     p_type = _same_dtype(params, "params", {f32} | half)
     g_type = _same_dtype(grads, "grads", {f32} | half if p_type == f32 else {p_type})

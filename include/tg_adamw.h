@@ -11,7 +11,7 @@
  *
  * All of it in fp32, each operation rounded on its own, the quotient within 2 units
  * in the last place; the factors that depend on t, lr and β alone are computed in 64
- * bits and rounded once.  p of 16 bits
+ * bits and rounded once (an eps below 2^-126 counts as 0).  p of 16 bits
  * is rounded once when it is stored, to nearest: updates below half a step of p
  * are lost, which is why training keeps p in fp32 and lets the call write the
  * 16-bit copy that the model computes with.

@@ -37,8 +37,9 @@ enum { TG_GROUPED_Y = 0, TG_GROUPED_DX = 1, TG_GROUPED_DW = 2 };
  * tg_grouped_workspace_bytes — device memory that a call needs as workspace
  * (host-only); -1 if the arguments would be refused.  `product` is one of the above; A and
  * B with their leading dimensions are the call's first two operands: X and W (Y),
- * dY and W (DX), dY and X (DW).  0 where all of them have 16-byte aligned rows and N and
- * K are multiples of 8; otherwise they are copied into the workspace first.
+ * dY and W (DX), dY and X (DW).  Operands that have no 16-byte aligned rows, or N or K
+ * that is no multiple of 8, are copied into it first, and sums over K, N or the rows
+ * that are cut into parts leave these there in fp32; 0 where neither is so.
  * A workspace holds nothing between calls; calls that may overlap must not share one.
  */
 int64_t tg_grouped_workspace_bytes(int product, const void *A, const void *B, int64_t M, int64_t E, int64_t N,
@@ -64,7 +65,7 @@ int64_t tg_grouped_workspace_bytes(int product, const void *A, const void *B, in
  * misaligned pointer with elements behind it, a workspace that is NULL, misaligned
  * or too small), TG_ERR_TOO_LARGE (M >= 2^31, E >= 2^16, N or K >= 2^21, a leading
  * dimension >= 2^31, w_stride >= 2^42 or a product of 2^23 or more tiles, which
- * are of 16×64 to 256×256), TG_ERR_DEVICE or TG_ERR_LAUNCH.
+ * are of 16×32 to 256×256), TG_ERR_DEVICE or TG_ERR_LAUNCH.
  */
 int tg_grouped_f16(const void *X, const void *W, const int64_t *ends, void *Y, int64_t M, int64_t E, int64_t N,
                    int64_t K, int64_t ldx, int64_t ldw, int64_t w_stride, int64_t ldy, void *workspace,

@@ -313,3 +313,11 @@ def test_shared_memory_is_refused():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(before, [t for x in (p, g, m, v) for t in x])) and not base.any()
     tg.adamw(p, [g[0], g[0]], m, v, 1, **HOW)  # one gradient twice is read twice
+
+
+def test_an_eps_below_the_normal_numbers_counts_as_zero():
+    """Moments of zero: 0/eps is 0 at the smallest normal eps and 0/0 below it."""
+    for eps, nan in ((2.0 ** -126, False), (2.0 ** -127, True), (0.0, True)):
+        p, g, m, v = (torch.full((300,), x, device="cuda") for x in (2.0, 0.0, 0.0, 0.0))
+        tg.adamw([p], [g], [m], [v], 1, lr=0.5, eps=eps, weight_decay=0.0)
+        assert bool(p.isnan().all()) if nan else bool((p == 2).all())

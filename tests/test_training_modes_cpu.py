@@ -205,3 +205,11 @@ def test_refusals_of_adamw():
     with fwad.dual_level():
         with pytest.raises(NotImplementedError, match="forward-mode"):
             tg.adamw(p, [fwad.make_dual(g[0], g[0].clone())], m, v, 1)
+
+
+def test_a_parameter_without_a_gradient_is_refused():
+    def on_card():
+        return torch.zeros(4).as_subclass(OnCard)
+
+    with pytest.raises(TypeError, match="grads"):
+        tg.adamw([on_card(), on_card()], [on_card(), None], [on_card(), on_card()], [on_card(), on_card()], 1)
