@@ -207,6 +207,18 @@ def _cuda():
     return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
+@functools.lru_cache(maxsize=None)
+def _forward_ad():
+    from torch.autograd import forward_ad
+
+    return forward_ad
+
+
+def _refuse(what, *tensors):
+    """_refuse_modes, which asks each tensor for a tangent only where there can be any."""
+    _refuse_modes(what, *(tensors if _forward_ad()._current_level >= 0 else ()))
+
+
 def _call(index, fn, args, what):
     """fn(*args, stream) on torch's current stream of device ``index``, as the current device."""
     stream, device = _cuda()
@@ -316,7 +328,7 @@ def _grouped_function():
         @staticmethod
         def backward(ctx, dY):
             X, W, ends = ctx.saved_tensors
-            _refuse_modes("grouped_linear (backward)", dY)
+            _refuse("grouped_linear (backward)", dY)
             gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
             need = ctx.needs_input_grad
             return (*gradients(X, W, ends, _rows(dY), ctx.strides, need[0], need[1]), None, None)
@@ -366,7 +378,7 @@ def grouped_linear(X, W, ends):
     if ends.shape[0] != W.shape[0]:
         raise ValueError(f"{ends.shape[0]} ends for {W.shape[0]} experts")
     strides = (_row_stride(X, "X", X.shape[1]), *_weight_strides(W))
-    _refuse_modes("grouped_linear", X, W)
+    _refuse("grouped_linear", X, W)
     ends = ends.contiguous()
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         return _grouped_function().apply(X, W, ends, strides)
@@ -431,7 +443,7 @@ def _embedding_function():
         @staticmethod
         def backward(ctx, dY):
             tokens, = ctx.saved_tensors
-            _refuse_modes("embedding (backward)", dY)
+            _refuse("embedding (backward)", dY)
             gradient = Gradient.apply if torch.is_grad_enabled() else _embedding_backward
             return None, gradient(tokens, dY, *ctx.how), None, None, None
 
@@ -475,7 +487,7 @@ def embedding(tokens, W, scale: float = 1.0, padding_idx: int | None = None):
     if padding_idx is not None and not 0 <= padding_idx < V:
         raise ValueError(f"padding_idx must be in [0, {V})")
     ldw = _row_stride(W, "W", K)
-    _refuse_modes("embedding", W)
+    _refuse("embedding", W)
     tokens = tokens.contiguous()
     if torch.is_grad_enabled() and W.requires_grad:
         return _embedding_function().apply(tokens, W, ldw, float(scale), -1 if padding_idx is None else padding_idx)
@@ -487,14 +499,6 @@ def _adamw_types():
     import torch
 
     return {torch.float32: TG_ADAMW_F32, torch.float16: TG_ADAMW_F16, torch.bfloat16: TG_ADAMW_BF16}
-
-
-@functools.lru_cache(maxsize=None)
-def _adamw_tools():
-    import torch
-    from torch.autograd import forward_ad
-
-    return forward_ad, torch.autograd.graph.increment_version
 
 
 def _same_dtype(ts, name, allowed):
@@ -554,8 +558,7 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
         if p_type != f32:
             raise ValueError("copies are for float32 parameters")
         copy_type = _same_dtype(lists[-1], "copies", half)
-    dual_level, increment_version = _adamw_tools()
-    _refuse_modes(what, *(params + grads if dual_level._current_level >= 0 else ()))
+    _refuse(what, *params, *grads)
     index, sizes = dev.index, [p.numel() for p in params]
     blocks = [(n + TG_ADAMW_BLOCK - 1) // TG_ADAMW_BLOCK for n in sizes] if scales else None
     for k, x in enumerate(lists):
@@ -588,7 +591,7 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
         table[6::8] = array.array("q", [t.data_ptr() for t in lists[-1]])
     table[7::8] = array.array("q", sizes)
     _call(index, _lib().tg_adamw, (table.buffer_info()[0], count, ctypes.byref(config)), what)
-    increment_version([t for x in written for t in x])
+    torch.autograd.graph.increment_version([t for x in written for t in x])
 
 
 def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
