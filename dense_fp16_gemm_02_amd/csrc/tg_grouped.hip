@@ -619,7 +619,7 @@ const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x
 // running and with one a unit, and per tile besides.  Here and below the numbers were
 // fitted to the times of every class for 760 problems on one MI355X (1 to 16384 rows, 1
 // to 128 experts, N and K from 64 to 14336, weights not in the caches): what is
-// chosen takes 2.3% (Y), 1.5% (dX) and 1.5% (dW) more than the best of them in the geometric
+// chosen takes 2.5% (Y), 1.7% (dX) and 1.5% (dW) more than the best of them in the geometric
 // mean, at most 1.5 times as much.
 struct RowsModel {
     TileClass c[CLASSES];
@@ -634,7 +634,7 @@ constexpr RowsModel Y_MODEL = {{{256, 256, 1, 1.08, 1.08, 16.4},
                                 {64, 64, 2, 0.37, 0.28, 3.8},
                                 {64, 128, 2, 0.77, 0.50, 4.8},
                                 {128, 128, 4, 2.30, 1.05, 4.5}},
-                               1.11, 0.35, 4.4e6, 0.50, 0.60, 0.38, 11.8, 3.1};
+                               1.11, 0.35, 4.4e6, 0.50, 0.60, 0.38, 12.5, 3.1};
 constexpr RowsModel DX_MODEL = {{{256, 256, 1, 1.54, 1.48, 14.5},
                                  {},
                                  {128, 128, 2, 0.92, 0.81, 7.9},
