@@ -504,10 +504,11 @@ def _adamw_types():
 def _same_dtype(ts, name, allowed):
     """The dtype that all of ts have, one of ``allowed``."""
     dtypes = {t.dtype for t in ts}
-    if len(dtypes) != 1 or not dtypes <= allowed:
+    dtype = dtypes.pop()
+    if dtypes or dtype not in allowed:
         raise TypeError(f"{name} must all be of one dtype among "
                         f"{', '.join(sorted(str(d).replace('torch.', '') for d in allowed))}")
-    return dtypes.pop()
+    return dtype
 
 
 def _scalar(x, name, dtype, dev):
@@ -532,7 +533,7 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
     lists = [list(params), list(grads)] + [list(x) for x in moments + scales] + ([list(copies)] if copies is not None else [])
     params, grads = lists[:2]
     count = len(params)
-    if any(len(x) != count for x in lists):
+    if any([len(x) != count for x in lists]):
         raise ValueError("there must be as many gradients, moments and copies as parameters")
     if count == 0:
         return
@@ -545,35 +546,36 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
         dense = False
     if not dense:
         raise TypeError("grads must be dense tensors")
-    f32, half = torch.float32, {torch.float16, torch.bfloat16}
-    p_type = _same_dtype(params, "params", {f32} | half)
-    g_type = _same_dtype(grads, "grads", {f32} | half if p_type == f32 else {p_type})
-    for x, name in zip(lists[2:4], ("exp_avgs", "exp_avg_sqs") if bits == 32 else ("exp_avgs", "roots")):
-        _same_dtype(x, name, {f32} if bits == 32 else {torch.float8_e4m3fn})
+    f32, half = torch.float32, (torch.float16, torch.bfloat16)
+    p_type = _same_dtype(params, "params", (f32, *half))
+    g_type = _same_dtype(grads, "grads", (f32, *half) if p_type is f32 else (p_type,))
+    held = f32 if bits == 32 else torch.float8_e4m3fn
+    _same_dtype(lists[2], "exp_avgs", (held,))
+    _same_dtype(lists[3], "exp_avg_sqs" if bits == 32 else "roots", (held,))
     if scales:
-        for x, name in zip(lists[4:6], ("exp_avg_scales", "root_scales")):
-            _same_dtype(x, name, {f32})
+        _same_dtype(lists[4] + lists[5], "exp_avg_scales and root_scales", (f32,))
     copy_type = None
     if copies is not None:
-        if p_type != f32:
+        if p_type is not f32:
             raise ValueError("copies are for float32 parameters")
         copy_type = _same_dtype(lists[-1], "copies", half)
     _refuse(what, *params, *grads)
+    # every list's tensors in a row, so that each question is asked in one pass
     index, sizes = dev.index, [p.numel() for p in params]
-    blocks = [(n + TG_ADAMW_BLOCK - 1) // TG_ADAMW_BLOCK for n in sizes] if scales else None
-    for k, x in enumerate(lists):
-        want = blocks if scales and k in (4, 5) else sizes
-        if [t.numel() for t in x] != want:
-            raise ValueError("gradients, moments and copies must have as many elements as their parameter"
-                             + (f", scales one for each {TG_ADAMW_BLOCK} of them" if scales else ""))
-        if not all([t.is_contiguous() for t in x]):
-            raise ValueError("parameters, gradients, moments and copies must be contiguous")
-        if {t.get_device() for t in x} != {index}:
-            raise ValueError("all tensors must be on one GPU")
+    every, want = [t for x in lists for t in x], sizes * len(lists)
+    if scales:
+        want[4 * count:6 * count] = [(n + TG_ADAMW_BLOCK - 1) // TG_ADAMW_BLOCK for n in sizes] * 2
+    if [t.numel() for t in every] != want:
+        raise ValueError("gradients, moments and copies must have as many elements as their parameter"
+                         + (f", scales one for each {TG_ADAMW_BLOCK} of them" if scales else ""))
+    if not all([t.is_contiguous() for t in every]):
+        raise ValueError("parameters, gradients, moments and copies must be contiguous")
+    if {t.get_device() for t in every} != {index}:
+        raise ValueError("all tensors must be on one GPU")
     if [g.shape for g in grads] != [p.shape for p in params]:
         raise ValueError("a gradient has another shape than its parameter")
-    written = lists[:1] + lists[2:]
-    if torch.is_grad_enabled() and not all([t.is_leaf for x in written for t in x if t.requires_grad]):
+    written = params + every[2 * count:]
+    if torch.is_grad_enabled() and not all([t.is_leaf for t in written if t.requires_grad]):
         raise ValueError("params, moments and copies that are results of autograd cannot be updated in place")
     types = _adamw_types()
     b1, b2 = betas
@@ -584,14 +586,13 @@ def _adamw(what, params, grads, moments, scales, step, lr, betas, eps, weight_de
     if g_scale is not None and not isinstance(g_scale, torch.Tensor):
         raise TypeError("grad_scale must be a tensor")
     # tg_adamw_tensor structures: eight words each, a word of all of them at a time
-    table = array.array("q", bytes(64 * count))
-    for word, x in zip((0, 1, 2, 3, 4, 5) if scales else (0, 1, 2, 3), lists):
-        table[word::8] = array.array("q", [t.data_ptr() for t in x])
-    if copies is not None:
-        table[6::8] = array.array("q", [t.data_ptr() for t in lists[-1]])
+    table, at = array.array("q", bytes(64 * count)), array.array("q", [t.data_ptr() for t in every])
+    for k, word in enumerate((0, 1, 2, 3, 4, 5, 6) if scales else (0, 1, 2, 3, 6)):
+        if k < len(lists):
+            table[word::8] = at[k * count:(k + 1) * count]
     table[7::8] = array.array("q", sizes)
     _call(index, _lib().tg_adamw, (table.buffer_info()[0], count, ctypes.byref(config)), what)
-    torch.autograd.graph.increment_version([t for x in written for t in x])
+    torch.autograd.graph.increment_version(written)
 
 
 def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
