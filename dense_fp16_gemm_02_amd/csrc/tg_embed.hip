@@ -114,9 +114,13 @@ __global__ __launch_bounds__(LOOK_THREADS) void embedding_kernel(LookArgs a)
 // -------------------------------------------------------------------- sort
 // A stable radix sort in as few passes as digits of up to 9 bits allow (two for
 // up to 2^18 rows).
-constexpr int SORT_PER = 8;              // pairs of a lane
 constexpr int DIGIT_BITS = 9, DIGITS = 1 << DIGIT_BITS;
 constexpr int FEW = 256, MANY = 1024;    // threads of a workgroup
+// Pairs of a lane, which are ordered 64 to a round: half as many where small workgroups
+// are there to spread the rounds over the chip (65536 tokens, lookup and gradient, 194 us,
+// 198 with eight).  Bound by the latency of the rounds: a pass over 65536 pairs some 14 us,
+// the two of one workgroup's 8192 22 us.
+constexpr int sort_per(int threads) { return threads == FEW ? 4 : 8; }
 struct SortArgs {
     const int64_t *tokens;          // first pass
     const uint32_t *key_in, *at_in; // later passes
@@ -177,10 +181,10 @@ __device__ inline uint32_t sum_before(uint32_t x, uint32_t *wave_sum)
 // by digit and, within one, as they came.  Lanes of a wave that hold the same
 // digit find each other with one ballot per bit.
 template <int THREADS>
-__device__ inline void sort_places(SortShared<THREADS> &s, const uint32_t (&key)[SORT_PER], int items, int shift, int bits,
-                                   uint32_t (&place)[SORT_PER])
+__device__ inline void sort_places(SortShared<THREADS> &s, const uint32_t (&key)[sort_per(THREADS)], int items,
+                                   int shift, int bits, uint32_t (&place)[sort_per(THREADS)])
 {
-    constexpr int WAVES = THREADS / 64;
+    constexpr int WAVES = THREADS / 64, PER = sort_per(THREADS);
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), per = wave_items<THREADS>(items);
     const uint32_t mask = (1u << bits) - 1;
     for (int d = lane; d < DIGITS; d += 64)
@@ -188,7 +192,7 @@ __device__ inline void sort_places(SortShared<THREADS> &s, const uint32_t (&key)
     __builtin_amdgcn_wave_barrier();
     volatile uint32_t *mine = s.wave_count[wave];
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r) {
+    for (int r = 0; r < PER; ++r) {
         place[r] = 0;
         if (sort_item(wave, 0, r, per) >= items)  // the same for the whole wave
             continue;
@@ -230,21 +234,22 @@ __device__ inline void sort_places(SortShared<THREADS> &s, const uint32_t (&key)
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r)
+    for (int r = 0; r < PER; ++r)
         place[r] += s.wave_count[wave][(key[r] >> shift) & mask];
 }
 
-// All passes of at most MANY·SORT_PER tokens, by one workgroup.
-constexpr int SORT_SMALL = MANY * SORT_PER;
+// All passes of at most SORT_SMALL tokens, by one workgroup.
+constexpr int SORT_SMALL = MANY * sort_per(MANY);
 __global__ __launch_bounds__(MANY) void sort_small_kernel(SortArgs a)
 {
+    constexpr int PER = sort_per(MANY);
     __shared__ SortShared<MANY> s;
     __shared__ uint32_t keys[SORT_SMALL], ats[SORT_SMALL];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int per = wave_items<MANY>(a.M);
-    uint32_t key[SORT_PER], at[SORT_PER], place[SORT_PER];
+    uint32_t key[PER], at[PER], place[PER];
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int i = sort_item(wave, lane, r, per);
         key[r] = i < a.M ? token_key(a, i) : 0;
         at[r] = (uint32_t)i;
@@ -252,14 +257,14 @@ __global__ __launch_bounds__(MANY) void sort_small_kernel(SortArgs a)
     for (int p = 0; p < a.passes; ++p) {
         sort_places<MANY>(s, key, a.M, a.bits * p, a.bits, place);
 #pragma unroll
-        for (int r = 0; r < SORT_PER; ++r)
+        for (int r = 0; r < PER; ++r)
             if (sort_item(wave, lane, r, per) < a.M) {
                 keys[place[r]] = key[r];
                 ats[place[r]] = at[r];
             }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < SORT_PER; ++r) {
+        for (int r = 0; r < PER; ++r) {
             const int i = sort_item(wave, lane, r, per);
             if (i < a.M) {
                 key[r] = keys[i];
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(MANY) void sort_small_kernel(SortArgs a)
         __syncthreads();
     }
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int i = sort_item(wave, lane, r, per);
         if (i < a.M) {
             a.key[i] = key[r];
@@ -282,15 +287,16 @@ __global__ __launch_bounds__(MANY) void sort_small_kernel(SortArgs a)
 template <int THREADS, bool FIRST>
 __global__ __launch_bounds__(THREADS) void sort_count_kernel(SortArgs a)
 {
+    constexpr int PER = sort_per(THREADS);
     __shared__ uint32_t count[DIGITS];
     const int tid = threadIdx.x;
     for (int d = tid; d < DIGITS; d += THREADS)
         count[d] = 0;
     __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * SORT_PER);
+    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * PER);
     const uint32_t mask = (1u << a.bits) - 1;
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int64_t i = i0 + r * THREADS + tid;
         if (i < a.M)
             atomicAdd(&count[((FIRST ? token_key(a, (int)i) : a.key_in[i]) >> a.shift) & mask], 1u);
@@ -334,14 +340,15 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(SortArgs a)
 template <int THREADS, bool FIRST>
 __global__ __launch_bounds__(THREADS) void sort_scatter_kernel(SortArgs a)
 {
+    constexpr int PER = sort_per(THREADS);
     __shared__ SortShared<THREADS> s;
     __shared__ uint32_t part[2][THREADS > DIGITS ? THREADS : DIGITS];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * SORT_PER);
-    const int items = (int)(a.M - i0 < THREADS * SORT_PER ? a.M - i0 : THREADS * SORT_PER), per = wave_items<THREADS>(items);
-    uint32_t key[SORT_PER], at[SORT_PER], place[SORT_PER];
+    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * PER);
+    const int items = (int)(a.M - i0 < THREADS * PER ? a.M - i0 : THREADS * PER), per = wave_items<THREADS>(items);
+    uint32_t key[PER], at[PER], place[PER];
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int i = sort_item(wave, lane, r, per);
         key[r] = i < items ? (FIRST ? token_key(a, (int)(i0 + i)) : a.key_in[i0 + i]) : 0;
         at[r] = i < items ? (FIRST ? (uint32_t)(i0 + i) : a.at_in[i0 + i]) : 0;
@@ -392,7 +399,7 @@ __global__ __launch_bounds__(THREADS) void sort_scatter_kernel(SortArgs a)
     sort_places<THREADS>(s, key, items, a.shift, a.bits, place);
     // (behind sort_places wave_count[0][d] is the digit's first place in the workgroup)
 #pragma unroll
-    for (int r = 0; r < SORT_PER; ++r)
+    for (int r = 0; r < PER; ++r)
         if (sort_item(wave, lane, r, per) < items) {
             const uint32_t d = (key[r] >> a.shift) & ((1u << a.bits) - 1);
             const uint32_t to = s.base[d] + place[r] - s.wave_count[0][d];
@@ -435,6 +442,8 @@ __device__ inline int walk_tokens(const uint32_t *key, int64_t M, int64_t V, int
     }
     return uniform((int)lo);
 }
+// Bound by memory: dW of 131072×4096 bf16 from 8192 rows 225 us (5.1 TB/s), of 32000×2048
+// fp16 from 65536 rows 80 us (4.8 TB/s).
 template <typename E>
 __global__ __launch_bounds__(WALK_THREADS) void embedding_walk_kernel(WalkArgs a)
 {
@@ -636,10 +645,10 @@ int lookup(const int64_t *tokens, const void *W, void *Y, int64_t M, int64_t V, 
 }
 
 // Of more workgroups than these, sums over their counts are made once, by a kernel of its
-// own, and not by each of them.  Whole gradients of 64 columns without and with it: 2^20
-// tokens (128 workgroups) 704 and 709 us, 2^22 (512) 2465 and 2448, 2^24 (2048) 9093 and
-// 8720; what it saves grows with the square.
-constexpr int SCAN_TILES = 256;
+// own, and not by each of them.  Without and with it: 2^20 tokens of 256 columns (128
+// workgroups) 704 and 709 us, 200000 of 1024 (196) 317 and 310, 2^22 of 64 (512) 2465 and
+// 2448, 2^24 (2048) 9093 and 8720; what it saves grows with the square.
+constexpr int SCAN_TILES = 128;
 struct Plan {
     int passes, bits, tiles, threads;  // of the sort
     int piece, pieces;       // of the walk
@@ -664,8 +673,8 @@ Plan make_plan(int64_t M, int64_t V, int64_t K)
     p.passes = (int)cdiv(bits, DIGIT_BITS);
     p.bits = (int)cdiv(bits, p.passes);
     // small workgroups spread a short sort over the chip; a long one takes large ones
-    p.threads = M <= SORT_SMALL || M > 128 * FEW * SORT_PER ? MANY : FEW;
-    p.tiles = (int)cdiv(M, p.threads * SORT_PER);
+    p.threads = M <= SORT_SMALL || M > 256 * FEW * sort_per(FEW) ? MANY : FEW;
+    p.tiles = (int)cdiv(M, p.threads * sort_per(p.threads));
     const int64_t segments = cdiv(K, 64 * 4);  // of the widest type
     p.piece = cdiv(M + V, 32) * segments <= 16384 ? 32 : 64;
     while (p.piece < 256 && cdiv(M + V, p.piece) * segments > (int64_t)1 << 22)
