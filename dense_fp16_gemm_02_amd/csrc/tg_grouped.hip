@@ -622,7 +622,7 @@ const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x
 // running and with one a unit, and per tile besides.  Here and below the numbers were
 // fitted to the times of every class for 760 problems on one MI355X (1 to 16384 rows, 1
 // to 128 experts, N and K from 64 to 14336, weights not in the caches): what is
-// chosen takes 2.5% (Y), 1.7% (dX) and 1.5% (dW) more than the best of them in the geometric
+// chosen takes 2.5% (Y), 1.5% (dX) and 1.5% (dW) more than the best of them in the geometric
 // mean, at most 1.5 times as much.
 struct RowsModel {
     TileClass c[CLASSES];
@@ -638,13 +638,13 @@ constexpr RowsModel Y_MODEL = {{{256, 256, 1, 1.08, 1.08, 16.4},
                                 {64, 128, 2, 0.77, 0.50, 4.8},
                                 {128, 128, 4, 2.30, 1.05, 4.5}},
                                1.11, 0.35, 4.4e6, 0.50, 0.60, 0.38, 12.5, 3.1};
-constexpr RowsModel DX_MODEL = {{{256, 256, 1, 1.54, 1.48, 14.5},
+constexpr RowsModel DX_MODEL = {{{256, 256, 1, 1.52, 1.52, 15.1},
                                  {},
-                                 {128, 128, 2, 0.92, 0.81, 7.9},
-                                 {64, 64, 2, 0.47, 0.29, 4.2},
-                                 {64, 128, 2, 0.85, 0.37, 4.4},
-                                 {128, 128, 4, 2.06, 1.77, 5.9}},
-                                1.49, 0.22, 4.8e6, 0.17, 0.41, 0.29, 8.1, 2.4};
+                                 {128, 128, 2, 0.92, 0.92, 8.4},
+                                 {64, 64, 2, 0.45, 0.36, 4.9},
+                                 {64, 128, 2, 0.81, 0.40, 5.0},
+                                 {128, 128, 4, 2.06, 2.06, 5.7}},
+                                1.53, 0.26, 5.8e6, 1.03, 0.36, 0.24, 8.6, 4.0};
 // The 64×128 tiles of Y read W past the caches: its rate in whole 128-byte lines, and
 // where rows end within a line, which is then read for both (76 experts of 1600×1464 and
 // 2881 rows: 130 us, 108 with 64×64 tiles; 64 of 1024×2048 and 1100 rows: 47 and 67).

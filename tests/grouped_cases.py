@@ -14,8 +14,8 @@ GROUPED = [
     (12190, 5, 8, 79, "pack_a pack_b y_64x64", "pack_b dx_64x128", "pack_b dw_64x64_split"),
     (405, 5, 8, 10340, "pack_a pack_b y_64x64_split", "pack_b dx_128x128x4", "pack_b dw_128x128"),
     (25, 20, 11335, 73, "pack_a pack_b y_128x128x4", "pack_a pack_b dx_64x128_split", "pack_a pack_b dw_128x128x4"),
-    (1, 1, 7761, 7684, "pack_a pack_b y_16x32", "pack_a pack_b dx_128x128_split", "pack_a pack_b dw_128x128x4"),
-    (2, 1, 11280, 6398, "pack_a pack_b y_64x128_split", "pack_b dx_128x128_split", "pack_b dw_128x128x4"),
+    (1, 1, 7761, 7684, "pack_a pack_b y_16x32", "pack_a pack_b dx_64x64_split", "pack_a pack_b dw_128x128x4"),
+    (2, 1, 11280, 6398, "pack_a pack_b y_64x128_split", "pack_b dx_64x64_split", "pack_b dw_128x128x4"),
     (13244, 5, 130, 147, "pack_a pack_b y_128x128", "pack_a pack_b dx_128x128", "pack_a pack_b dw_64x64_split"),
     (7789, 5, 6834, 8, "y_128x128x4", "pack_a dx_128x128x4_split", "pack_a dw_128x128"),
     (9722, 70, 419, 488, "y_192x192", "pack_a dx_128x128x4", "pack_a dw_128x128x4"),
@@ -24,7 +24,9 @@ GROUPED = [
     (6094, 1, 70, 10950, "pack_a pack_b y_128x128x4_split", "pack_a pack_b dx_128x128x4", "pack_a pack_b dw_128x128_split"),
     (8120, 70, 756, 823, "pack_a pack_b y_256x256", "pack_a pack_b dx_128x128x4", "pack_a pack_b dw_128x128x4"),
     (11614, 2, 4052, 165, "pack_a pack_b y_128x128x4", "pack_a pack_b dx_256x256_split", "pack_a pack_b dw_192x192_split"),
-    (1609, 9, 1230, 4700, "pack_a pack_b y_256x256_split", "pack_a pack_b dx_256x256", "pack_a pack_b dw_128x128x4"),
+    (1609, 9, 1230, 4700, "pack_a pack_b y_256x256_split", "pack_a pack_b dx_128x128x4", "pack_a pack_b dw_128x128x4"),
+    (1, 1, 9216, 9889, "pack_a pack_b y_16x32", "pack_b dx_128x128_split", "pack_b dw_128x128x4"),
+    (2296, 5, 1163, 3962, "pack_a pack_b y_256x256_split", "pack_a pack_b dx_256x256", "pack_a pack_b dw_128x128x4"),
     (16381, 9, 168, 6432, "y_256x256_split", "dx_128x128x4", "dw_256x256"),
 ]
 # the kernels of dW for so many rows that only dW is compared
