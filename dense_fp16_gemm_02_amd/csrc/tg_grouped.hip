@@ -350,9 +350,8 @@ __device__ inline Operand rows_of(const RowsArgs &a, const Tile2d &t, int k0)
     return {reinterpret_cast<const uint16_t *>(a.a) + (int64_t)t.lo * a.lda + k0, a.lda, t.rows};
 }
 // SPLIT: all whole rounds; the last one too where it is not cut into parts.  16384 rows of 8
-// experts of 14336×4096 bf16: Y 1500-1540 us, matrix cores busy 0.78 of the waves' time under
-// the power limit; dX 1550-1640 us and 160 for its last round, busy 0.63 (one operand's
-// fragments take two transposed reads each).
+// experts of 14336×4096 bf16: Y 1500-1540 us, dX 1320-1400 and 145 for its last round,
+// matrix cores busy 0.78 of the waves' time under the power limit.
 template <typename E, typename T, bool SPLIT>
 __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(waves_of<T>()) void grouped_rows_kernel(
     RowsArgs a)
