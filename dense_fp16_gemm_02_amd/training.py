@@ -208,15 +208,20 @@ def _cuda():
 
 
 @functools.lru_cache(maxsize=None)
-def _forward_ad():
+def _queries():
+    """torch.jit.is_tracing, whether any dispatch mode is on, and forward mode's levels."""
+    import torch
     from torch.autograd import forward_ad
+    from torch.utils._python_dispatch import is_in_torch_dispatch_mode
 
-    return forward_ad
+    return torch.jit.is_tracing, is_in_torch_dispatch_mode, forward_ad
 
 
 def _refuse(what, *tensors):
-    """_refuse_modes, which asks each tensor for a tangent only where there can be any."""
-    _refuse_modes(what, *(tensors if _forward_ad()._current_level >= 0 else ()))
+    """_refuse_modes where there is any mode to refuse: a trace, or a level of dual tensors."""
+    is_tracing, in_any_mode, forward_ad = _queries()
+    if is_tracing() or in_any_mode() or forward_ad._current_level >= 0:
+        _refuse_modes(what, *tensors)
 
 
 def _call(index, fn, args, what):
@@ -255,11 +260,16 @@ def _grouped_call(product, A, B, lda, ldb, w_stride, ends, D, N, K, ldd, d_strid
           "grouped_linear (backward)" if product else "grouped_linear")
 
 
-def _bytes(like, size):
-    """A workspace on the device of ``like``."""
+@functools.lru_cache(maxsize=None)
+def _uint8():
     import torch
 
-    return torch.empty(size, dtype=torch.uint8, device=like.device)
+    return torch.uint8
+
+
+def _bytes(like, size):
+    """A workspace on the device of ``like``."""
+    return like.new_empty((size,), dtype=_uint8())
 
 
 def _weight_strides(W):
@@ -284,14 +294,17 @@ def _grouped_forward(X, W, ends, strides):
 def _grouped_backward(X, W, ends, dY, strides, need_x, need_w):
     N, K = W.shape[1:]
     ldx, ldw, w_stride = strides
-    ldy = _row_stride(dY, "dY", N)
+    ldy, ldk = N or 1, K or 1
+    if not dY.is_contiguous():
+        dY = _rows(dY)
+        ldy = _row_stride(dY, "dY", N)
     dX = dW = None
     if need_x:
         dX = X.new_empty(X.shape)
-        _grouped_call(TG_GROUPED_DX, dY, W, ldy, ldw, w_stride, ends, dX, N, K, max(K, 1))
+        _grouped_call(TG_GROUPED_DX, dY, W, ldy, ldw, w_stride, ends, dX, N, K, ldk)
     if need_w:
         dW = W.new_empty(W.shape)
-        _grouped_call(TG_GROUPED_DW, dY, X, ldy, ldx, 0, ends, dW, N, K, max(K, 1), N * max(K, 1))
+        _grouped_call(TG_GROUPED_DW, dY, X, ldy, ldx, 0, ends, dW, N, K, ldk, N * ldk)
     return dX, dW
 
 
@@ -331,7 +344,7 @@ def _grouped_function():
             _refuse("grouped_linear (backward)", dY)
             gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
             need = ctx.needs_input_grad
-            return (*gradients(X, W, ends, _rows(dY), ctx.strides, need[0], need[1]), None, None)
+            return (*gradients(X, W, ends, dY, ctx.strides, need[0], need[1]), None, None)
 
     return GroupedLinear
 
@@ -392,10 +405,15 @@ def _embedding_names():
     return {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 
 
+@functools.lru_cache(maxsize=8)
+def _embedding_entry(dtype, backward):
+    return getattr(_lib(), ("tg_embedding_bwd_" if backward else "tg_embedding_") + _embedding_names()[dtype])
+
+
 def _embedding_forward(tokens, W, ldw, scale):
     V, K = W.shape
     Y = W.new_empty((*tokens.shape, K))
-    _call(W.get_device(), getattr(_lib(), "tg_embedding_" + _embedding_names()[W.dtype]),
+    _call(W.get_device(), _embedding_entry(W.dtype, False),
           (tokens.data_ptr(), W.data_ptr(), Y.data_ptr(), tokens.numel(), V, K, ldw, max(K, 1), scale), "embedding")
     return Y
 
@@ -407,13 +425,16 @@ def _embedding_size(M, V, K):
 
 def _embedding_backward(tokens, dY, V, scale, padding):
     M, K = tokens.numel(), dY.shape[-1]
-    dY = _rows(dY.reshape(M, K))
+    lddy = K
+    if not dY.is_contiguous():
+        dY = _rows(dY.reshape(M, K))
+        lddy = _row_stride(dY, "dY", K)
     dW = dY.new_empty((V, K))
     size = _embedding_size(M, V, K)
     ws = _bytes(dY, size)
-    _call(dY.get_device(), getattr(_lib(), "tg_embedding_bwd_" + _embedding_names()[dY.dtype]),
-          (tokens.data_ptr(), dY.data_ptr(), dW.data_ptr(), M, V, K, _row_stride(dY, "dY", K), max(K, 1), scale, padding,
-           ws.data_ptr(), size), "embedding (backward)")
+    _call(dY.get_device(), _embedding_entry(dY.dtype, True),
+          (tokens.data_ptr(), dY.data_ptr(), dW.data_ptr(), M, V, K, lddy, K, scale, padding, ws.data_ptr(), size),
+          "embedding (backward)")
     return dW
 
 
