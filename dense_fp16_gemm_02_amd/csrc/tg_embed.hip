@@ -759,7 +759,7 @@ int gradient(const int64_t *tokens, const void *dY, void *dW, int64_t M, int64_t
     w.carried = reinterpret_cast<int2 *>(base + p.carried);
     w.head = reinterpret_cast<float *>(base + p.head), w.tail = reinterpret_cast<float *>(base + p.tail);
     ok = ok && launch(embedding_walk_kernel<E>, cdiv((int64_t)p.pieces * w.segments, WALK_WAVES), WALK_THREADS, stream, w);
-    if (M > 1)
+    if (M > 0)  // a single token, too, may lie in the piece before its row's
         ok = ok && launch(embedding_join_kernel<E>, cdiv(p.pieces, JOIN) * w.segments, WALK_THREADS, stream, w);
     return ok ? TG_OK : TG_ERR_LAUNCH;
 }

@@ -233,3 +233,36 @@ def test_graph_replays_read_the_tokens_anew(M):
             torch.cuda.synchronize()
             want = step()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), kind
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [1, 40, 600])
+def test_one_and_two_tokens_at_every_row(dtype, K):
+    """A piece of the walk may end between a token and its row, at any number of tokens: with one
+    token t of V rows the row is item t + 1 of the two lists, and pieces hold 32 items."""
+    for V in (1, 31, 32, 33, 64, 100):
+        gen = torch.Generator().manual_seed(V + K)
+        dY = torch.randint(-8, 9, (2, K), generator=gen).to(dtype).cuda()
+        entry = {torch.float32: tg.tg_embedding_bwd_f32, torch.float16: tg.tg_embedding_bwd_f16,
+                 torch.bfloat16: tg.tg_embedding_bwd_bf16}[dtype]
+        for first in range(V):
+            for tokens in ((first,), (first, first), (first, V - 1 - first)):
+                at = torch.tensor(tokens, device="cuda")
+                M = len(tokens)
+                dW = torch.full((V, K), math.nan, dtype=dtype, device="cuda")
+                n = tg.tg_embedding_bwd_workspace_bytes(M, V, K)
+                ws = torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+                assert entry(at, dY, dW, M, V, K, K, K, 1.0, -1, ws, n, torch.cuda.current_stream()) == tg.TG_OK
+                want = torch.zeros(V, K, dtype=torch.float64, device="cuda").index_add(0, at, dY[:M].double())
+                assert torch.equal(dW.double(), want), (V, tokens)  # sums of small whole numbers
+
+
+@pytest.mark.parametrize("V,tokens", [(100, (31, 63, 95, 30, 32, 99)), (600011, (63, 127, 600010, 62, 64, 524287))])
+def test_one_token_of_a_table(V, tokens):
+    """Through autograd, with pieces of 32 items and of 64."""
+    for t in tokens:
+        W = torch.zeros(V, 4, device="cuda", requires_grad=True)
+        dY = torch.tensor([[1.0, -2.0, 3.0, 4.0]], device="cuda")
+        torch.full((V, 4), math.nan, device="cuda")  # what the gradient's memory held before
+        dW, = torch.autograd.grad(tg.embedding(torch.tensor([t], device="cuda"), W), W, dY)
+        assert torch.equal(dW[t], dY[0]) and int((dW != 0).sum()) == 4, t
