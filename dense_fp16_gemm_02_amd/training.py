@@ -272,6 +272,26 @@ def _bytes(like, size):
     return like.new_empty((size,), dtype=_uint8())
 
 
+def _grouped_strides(X, W, ends, dev):
+    """Row strides of X and W and the expert stride of W, of operands that are checked: all on
+    the GPU ``dev`` (None: X is on none)."""
+    import torch
+
+    if X.dtype != W.dtype or X.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("X and W must both be float16 or both bfloat16")
+    if ends.dtype != torch.int64:
+        raise TypeError("ends must be int64")
+    if not X.device == W.device == ends.device == dev:
+        raise ValueError("X, W and ends must be GPU tensors on the same device")
+    if X.dim() != 2 or W.dim() != 3 or ends.dim() != 1:
+        raise ValueError("X must be 2-D, W 3-D and ends 1-D")
+    if X.shape[1] != W.shape[2]:
+        raise ValueError(f"K mismatch: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
+    if ends.shape[0] != W.shape[0]:
+        raise ValueError(f"{ends.shape[0]} ends for {W.shape[0]} experts")
+    return (_row_stride(X, "X", X.shape[1]), *_weight_strides(W))
+
+
 def _weight_strides(W):
     """Row and expert strides of the weights; experts may share memory, rows may not."""
     E, N, K = W.shape
@@ -315,6 +335,20 @@ def _rows(t):
     return t
 
 
+def _grouped_saved(X, W, ends, dY):
+    """What the forward pass saved, and its strides: hooks on saved tensors (offloading) may
+    bring them back in other memory than they were in."""
+    if X.dim() == 2:
+        X = _rows(X)
+    if W.dim() == 3 and ((W.shape[2] > 1 and W.stride(2) != 1) or (W.shape[1] > 1 and W.stride(1) < W.shape[2])):
+        W = W.contiguous()
+    ends = ends.contiguous()
+    strides = _grouped_strides(X, W, ends, dY.device)
+    if dY.dtype != X.dtype or dY.shape != (X.shape[0], W.shape[1]):
+        raise ValueError("X or W comes back from its hook as another tensor than was saved")
+    return X, W, ends, strides
+
+
 @functools.lru_cache(maxsize=None)
 def _grouped_function():
     import torch
@@ -335,16 +369,15 @@ def _grouped_function():
         @staticmethod
         def forward(ctx, X, W, ends, strides):
             ctx.save_for_backward(X, W, ends)
-            ctx.strides = strides
             return _grouped_forward(X, W, ends, strides)
 
         @staticmethod
         def backward(ctx, dY):
-            X, W, ends = ctx.saved_tensors
+            X, W, ends, strides = _grouped_saved(*ctx.saved_tensors, dY)
             _refuse("grouped_linear (backward)", dY)
             gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
             need = ctx.needs_input_grad
-            return (*gradients(X, W, ends, dY, ctx.strides, need[0], need[1]), None, None)
+            return (*gradients(X, W, ends, dY, strides, need[0], need[1]), None, None)
 
     return GroupedLinear
 
@@ -378,19 +411,7 @@ def grouped_linear(X, W, ends):
 
     if torch.compiler.is_dynamo_compiling():  # the call stays between the compiled parts
         return torch.compiler.disable(grouped_linear)(X, W, ends)
-    if X.dtype != W.dtype or X.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("X and W must both be float16 or both bfloat16")
-    if ends.dtype != torch.int64:
-        raise TypeError("ends must be int64")
-    if not X.is_cuda or W.device != X.device or ends.device != X.device:
-        raise ValueError("X, W and ends must be GPU tensors on the same device")
-    if X.dim() != 2 or W.dim() != 3 or ends.dim() != 1:
-        raise ValueError("X must be 2-D, W 3-D and ends 1-D")
-    if X.shape[1] != W.shape[2]:
-        raise ValueError(f"K mismatch: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
-    if ends.shape[0] != W.shape[0]:
-        raise ValueError(f"{ends.shape[0]} ends for {W.shape[0]} experts")
-    strides = (_row_stride(X, "X", X.shape[1]), *_weight_strides(W))
+    strides = _grouped_strides(X, W, ends, X.device if X.is_cuda else None)
     _refuse("grouped_linear", X, W)
     ends = ends.contiguous()
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
@@ -463,7 +484,9 @@ def _embedding_function():
 
         @staticmethod
         def backward(ctx, dY):
-            tokens, = ctx.saved_tensors
+            tokens = ctx.saved_tensors[0].contiguous()  # a hook may have brought them back in other memory
+            if tokens.dtype != torch.int64 or tokens.shape != dY.shape[:-1] or tokens.device != dY.device:
+                raise ValueError("tokens come back from their hook as another tensor than was saved")
             _refuse("embedding (backward)", dY)
             gradient = Gradient.apply if torch.is_grad_enabled() else _embedding_backward
             return None, gradient(tokens, dY, *ctx.how), None, None, None

@@ -116,3 +116,34 @@ def test_a_table_that_is_the_projection_too():
     loss = tg.linear_cross_entropy(tg.embedding(tokens, looked), projected, target)
     a, b = torch.autograd.grad(loss, (looked, projected))
     assert torch.equal(both, a + b)
+
+
+@pytest.mark.parametrize("pin", [False, True])
+@pytest.mark.parametrize("layout", ["contiguous", "window of X", "window of W", "experts inside", "shared weight"])
+def test_saved_tensors_that_were_offloaded(layout, pin):
+    """torch.autograd.graph.save_on_cpu brings operands back in rows without what lay between them."""
+    T, W, tokens, ends, dY = problem(8)
+    E, N, K = W.shape
+    X = tg.embedding(tokens, T).detach()
+    W = W.detach()
+    if layout == "window of X":
+        wide = torch.full((X.shape[0], 3 * K), float("nan"), dtype=X.dtype, device="cuda")
+        wide[:, K:2 * K] = X
+        X = wide[:, K:2 * K]
+    elif layout == "window of W":
+        deep = torch.full((E, N + 5, K + 8), float("nan"), dtype=W.dtype, device="cuda")
+        deep[:, 2:2 + N, :K] = W
+        W = deep[:, 2:2 + N, :K]
+    elif layout == "experts inside":
+        W = W.permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    elif layout == "shared weight":
+        W = W[:1].expand(E, N, K)
+    X.requires_grad_(), W.requires_grad_()
+    Y = tg.grouped_linear(X, W, ends)
+    want = (Y.detach(), *torch.autograd.grad(Y, (X, W), dY))
+    with torch.autograd.graph.save_on_cpu(pin_memory=pin):
+        Z = tg.grouped_linear(X, W, ends)
+        rows = tg.embedding(tokens.view(7, 100), T)
+    assert same((Z.detach(), *torch.autograd.grad(Z, (X, W), dY)), want)
+    up = torch.ones_like(rows)
+    assert torch.equal(torch.autograd.grad(rows, T, up)[0], torch.autograd.grad(tg.embedding(tokens.view(7, 100), T), T, up)[0])
