@@ -257,6 +257,25 @@ def _backward(H, W, target, lse, dloss, dlse, need_h, need_w, ignore_index, redu
     return dH, dW
 
 
+def _rows(t):
+    """t with a contiguous last dimension and rows that do not overlap."""
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        return t.contiguous()
+    return t
+
+
+def _xent_saved(H, W, target, lse, h_shape, w_shape, dtype):
+    """What the forward pass saved: hooks on saved tensors (offloading) may bring it back in
+    other memory than it was in."""
+    import torch
+
+    if (H.shape, W.shape, H.dtype, W.dtype) != (h_shape, w_shape, dtype, dtype) or \
+            (target.dtype, lse.dtype) != (torch.int64, torch.float32) or \
+            not target.shape == lse.shape == h_shape[:1] or not H.device == W.device == target.device == lse.device:
+        raise ValueError("a saved operand comes back from its hook as another tensor than was saved")
+    return _rows(H), _rows(W), target.contiguous(), lse.contiguous()
+
+
 @functools.lru_cache(maxsize=None)
 def _xent_function():
     import torch
@@ -279,14 +298,16 @@ def _xent_function():
             loss, lse = _forward(H, W, target, ignore_index, reduction, True)
             ctx.save_for_backward(H, W, target, lse)
             ctx.ignore_index, ctx.reduction = ignore_index, reduction
+            ctx.operands = H.shape, W.shape, H.dtype
             ctx.set_materialize_grads(False)
             return loss, lse
 
         @staticmethod
         def backward(ctx, dloss, dlse):
-            H, W, target, lse = ctx.saved_tensors
+            saved = ctx.saved_tensors
             if dloss is None and dlse is None:
                 return None, None, None, None, None
+            H, W, target, lse = _xent_saved(*saved, *ctx.operands)
             _refuse_modes("linear_cross_entropy (backward)", dloss, dlse)
             if dloss is None:
                 dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, device=H.device)

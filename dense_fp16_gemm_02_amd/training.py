@@ -19,7 +19,7 @@ import ctypes
 import functools
 import math
 
-from .projection import _lib, _p, _pkg, _refuse_modes, _row_stride, _s
+from .projection import _lib, _p, _pkg, _refuse_modes, _row_stride, _rows, _s
 
 TG_GROUPED_Y = 0  # include/tg_grouped.h
 TG_GROUPED_DX = 1
@@ -326,13 +326,6 @@ def _grouped_backward(X, W, ends, dY, strides, need_x, need_w):
         dW = W.new_empty(W.shape)
         _grouped_call(TG_GROUPED_DW, dY, X, ldy, ldx, 0, ends, dW, N, K, ldk, N * ldk)
     return dX, dW
-
-
-def _rows(t):
-    """t with a contiguous last dimension and rows that do not overlap."""
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        return t.contiguous()
-    return t
 
 
 def _grouped_saved(X, W, ends, dY):

@@ -67,3 +67,17 @@ def test_first_derivatives_under_create_graph_and_no_second_ones():
     assert torch.equal(tg.newton_schulz(W.detach(), out=out), tg.newton_schulz(W.detach()))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         held.backward()
+
+
+@pytest.mark.parametrize("pin", [False, True])
+def test_saved_tensors_that_were_offloaded(pin):
+    """torch.autograd.graph.save_on_cpu brings a window back without what lay between its rows."""
+    H, W, t = operands()
+    wide = torch.full((60, 400), float("nan"), dtype=H.dtype, device="cuda")
+    wide[:, 136:272] = H
+    h, w, spread = wide[:, 136:272].requires_grad_(), W.requires_grad_(), torch.zeros(60, 2, dtype=t.dtype, device="cuda")
+    spread[:, 1] = t
+    want = torch.autograd.grad(tg.linear_cross_entropy(h, w, t), (h, w))
+    with torch.autograd.graph.save_on_cpu(pin_memory=pin):
+        loss = tg.linear_cross_entropy(h, w, spread[:, 1])
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(loss, (h, w)), want))
