@@ -35,6 +35,7 @@ static_assert(MOST / CHUNK * THREADS < (int64_t)1 << 32, "threads of a launch");
 constexpr float TOP = 448.0f;    // E4M3's largest value
 constexpr float LEAST = 0x1p-9f; // its smallest above zero
 constexpr float FLUSH = 0x1p-110f;
+constexpr float ROOT_LEAST = 0x1p-74f;  // of a root: rounded to E4M3 and squared, still above zero in fp32
 
 // What depends on the step alone, rounded once from 64 bits.
 struct Factors {
@@ -140,12 +141,17 @@ __device__ inline Raw<uint8_t> encode(const float (&x)[PER_LANE], float &scale)
     const bool held = !(most < FLUSH);
     const float per = held ? 1.0f / most * TOP : 0.0f;
     scale = held ? most * (1.0f / TOP) : 0.0f;
+    // A root above zero is held as one whose square is above zero, so that v never reads as
+    // zero where it is not: at least as the smallest value, and, in blocks whose largest is
+    // below 2^-56, as 2^-74: an E4M3 value above 2^-9 is rounded down by less than a third, and
+    // the square of 2/3·2^-74 is 0.9 of fp32's smallest number, to which it is rounded.
+    const float least = ROOT ? fminf(fmaxf(ROOT_LEAST * per, LEAST), TOP) : 0.0f;
     float q[PER_LANE];
 #pragma unroll
     for (int e = 0; e < PER_LANE; ++e) {
         q[e] = fminf(fmaxf(x[e] * per, -TOP), TOP);
         if (ROOT && q[e] > 0.0f)
-            q[e] = fmaxf(q[e], LEAST);
+            q[e] = fmaxf(q[e], least);
     }
     int w = 0;
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -23,8 +23,9 @@
  * held, the same way, whose exponents span half of v's.  A rounding is at most
  * 2^-4 of the value (and 2^-10 of the unit below 2^-6 of it); the step itself takes
  * m and √v as they are before they are rounded.  Three rules keep the division safe:
- * a root above zero is held as at least the smallest value above zero (2^-9 units),
- * so that v never reads as zero where it is not; a block whose largest magnitude
+ * a root above zero is held as at least the smallest value above zero (2^-9 units)
+ * and 2^-74 (the block's largest, where that is below), whose square is a number of
+ * fp32, so that v never reads as zero where it is not; a block whose largest magnitude
  * is below 2^-110 is held as zeros; and a NaN or an infinity in a block makes
  * that block's moments not finite (in 32 bits only the element's).  A moment
  * that moves by less than half a step of its format relative to its block's largest

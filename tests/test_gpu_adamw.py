@@ -321,3 +321,21 @@ def test_an_eps_below_the_normal_numbers_counts_as_zero():
         p, g, m, v = (torch.full((300,), x, device="cuda") for x in (2.0, 0.0, 0.0, 0.0))
         tg.adamw([p], [g], [m], [v], 1, lr=0.5, eps=eps, weight_decay=0.0)
         assert bool(p.isnan().all()) if nan else bool((p == 2).all())
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-8])
+def test_roots_that_are_held_in_8_bits_square_to_more_than_zero(eps):
+    """Blocks whose largest root is 2^-74 to 2^-50, the others the roots of the first few fp32 numbers; then
+    steps without gradients, in which with an eps of zero no moment may be divided by zero."""
+    blocks = 1200
+    largest = 2.0 ** torch.linspace(-74, -50, blocks, dtype=torch.float64)  # 2% apart
+    v = (torch.arange(256) % 5 + 1.0).double().repeat(blocks, 1) * 2.0 ** -149
+    v[:, 0] = largest.square()
+    g = (v / 1e-3).sqrt().float().flatten().cuda()
+    p, zero = torch.zeros_like(g), torch.zeros_like(g)
+    state = [[t] for t in tg.adamw_8bit_state(p)]
+    for step in range(1, 7):
+        tg.adamw_8bit([p], [g if step == 1 else zero], *state, step, lr=1e-3, betas=(0.9, 0.999), eps=eps, weight_decay=0.0)
+        r = oracle.decode(state[2][0], state[3][0])
+        assert (r * r > 0).all(), (step, int((r * r == 0).sum()))
+        assert torch.isfinite(p).all(), step
