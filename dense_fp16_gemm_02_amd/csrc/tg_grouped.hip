@@ -524,10 +524,12 @@ struct WeightArgs {
     float *sums;  // PARTS
     int parts;
 };
+constexpr int DW_AHEAD = 3;  // K-tiles that are asked for ahead, at most
 template <typename E, typename T, bool PARTS>
 __global__ __launch_bounds__(T::THREADS) PT_WAVES_PER_SIMD(waves_of<T>()) void grouped_weight_kernel(
     WeightArgs a)
 {
+    static_assert(T::S <= DW_AHEAD, "the limit on rows counts them");
     __shared__ __attribute__((aligned(1024))) E smem[T::LDS_ELEMS];
     const int per = a.tiles_m * a.tiles_n, total = a.E * per;
     const int z = PARTS ? (int)blockIdx.x / total : 0;
@@ -816,6 +818,12 @@ Plan make_plan(const Call &q)
 // 16384 rows 163 -> 115; Y of 16384×14336 1522 -> 1505).
 constexpr int64_t NT_BYTES = (int64_t)64 << 20;
 constexpr int64_t LIM = (int64_t)1 << 31, LIM_STRIDE = (int64_t)1 << 42;
+// Rows of dW's sums: their K-tiles, and the DW_AHEAD that are asked for past the last one,
+// begin at rows of 31 bits.  (Y and dX sum over N and K, and have fewer rows: tiles of up to 256
+// rows, fewer than MAX_GRID.)
+constexpr int64_t LIM_ROWS = LIM - 256;
+static_assert((cdiv(LIM_ROWS - 1, BK) + DW_AHEAD) * BK < LIM, "rows of 31 bits");
+static_assert(MAX_GRID * 256 <= LIM, "rows of 31 bits");
 // Whether anything is multiplied: otherwise the result is zeros, or nothing.
 bool multiplies(const Call &q) { return q.M > 0 && q.E > 0 && q.N > 0 && q.K > 0; }
 int validate(const Call &q)
@@ -825,8 +833,8 @@ int validate(const Call &q)
     const bool dw = q.product == TG_GROUPED_DW;
     if (q.lda < (q.product == TG_GROUPED_Y ? q.K : q.N) || q.ldb < q.K || (!dw && q.E > 1 && q.w_stride < 0))
         return TG_ERR_INVALID_ARG;
-    if (q.M >= LIM || q.E >= 1 << 16 || q.N >= MAX_DMA_LD || q.K >= MAX_DMA_LD || q.lda >= LIM || q.ldb >= LIM ||
-        (!dw && q.E > 1 && q.w_stride >= LIM_STRIDE))
+    if (q.M >= (dw ? LIM_ROWS : LIM) || q.E >= 1 << 16 || q.N >= MAX_DMA_LD || q.K >= MAX_DMA_LD || q.lda >= LIM ||
+        q.ldb >= LIM || (!dw && q.E > 1 && q.w_stride >= LIM_STRIDE))
         return TG_ERR_TOO_LARGE;
     if (!multiplies(q))
         return TG_OK;

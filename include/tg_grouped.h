@@ -90,7 +90,8 @@ int tg_grouped_dx_bf16(const void *dY, const void *W, const int64_t *ends, void 
  * tg_grouped_dw_f16, tg_grouped_dw_bf16 — enqueue dW (row n of expert e at
  * dW + e·dw_stride + n·lddw, dw_stride >= (N − 1)·lddw + K for E > 1), with a
  * workspace for (TG_GROUPED_DW, dY, X, ..., w_stride not looked at).  E, N or K == 0: nothing
- * happens.  M == 0: dW is set to 0.  Status codes as above.
+ * happens.  M == 0: dW is set to 0.  Status codes as above, TG_ERR_TOO_LARGE also for
+ * M >= 2^31 − 256.
  */
 int tg_grouped_dw_f16(const void *dY, const void *X, const int64_t *ends, void *dW, int64_t M, int64_t E, int64_t N,
                       int64_t K, int64_t lddy, int64_t ldx, int64_t lddw, int64_t dw_stride, void *workspace,

@@ -320,3 +320,21 @@ def test_c99_caller(tmp_path):
                     str(src), "-o", str(exe), tg.lib_path(), f"-Wl,-rpath,{lib}"], check=True)
     p = subprocess.run([str(exe)], capture_output=True, text=True)
     assert p.returncode == 0, p.stdout
+
+
+# ------------------------------------------------- sums as long as 32 bits hold
+def test_grouped_dw_sums_end_before_32_bits_do():
+    """A sum over M rows counts K-tiles of 64 rows, up to four past the last, in 32 bits: the rows that
+    these end at have to be numbers of 32 bits.  (Y and dX have fewer rows: their tiles are limited.)"""
+    most = LIM - 257
+    tiles = (most + 63) // 64
+    assert (tiles + 3) * 64 < LIM <= ((most + 64 + 63) // 64 + 3) * 64
+    for M, fits in ((most, True), (most + 1, False), (LIM - 64, False), (LIM - 1, False)):
+        for E, N, K in ((1, 8, 8), (3, 64, 128)):
+            sizes = (tg.TG_GROUPED_DW, A, A, M, E, N, K, N, K, 0)
+            assert (tg.tg_grouped_workspace_bytes(*sizes) >= 0) == fits, (M, E)
+            assert tg.tg_grouped_plan(*sizes)[0] == (tg.TG_OK if fits else tg.TG_ERR_TOO_LARGE)
+            if not fits:
+                assert dw(M=M, E=E, N=N, K=K, lddy=N, ldx=K, lddw=K, dws=N * K) == tg.TG_ERR_TOO_LARGE
+    for product in (tg.TG_GROUPED_Y, tg.TG_GROUPED_DX):
+        assert tg.tg_grouped_workspace_bytes(product, A, A, LIM - 511, 1, 8, 8, 8, 8, 64) == -1
