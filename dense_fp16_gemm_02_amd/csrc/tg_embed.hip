@@ -654,11 +654,12 @@ struct Plan {
     int piece, pieces;       // of the walk
     int64_t key, at, key2, at2, count, carried, head, tail, bytes;  // offsets in the workspace
 };
+// (M + V: the walk counts tokens 64 at a time in 32 bits, up to one step past the last)
 int validate(int64_t M, int64_t V, int64_t K)
 {
     if (M < 0 || V < 0 || K < 0)
         return TG_ERR_INVALID_ARG;
-    return M >= LIMIT || V >= LIMIT || K >= LIMIT || M + V >= LIMIT || (M + V) * K >= MOST ? TG_ERR_TOO_LARGE : TG_OK;
+    return M >= LIMIT || V >= LIMIT || K >= LIMIT || M + V >= LIMIT - 64 || (M + V) * K >= MOST ? TG_ERR_TOO_LARGE : TG_OK;
 }
 // Pieces of 32 items where there are few, of 64 otherwise (with gradient: 333 tokens
 // on 50001×1000 fp32 70 us with 32, 80 with 64; 65536 on 32000×2048 fp16 238 and 219,

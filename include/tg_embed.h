@@ -62,8 +62,8 @@ int64_t tg_embedding_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K);
  *
  * Only kernels are launched.  V == 0 or K == 0: nothing happens; M == 0: dW is set
  * to 0.  Status codes as above, TG_ERR_INVALID_ARG also for a workspace that is
- * NULL, misaligned or too small, TG_ERR_TOO_LARGE also for M + V >= 2^31 or
- * (M + V)·K >= 2^40.
+ * NULL, misaligned or too small, TG_ERR_TOO_LARGE also for M + V >= 2^31 − 64
+ * or (M + V)·K >= 2^40.
  */
 int tg_embedding_bwd_f32(const int64_t *tokens, const void *dY, void *dW, int64_t M, int64_t V, int64_t K,
                          int64_t lddy, int64_t lddw, float scale, int64_t padding, void *workspace,

@@ -338,3 +338,12 @@ def test_grouped_dw_sums_end_before_32_bits_do():
                 assert dw(M=M, E=E, N=N, K=K, lddy=N, ldx=K, lddw=K, dws=N * K) == tg.TG_ERR_TOO_LARGE
     for product in (tg.TG_GROUPED_Y, tg.TG_GROUPED_DX):
         assert tg.tg_grouped_workspace_bytes(product, A, A, LIM - 511, 1, 8, 8, 8, 8, 64) == -1
+
+
+def test_embedding_gradients_end_before_32_bits_do():
+    """The walk takes sorted tokens 64 at a time, counted in 32 bits up to one step past its last."""
+    for M, V, fits in ((LIM - 66, 1, True), (1, LIM - 66, True), (1 << 30, (1 << 30) - 65, True), (LIM - 65, 1, False),
+                       (LIM - 2, 1, False), (1, LIM - 65, False), (1 << 30, (1 << 30) - 1, False)):
+        assert (tg.tg_embedding_bwd_workspace_bytes(M, V, 1) > 0) == fits, (M, V)
+        if not fits:
+            assert back(M=M, V=V, K=1, lddy=1, lddw=1) == tg.TG_ERR_TOO_LARGE
