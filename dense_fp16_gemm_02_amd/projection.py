@@ -310,7 +310,8 @@ def _xent_function():
             H, W, target, lse = _xent_saved(*saved, *ctx.operands)
             _refuse_modes("linear_cross_entropy (backward)", dloss, dlse)
             if dloss is None:
-                dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, device=H.device)
+                dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, dtype=torch.float32,
+                                    device=H.device)
             dloss = dloss.contiguous()
             dlse = None if dlse is None else dlse.contiguous()
             gradients = Gradients.apply if torch.is_grad_enabled() else _backward

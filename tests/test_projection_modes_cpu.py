@@ -269,3 +269,26 @@ def test_in_place_is_not_compared_row_by_row(update, monkeypatch):
     tg.newton_schulz(G.half(), out=None)
     half = G.half()
     tg.newton_schulz(half, out=half.view(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64, torch.bfloat16])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+def test_a_missing_gradient_of_the_loss_is_fp32_zeros(card, monkeypatch, dtype, reduction):
+    """Where only lse is differentiated, whatever type torch makes by default."""
+    H, W, t = card
+    seen = []
+
+    def keep(H, W, target, lse, dloss, dlse, *how):
+        seen.append((dloss.dtype, dloss.numel(), bool(dloss.any()), dlse.dtype))
+        return torch.zeros(H.shape, dtype=H.dtype), torch.zeros(W.shape, dtype=W.dtype)
+
+    monkeypatch.setattr(pr, "_backward", keep)
+    h, w = H.clone().requires_grad_(), W.clone().requires_grad_()
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(dtype)
+    try:
+        loss, lse = tg.linear_cross_entropy(h, w, t, reduction=reduction, return_lse=True)
+        torch.autograd.grad(lse, (h, w), torch.ones_like(lse))
+    finally:
+        torch.set_default_dtype(before)
+    assert seen == [(torch.float32, 6 if reduction == "none" else 1, False, torch.float32)]
