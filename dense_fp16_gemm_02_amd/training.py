@@ -328,9 +328,15 @@ def _grouped_backward(X, W, ends, dY, strides, need_x, need_w):
     return dX, dW
 
 
+def _layout(X, W, ends):
+    """All that a call of the library takes from its operands besides their addresses."""
+    return (X.shape, X.stride(), X.dtype, X.get_device(), W.shape, W.stride(), W.dtype, W.get_device(), ends.shape,
+            ends.stride(), ends.dtype, ends.get_device())
+
+
 def _grouped_saved(X, W, ends, dY):
-    """What the forward pass saved, and its strides: hooks on saved tensors (offloading) may
-    bring them back in other memory than they were in."""
+    """What the forward pass saved, and its strides, where hooks on saved tensors (offloading)
+    brought it back in other memory than it was in."""
     if X.dim() == 2:
         X = _rows(X)
     if W.dim() == 3 and ((W.shape[2] > 1 and W.stride(2) != 1) or (W.shape[1] > 1 and W.stride(1) < W.shape[2])):
@@ -362,11 +368,16 @@ def _grouped_function():
         @staticmethod
         def forward(ctx, X, W, ends, strides):
             ctx.save_for_backward(X, W, ends)
+            ctx.layout, ctx.strides = _layout(X, W, ends), strides
             return _grouped_forward(X, W, ends, strides)
 
         @staticmethod
         def backward(ctx, dY):
-            X, W, ends, strides = _grouped_saved(*ctx.saved_tensors, dY)
+            X, W, ends = ctx.saved_tensors
+            strides = ctx.strides
+            # (one comparison: every question here costs twice, on autograd's own thread)
+            if _layout(X, W, ends) != ctx.layout:
+                X, W, ends, strides = _grouped_saved(X, W, ends, dY)
             _refuse("grouped_linear (backward)", dY)
             gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
             need = ctx.needs_input_grad
@@ -478,7 +489,8 @@ def _embedding_function():
         @staticmethod
         def backward(ctx, dY):
             tokens = ctx.saved_tensors[0].contiguous()  # a hook may have brought them back in other memory
-            if tokens.dtype != torch.int64 or tokens.shape != dY.shape[:-1] or tokens.device != dY.device:
+            if tokens.dtype != torch.int64 or tokens.shape != dY.shape[:-1] or \
+                    tokens.get_device() != dY.get_device():
                 raise ValueError("tokens come back from their hook as another tensor than was saved")
             _refuse("embedding (backward)", dY)
             gradient = Gradient.apply if torch.is_grad_enabled() else _embedding_backward
