@@ -76,7 +76,10 @@ struct LookArgs {
     int segments;  // of 64 lanes · LOOK_STEPS to a row
     float scale;
 };
-// A wave takes LOOK_STEPS·64 lanes of one row.  Bound by memory.  NT: Y is too large
+// A wave takes LOOK_STEPS·64 lanes of one row.  Bound by memory where a row fills them; of
+// narrower rows some 3.4 a ns are looked up whatever their width (2^20 of them from 32000
+// rows: 64, 128 and 256 fp32 314, 314 and 306 us, where a copy of the bytes would take 56, 110
+// and 218; as many bf16 377-379 us).  NT: Y is too large
 // to be kept for its reader anyway; without it Y displaces W from the last-level cache
 // (65536 tokens of 32000×2048 fp16, 268 MB of Y: 64 us, 86 without; 8192 of
 // 131072×4096 bf16, 64 MiB: 23.5 and 24.9).
@@ -443,7 +446,8 @@ __device__ inline int walk_tokens(const uint32_t *key, int64_t M, int64_t V, int
     return uniform((int)lo);
 }
 // Bound by memory: dW of 131072×4096 bf16 from 8192 rows 225 us (5.1 TB/s), of 32000×2048
-// fp16 from 65536 rows 80 us (4.8 TB/s).
+// fp16 from 65536 rows 80 us (4.8 TB/s).  A piece of a row narrower than a wave's 64·VEC
+// elements leaves lanes idle.
 template <typename E>
 __global__ __launch_bounds__(WALK_THREADS) void embedding_walk_kernel(WalkArgs a)
 {

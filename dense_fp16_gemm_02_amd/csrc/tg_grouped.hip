@@ -624,7 +624,8 @@ const char *const CLASS_NAME[] = {"256x256", "192x192", "128x128", "64x64", "64x
 // fitted to the times of every class for 760 problems on one MI355X (1 to 16384 rows, 1
 // to 128 experts, N and K from 64 to 14336, weights not in the caches): what is
 // chosen takes 2.5% (Y), 1.5% (dX) and 1.5% (dW) more than the best of them in the geometric
-// mean, at most 1.5 times as much.
+// mean, at most 1.5 times as much.  A kernel that changes leaves its numbers stale: they choose
+// a class, and no result depends on them beyond the order of its sums.
 struct RowsModel {
     TileClass c[CLASSES];
     double more, tail;    // tile rows: how many more than of even shares, and of a share's last tile

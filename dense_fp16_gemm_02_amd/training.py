@@ -508,7 +508,8 @@ def embedding(tokens, W, scale: float = 1.0, padding_idx: int | None = None):
     differentiated with respect to W, once (under create_graph, what depends on the
     gradient raises RuntimeError): dW[v] = scale·Σ dY over the tokens v, summed in
     fp32 in the order of the tokens and rounded once, so that it is the same at every
-    call.  Row ``padding_idx`` gets no gradient (its row of Y is read as any other).
+    call.  Row ``padding_idx``, from 0 to V - 1, gets no gradient (its row of Y is read as
+    any other).
     A token outside [0, V) makes its row NaN and adds to no gradient.
 
     It gathers any rows: the tokens' hidden states in the order that ``grouped_linear``
@@ -657,7 +658,8 @@ def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999
     fp32 and zeros before the first step.  ``step`` counts from 1.  ``copies``, where
     given, are fp16 or bf16 tensors of fp32 parameters' sizes that receive them rounded.
     ``grad_scale``, a one-element fp32 tensor on the device, multiplies the gradients
-    (the factor that clips their norm, or a loss scale's inverse).
+    (the factor that clips their norm, or a loss scale's inverse).  An ``eps`` below 2^-126
+    counts as 0, with which an element whose moments are 0 becomes NaN.
 
     ``lr`` and ``step`` may be one-element tensors on the device (fp32 and int64): a
     call captured into a graph reads them anew at each replay.  Nothing is advanced
@@ -696,7 +698,8 @@ def adamw_8bit(params, grads, exp_avgs, exp_avg_scales, roots, root_scales, step
     """``adamw`` with moments held in 8 bits: E4M3 tensors of the parameters' sizes
     with one fp32 scale for each 256 elements, of m and of √v (``adamw_8bit_state``
     makes them).  The step itself uses the moments before they are rounded; a rounding
-    is at most 2^-4 of the value.  include/tg_adamw.h says what is held of small,
+    is at most 2^-4 of the value.  Large updates take a fifth longer with ``lr`` or ``step`` on
+    the device.  include/tg_adamw.h says what is held of small,
     infinite and NaN values.  Everything else is as for ``adamw``."""
     _adamw("adamw_8bit", params, grads, [exp_avgs, roots], [exp_avg_scales, root_scales], step, lr, betas, eps,
            weight_decay, grad_scale, copies)

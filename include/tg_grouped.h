@@ -10,8 +10,8 @@
  *     dX[i] = dY[i]·W[e]
  *     dW[e] = Σ_i dY[i]ᵀ·X[i]     over the rows of expert e, 0 where it has none
  *
- * Rows from ends[E−1] on belong to no expert: they are not read, and their rows of
- * Y and dX are 0.  `ends` lies in device memory and is read there, so that a
+ * Rows from ends[E−1] on belong to no expert: what they hold reaches nothing, and their
+ * rows of Y and dX are 0.  `ends` lies in device memory and is read there, so that a
  * router's counts never pass through the host.  Whatever it holds, nothing outside
  * the arrays is touched: a value counts as at least the one before it, and
  * as 0 to M.
