@@ -264,14 +264,16 @@ def _rows(t):
     return t
 
 
-def _xent_saved(H, W, target, lse, h_shape, w_shape, dtype):
-    """What the forward pass saved: hooks on saved tensors (offloading) may bring it back in
-    other memory than it was in."""
-    import torch
+def _xent_layout(H, W, target, lse):
+    """What a call of the library takes from its operands besides their addresses."""
+    return (H.stride(), W.stride(), target.stride(), lse.stride(), H.shape, W.shape, target.shape, lse.shape, H.dtype,
+            W.dtype, target.dtype, lse.dtype, H.get_device(), W.get_device(), target.get_device(), lse.get_device())
 
-    if (H.shape, W.shape, H.dtype, W.dtype) != (h_shape, w_shape, dtype, dtype) or \
-            (target.dtype, lse.dtype) != (torch.int64, torch.float32) or \
-            not target.shape == lse.shape == h_shape[:1] or not H.device == W.device == target.device == lse.device:
+
+def _xent_saved(H, W, target, lse, layout):
+    """What the forward pass saved, where hooks on saved tensors (offloading) brought it back in
+    other memory than it was in."""
+    if _xent_layout(H, W, target, lse)[4:] != layout[4:]:
         raise ValueError("a saved operand comes back from its hook as another tensor than was saved")
     return _rows(H), _rows(W), target.contiguous(), lse.contiguous()
 
@@ -298,7 +300,7 @@ def _xent_function():
             loss, lse = _forward(H, W, target, ignore_index, reduction, True)
             ctx.save_for_backward(H, W, target, lse)
             ctx.ignore_index, ctx.reduction = ignore_index, reduction
-            ctx.operands = H.shape, W.shape, H.dtype
+            ctx.layout = _xent_layout(H, W, target, lse)
             ctx.set_materialize_grads(False)
             return loss, lse
 
@@ -307,7 +309,9 @@ def _xent_function():
             saved = ctx.saved_tensors
             if dloss is None and dlse is None:
                 return None, None, None, None, None
-            H, W, target, lse = _xent_saved(*saved, *ctx.operands)
+            H, W, target, lse = saved
+            if _xent_layout(H, W, target, lse) != ctx.layout:
+                H, W, target, lse = _xent_saved(H, W, target, lse, ctx.layout)
             _refuse_modes("linear_cross_entropy (backward)", dloss, dlse)
             if dloss is None:
                 dloss = torch.zeros(H.shape[0] if ctx.reduction == TG_XENT_NONE else 1, dtype=torch.float32,

@@ -328,10 +328,10 @@ def _grouped_backward(X, W, ends, dY, strides, need_x, need_w):
     return dX, dW
 
 
-def _layout(X, W, ends):
-    """All that a call of the library takes from its operands besides their addresses."""
-    return (X.shape, X.stride(), X.dtype, X.get_device(), W.shape, W.stride(), W.dtype, W.get_device(), ends.shape,
-            ends.stride(), ends.dtype, ends.get_device())
+def _grouped_layout(X, W, ends):
+    """What a call of the library takes from its operands besides their addresses."""
+    return (X.stride(), W.stride(), ends.stride(), X.shape, W.shape, ends.shape, X.dtype, W.dtype, ends.dtype,
+            X.get_device(), W.get_device(), ends.get_device())
 
 
 def _grouped_saved(X, W, ends, dY):
@@ -368,7 +368,7 @@ def _grouped_function():
         @staticmethod
         def forward(ctx, X, W, ends, strides):
             ctx.save_for_backward(X, W, ends)
-            ctx.layout, ctx.strides = _layout(X, W, ends), strides
+            ctx.layout, ctx.strides = _grouped_layout(X, W, ends), strides
             return _grouped_forward(X, W, ends, strides)
 
         @staticmethod
@@ -376,7 +376,7 @@ def _grouped_function():
             X, W, ends = ctx.saved_tensors
             strides = ctx.strides
             # (one comparison: every question here costs twice, on autograd's own thread)
-            if _layout(X, W, ends) != ctx.layout:
+            if _grouped_layout(X, W, ends) != ctx.layout:
                 X, W, ends, strides = _grouped_saved(X, W, ends, dY)
             _refuse("grouped_linear (backward)", dY)
             gradients = Gradients.apply if torch.is_grad_enabled() else _grouped_backward
